@@ -13,12 +13,19 @@ The C ABI (include/fp8gb.h) is mirrored one to one:
   fp8_grouped_gemm         the same over MoE expert groups
   fp8_group_padded_offsets host helper for the grouped colwise layout
   fp8_sync_status          stream sync + device error word
+  fp8_norm_forward         layer / RMS norm, optionally with an 8-bit
+                           checkpoint of the normalized rows
+  fp8_norm_backward        its backward, from x or from the checkpoint
+  fp8_swiglu_checkpoint    SwiGLU that stores gate|up in 8 bits
+  fp8_swiglu_backward      its backward, from gate|up or from the checkpoint
+  fp8_checkpoint[_restore] any activation to 8 bits and back
 
 `quantize`, `scaled_gemm`, `grouped_gemm` are convenience wrappers that
 allocate the outputs with torch and call the entry points above.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -32,6 +39,8 @@ MOST_RECENT, MAX = 0, 1
 LAYOUT_ROW, LAYOUT_COLT = 1, 2
 SCALE_TENSOR, SCALE_PER_ROW = 0, 1
 GROUPED_M, GROUPED_K, GROUPED_M_BT = 0, 1, 2
+LAYER_NORM, RMS_NORM = 0, 1
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 STATUS = {0: "FP8_OK", 1: "FP8_ERR_INVALID_ARG", 2: "FP8_ERR_UNSUPPORTED", 3: "FP8_ERR_ALIGNMENT",
           4: "FP8_ERR_CUDA", 5: "FP8_ERR_TIMEOUT"}
 
@@ -41,7 +50,9 @@ EXPORTED = ("fp8_quantize", "fp8_update_amax_history", "fp8_scaled_gemm", "fp8_g
             "fp8_group_padded_offsets", "fp8_sync_status", "fp8_selftest_bounded_wait", "fp8_status_string",
             "fp8_last_cuda_error", "fp8_version", "fp8_mx_scale_bytes", "fp8_mx_quantize", "fp8_mx_gemm",
             "fp8_mx_grouped_gemm", "fp8_mx_permute_quantize", "fp8_mx_swiglu_quantize", "fp8_blockwise_quantize",
-            "fp8_quantize_rowwise_resident", "fp8_permute_quantize", "fp8_swiglu_quantize")
+            "fp8_quantize_rowwise_resident", "fp8_permute_quantize", "fp8_swiglu_quantize", "fp8_checkpoint",
+            "fp8_checkpoint_restore", "fp8_swiglu_checkpoint", "fp8_swiglu_backward", "fp8_norm_forward",
+            "fp8_norm_workspace_bytes", "fp8_norm_backward")
 MX_BLOCK = 32
 MX_GROUP_ALIGN = 128
 
@@ -133,6 +144,23 @@ def load_library():
             lib.fp8_mx_swiglu_quantize.argtypes = [P, i64, i64, i64, i32, i32, P, i64, P, P, P, i64, P, P, i32, P]
             lib.fp8_blockwise_quantize.restype = i32
             lib.fp8_blockwise_quantize.argtypes = [P, i64, i64, i64, i32, i32, i32, P, P, P, i64, P, P]
+            f32 = ctypes.c_float
+            lib.fp8_checkpoint.restype = i32
+            lib.fp8_checkpoint.argtypes = [P, i32, i64, i64, i64, i32, i32, P, i64, P, i64, P]
+            lib.fp8_checkpoint_restore.restype = i32
+            lib.fp8_checkpoint_restore.argtypes = [P, i64, P, i64, i32, i64, i64, i32, P, i32, i64, P]
+            lib.fp8_swiglu_checkpoint.restype = i32
+            lib.fp8_swiglu_checkpoint.argtypes = [P, i64, i64, i64, i32, P, i64, P, i64, P, i64, P]
+            lib.fp8_swiglu_backward.restype = i32
+            lib.fp8_swiglu_backward.argtypes = [P, i64, P, i64, P, i64, P, i64, i32, i64, i64, P, i64, P, i64, P]
+            lib.fp8_norm_forward.restype = i32
+            lib.fp8_norm_forward.argtypes = [P, i32, i64, i64, i64, i32, f32, P, P, i32, P, i32, i64, P, P, i32, P,
+                                             i64, P, i64, P]
+            lib.fp8_norm_workspace_bytes.restype = i64
+            lib.fp8_norm_workspace_bytes.argtypes = [i64, i64]
+            lib.fp8_norm_backward.restype = i32
+            lib.fp8_norm_backward.argtypes = [P, i32, i64, P, i64, P, i64, P, i64, i32, i64, i64, i32, P, P, P, i32, P,
+                                              i32, i64, P, P, P, i64, P]
             lib.fp8_mx_gemm.restype = i32
             lib.fp8_mx_gemm.argtypes = [P, i32, i64, P, P, i32, i64, P, i64, i64, i64, P, i64, P]
             lib.fp8_mx_grouped_gemm.restype = i32
@@ -299,6 +327,64 @@ def fp8_mx_grouped_gemm(mode, A, fa, sA, B, fb, sB, group_offsets, G, M_total, N
                                             M_total, N, K, _p(C), ld_T, _stream(stream))
     if check:
         _check(rc, "fp8_mx_grouped_gemm")
+    return rc
+
+
+def fp8_checkpoint(x, dtype, rows, cols, ld_x, parts, fmt, q, ld_q, s, ld_s, stream=None, check=True):
+    rc = load_library().fp8_checkpoint(_p(x), dtype, rows, cols, ld_x, parts, fmt, _p(q), ld_q, _p(s), ld_s,
+                                       _stream(stream))
+    if check:
+        _check(rc, "fp8_checkpoint")
+    return rc
+
+
+def fp8_checkpoint_restore(q, ld_q, s, ld_s, fmt, rows, cols, parts, x, dtype, ld_x, stream=None, check=True):
+    rc = load_library().fp8_checkpoint_restore(_p(q), ld_q, _p(s), ld_s, fmt, rows, cols, parts, _p(x), dtype, ld_x,
+                                               _stream(stream))
+    if check:
+        _check(rc, "fp8_checkpoint_restore")
+    return rc
+
+
+def fp8_swiglu_checkpoint(gate_up, rows, F, ld, fmt, h, ld_h, q, ld_q, s, ld_s, stream=None, check=True):
+    rc = load_library().fp8_swiglu_checkpoint(_p(gate_up), rows, F, ld, fmt, _p(h), ld_h, _p(q), ld_q, _p(s), ld_s,
+                                              _stream(stream))
+    if check:
+        _check(rc, "fp8_swiglu_checkpoint")
+    return rc
+
+
+def fp8_swiglu_backward(dh, ld_dh, gate_up, ld, q, ld_q, s, ld_s, fmt, rows, F, d_gate_up, ld_d, h=None, ld_h=0,
+                        stream=None, check=True):
+    rc = load_library().fp8_swiglu_backward(_p(dh), ld_dh, _p(gate_up), ld, _p(q), ld_q, _p(s), ld_s, fmt, rows, F,
+                                            _p(d_gate_up), ld_d, _p(h), ld_h, _stream(stream))
+    if check:
+        _check(rc, "fp8_swiglu_backward")
+    return rc
+
+
+def fp8_norm_forward(x, x_dtype, ld_x, rows, cols, kind, eps, weight, bias, w_dtype, y, y_dtype, ld_y, mean, rstd,
+                     fmt=0, q=None, ld_q=0, s=None, ld_s=0, stream=None, check=True):
+    rc = load_library().fp8_norm_forward(_p(x), x_dtype, ld_x, rows, cols, kind, eps, _p(weight), _p(bias), w_dtype,
+                                         _p(y), y_dtype, ld_y, _p(mean), _p(rstd), fmt, _p(q), ld_q, _p(s), ld_s,
+                                         _stream(stream))
+    if check:
+        _check(rc, "fp8_norm_forward")
+    return rc
+
+
+def fp8_norm_workspace_bytes(rows: int, cols: int) -> int:
+    return int(load_library().fp8_norm_workspace_bytes(rows, cols))
+
+
+def fp8_norm_backward(dy, y_dtype, ld_dy, x, ld_x, q, ld_q, s, ld_s, fmt, rows, cols, kind, mean, rstd, weight,
+                      w_dtype, dx, x_dtype, ld_dx, dweight, dbias, workspace, workspace_bytes, stream=None,
+                      check=True):
+    rc = load_library().fp8_norm_backward(_p(dy), y_dtype, ld_dy, _p(x), ld_x, _p(q), ld_q, _p(s), ld_s, fmt, rows,
+                                          cols, kind, _p(mean), _p(rstd), _p(weight), w_dtype, _p(dx), x_dtype, ld_dx,
+                                          _p(dweight), _p(dbias), _p(workspace), workspace_bytes, _stream(stream))
+    if check:
+        _check(rc, "fp8_norm_backward")
     return rc
 
 
@@ -561,3 +647,216 @@ def blockwise_quantize(x: torch.Tensor, fmt: int, block_rows: int, layouts: int 
     fp8_blockwise_quantize(x, rows, cols, x.stride(0), fmt, block_rows, layouts, q.q_row, q.s_row, q.q_colT,
                            q.ld_colT, q.s_col, stream)
     return q
+
+
+# --- norms, SwiGLU backward and 8-bit checkpoints -------------------------------
+
+def _require(ok, where: str, detail: str):
+    if not ok:
+        raise Fp8Error(1, where, detail)
+
+
+def _alloc_on(stream):
+    """Context in which torch allocates for `stream`: what is allocated there
+    is reused in that stream's order, so a workspace dropped at return is safe
+    while the launch is still running."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _matrix(t: torch.Tensor, where: str, name: str, rows=None, cols=None, dtype=None) -> int:
+    """Check a CUDA matrix; returns its row stride."""
+    _require(t.is_cuda and t.dim() == 2, where, f"{name} must be a CUDA matrix")
+    _require(t.dtype in DTYPES if dtype is None else t.dtype == dtype, where, f"{name} has type {t.dtype}")
+    n, c = t.shape
+    _require((rows is None or n == rows) and (cols is None or c == cols), where,
+             f"{name} is {n} x {c}, not {rows} x {cols}")
+    _require(c > 0 and (c == 1 or t.stride(1) == 1), where, f"{name} must have consecutive columns")
+    return t.stride(0) if n > 1 else max(c, t.stride(0))
+
+
+def _vector(t, where: str, name: str, n: int, dtype=None):
+    if t is not None:
+        _require(t.is_cuda and t.dim() == 1 and t.numel() == n and t.is_contiguous(), where,
+                 f"{name} must be a contiguous CUDA vector of {n} elements")
+        _require(t.dtype in DTYPES if dtype is None else t.dtype == dtype, where, f"{name} has type {t.dtype}")
+
+
+@dataclass
+class Checkpoint:
+    """An activation of `parts` side-by-side tensors of `cols` columns each,
+    kept in 8 bits (format in include/fp8gb.h): q u8 [rows, parts * W], W =
+    cols rounded up to 32, and one scale byte per 32 columns in s u8
+    [rows, parts * W / 32]."""
+    q: torch.Tensor
+    s: torch.Tensor
+    fmt: int
+    cols: int
+    parts: int = 1
+
+    @property
+    def rows(self) -> int:
+        return self.q.shape[0]
+
+
+def _checkpoint_buffers(rows, cols, parts, dev, fmt) -> Checkpoint:
+    w = (cols + MX_BLOCK - 1) // MX_BLOCK * MX_BLOCK * parts
+    return Checkpoint(torch.empty((rows, w), dtype=torch.uint8, device=dev),
+                      torch.empty((rows, w // MX_BLOCK), dtype=torch.uint8, device=dev), fmt, cols, parts)
+
+
+def _checkpoint_strides(c: Checkpoint, where: str, rows=None, cols=None, parts=None):
+    _require((rows is None or c.rows == rows) and (cols is None or c.cols == cols) and
+             (parts is None or c.parts == parts), where,
+             f"the checkpoint holds {c.rows} x {c.parts} x {c.cols}, not {rows} x {parts} x {cols}")
+    w = (c.cols + MX_BLOCK - 1) // MX_BLOCK * MX_BLOCK * c.parts
+    return (_matrix(c.q, where, "checkpoint codes", c.rows, w, torch.uint8),
+            _matrix(c.s, where, "checkpoint scales", c.rows, w // MX_BLOCK, torch.uint8))
+
+
+def checkpoint(x: torch.Tensor, fmt: int = E4M3FN, parts: int = 1, stream=None) -> Checkpoint:
+    """Keep a [rows, parts * cols] bf16 / fp16 / fp32 activation in 8 bits."""
+    where = "checkpoint"
+    ld = _matrix(x, where, "x")
+    rows, total = x.shape
+    _require(parts >= 1 and total % parts == 0, where, f"{total} columns are not {parts} equal parts")
+    with _alloc_on(stream):
+        c = _checkpoint_buffers(rows, total // parts, parts, x.device, fmt)
+    fp8_checkpoint(x, DTYPES[x.dtype], rows, c.cols, ld, parts, fmt, c.q, c.q.shape[1], c.s, c.s.shape[1], stream)
+    return c
+
+
+def checkpoint_restore(c: Checkpoint, dtype: torch.dtype = torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """The [rows, parts * cols] activation a checkpoint stands for."""
+    where = "checkpoint_restore"
+    ld_q, ld_s = _checkpoint_strides(c, where)
+    if out is None:
+        _require(dtype in DTYPES, where, f"cannot restore to {dtype}")
+        with _alloc_on(stream):
+            out = torch.empty((c.rows, c.parts * c.cols), dtype=dtype, device=c.q.device)
+    ld = _matrix(out, where, "out", c.rows, c.parts * c.cols)
+    fp8_checkpoint_restore(c.q, ld_q, c.s, ld_s, c.fmt, c.rows, c.cols, c.parts, out, DTYPES[out.dtype], ld, stream)
+    return out
+
+
+def swiglu_checkpoint(gate_up: torch.Tensor, fmt: int = E4M3FN, h_out=None, stream=None):
+    """h = bf16(silu(gate) * up) of a bf16 [rows, 2F] gate|up tensor, and its
+    2-part 8-bit checkpoint, from one read.  Returns (h, checkpoint)."""
+    where = "swiglu_checkpoint"
+    ld = _matrix(gate_up, where, "gate_up", dtype=torch.bfloat16)
+    rows, total = gate_up.shape
+    _require(total % 2 == 0, where, "gate_up must have an even number of columns")
+    F = total // 2
+    with _alloc_on(stream):
+        h = torch.empty((rows, F), dtype=torch.bfloat16, device=gate_up.device) if h_out is None else h_out
+        c = _checkpoint_buffers(rows, F, 2, gate_up.device, fmt)
+    ld_h = _matrix(h, where, "h_out", rows, F, torch.bfloat16)
+    fp8_swiglu_checkpoint(gate_up, rows, F, ld, fmt, h, ld_h, c.q, c.q.shape[1], c.s, c.s.shape[1], stream)
+    return h, c
+
+
+def swiglu_backward(dh: torch.Tensor, src, out=None, return_h: bool = False, stream=None):
+    """Gradient of gate|up from dh (bf16 [rows, F]) and src: the bf16
+    [rows, 2F] gate|up tensor or its checkpoint.  With return_h also
+    h = bf16(silu(gate) * up) of what src holds: (d_gate_up, h)."""
+    where = "swiglu_backward"
+    ld_dh = _matrix(dh, where, "dh", dtype=torch.bfloat16)
+    rows, F = dh.shape
+    gate_up = q = s = None
+    ld = ld_q = ld_s = fmt = 0
+    if isinstance(src, Checkpoint):
+        ld_q, ld_s = _checkpoint_strides(src, where, rows, F, 2)
+        q, s, fmt = src.q, src.s, src.fmt
+    else:
+        gate_up, ld = src, _matrix(src, where, "gate_up", rows, 2 * F, torch.bfloat16)
+    with _alloc_on(stream):
+        d = torch.empty((rows, 2 * F), dtype=torch.bfloat16, device=dh.device) if out is None else out
+        h = torch.empty((rows, F), dtype=torch.bfloat16, device=dh.device) if return_h else None
+    ld_d = _matrix(d, where, "out", rows, 2 * F, torch.bfloat16)
+    fp8_swiglu_backward(dh, ld_dh, gate_up, ld, q, ld_q, s, ld_s, fmt, rows, F, d, ld_d, h, F, stream)
+    return (d, h) if return_h else d
+
+
+@dataclass
+class NormForward:
+    y: torch.Tensor
+    mean: torch.Tensor | None        # fp32 [rows]; None for RMS_NORM
+    rstd: torch.Tensor               # fp32 [rows]
+    checkpoint: Checkpoint | None    # of the normalized rows
+
+
+@dataclass
+class NormBackward:
+    dx: torch.Tensor
+    dweight: torch.Tensor | None
+    dbias: torch.Tensor | None
+
+
+def norm_forward(x: torch.Tensor, weight=None, bias=None, kind: int = LAYER_NORM, eps: float = 1e-5, out_dtype=None,
+                 checkpoint_fmt=None, out=None, stream=None) -> NormForward:
+    """Layer or RMS norm of the rows of x (bf16 / fp16 / fp32 [rows, cols]),
+    y = xhat * weight + bias, in x's type or, for an fp32 x, out_dtype.  With
+    checkpoint_fmt (E4M3FN or E5M2) xhat is kept in 8 bits for norm_backward,
+    which then needs neither x nor the mean."""
+    where = "norm_forward"
+    ld = _matrix(x, where, "x")
+    rows, cols = x.shape
+    _vector(weight, where, "weight", cols)
+    _vector(bias, where, "bias", cols, None if weight is None else weight.dtype)
+    w = weight if weight is not None else bias
+    out_dtype = out.dtype if out is not None else out_dtype or x.dtype
+    _require(out_dtype in DTYPES, where, f"cannot write {out_dtype}")
+    with _alloc_on(stream):
+        y = torch.empty((rows, cols), dtype=out_dtype, device=x.device) if out is None else out
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device) if kind == LAYER_NORM else None
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        c = _checkpoint_buffers(rows, cols, 1, x.device, checkpoint_fmt) if checkpoint_fmt is not None else None
+    ld_y = _matrix(y, where, "out", rows, cols)
+    q, s, ld_q, ld_s, fmt = (c.q, c.s, c.q.shape[1], c.s.shape[1], c.fmt) if c else (None, None, 0, 0, 0)
+    fp8_norm_forward(x, DTYPES[x.dtype], ld, rows, cols, kind, eps, weight, bias, 0 if w is None else DTYPES[w.dtype],
+                     y, DTYPES[out_dtype], ld_y, mean, rstd, fmt, q, ld_q, s, ld_s, stream)
+    return NormForward(y, mean, rstd, c)
+
+
+def norm_backward(dy: torch.Tensor, src, mean, rstd: torch.Tensor, weight=None, kind: int = LAYER_NORM, dx_dtype=None,
+                  weight_grad: bool = True, bias_grad=None, out=None, stream=None) -> NormBackward:
+    """Backward of norm_forward from src: the forward's x, or the checkpoint
+    it made (mean is then not read and may be None).  dweight and dbias have
+    the weight's type (fp32 without a weight); bias_grad defaults to whether
+    the norm is a layer norm.  dx has x's type; from a checkpoint, dx_dtype,
+    by default dy's type."""
+    where = "norm_backward"
+    ld_dy = _matrix(dy, where, "dy")
+    rows, cols = dy.shape
+    _vector(rstd, where, "rstd", rows, torch.float32)
+    _vector(mean, where, "mean", rows, torch.float32)
+    _vector(weight, where, "weight", cols)
+    x = q = s = None
+    ld_x = ld_q = ld_s = fmt = 0
+    if isinstance(src, Checkpoint):
+        ld_q, ld_s = _checkpoint_strides(src, where, rows, cols, 1)
+        q, s, fmt = src.q, src.s, src.fmt
+        dx_dtype = dx_dtype or (dy.dtype if out is None else out.dtype)
+    else:
+        x, ld_x = src, _matrix(src, where, "x", rows, cols)
+        _require(dx_dtype is None or dx_dtype == x.dtype, where, f"dx of a {x.dtype} x cannot be {dx_dtype}")
+        _require(kind != LAYER_NORM or mean is not None, where, "a layer norm's backward from x needs its mean")
+        dx_dtype = x.dtype
+    _require(dx_dtype in DTYPES, where, f"cannot write {dx_dtype}")
+    bias_grad = kind == LAYER_NORM if bias_grad is None else bias_grad
+    w_dtype = torch.float32 if weight is None else weight.dtype
+    with _alloc_on(stream):
+        dx = torch.empty((rows, cols), dtype=dx_dtype, device=dy.device) if out is None else out
+        dw = torch.empty(cols, dtype=w_dtype, device=dy.device) if weight_grad else None
+        db = torch.empty(cols, dtype=w_dtype, device=dy.device) if bias_grad else None
+        ws, n = None, 0
+        if weight_grad or bias_grad:
+            n = fp8_norm_workspace_bytes(rows, cols)
+            ws = torch.empty(n, dtype=torch.uint8, device=dy.device)
+    ld_dx = _matrix(dx, where, "out", rows, cols, dx_dtype)
+    fp8_norm_backward(dy, DTYPES[dy.dtype], ld_dy, x, ld_x, q, ld_q, s, ld_s, fmt, rows, cols, kind, mean, rstd,
+                      weight, DTYPES[w_dtype], dx, DTYPES[dx_dtype], ld_dx, dw, db, ws, n, stream)
+    return NormBackward(dx, dw, db)

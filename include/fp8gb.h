@@ -18,7 +18,11 @@
  * (fp8_permute_quantize, fp8_swiglu_quantize), the MXFP8 recipe (fp8_mx_quantize, fp8_mx_gemm,
  * fp8_mx_grouped_gemm, and the fused MoE prologues fp8_mx_permute_quantize
  * and fp8_mx_swiglu_quantize), and the blockwise recipe
- * (fp8_blockwise_quantize, whose scales feed fp8_mx_gemm).
+ * (fp8_blockwise_quantize, whose scales feed fp8_mx_gemm).  Between the linear
+ * layers: layer / RMS norm forward and backward (fp8_norm_forward,
+ * fp8_norm_backward), the SwiGLU forward and backward
+ * (fp8_swiglu_checkpoint, fp8_swiglu_backward) and 8-bit checkpoints of what
+ * their backward needs (fp8_checkpoint, fp8_checkpoint_restore).
  *
  * Method sources (page title, section):
  *   - "FP8 training for Flux models" (AMD Primus guide), Configuration >
@@ -509,6 +513,109 @@ FP8GB_API fp8_status_t fp8_mx_grouped_gemm(int mode, const uint8_t *A, int fa, c
                                            const uint8_t *B, int fb, const uint8_t *sB,
                                            const int32_t *group_offsets, int G, int64_t M_total, int64_t N,
                                            int64_t K, void *C_bf16, int64_t ld_T, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The non-linear parts of a block between two linear layers: norms, the
+ * SwiGLU backward, and 8-bit checkpoints of what their backward needs.  The
+ * pages name neither; these entry points are this library's own.
+ *
+ * Element types of the tensors below (the linear-layer entry points above
+ * take bf16).  Tensors are row-major with a row stride (ld) in elements, of
+ * any width and any element-aligned address and stride; wide accesses are
+ * used where the addresses and strides allow them.  Outputs must not overlap
+ * inputs.  rows, cols <= 2^31 - 33.
+ *
+ * Checkpoint format.  A row is cut into blocks of FP8_MX_BLOCK = 32 columns
+ * (the last one may be short).  A block's scale is X = 2^e, e the smallest
+ * integer with amax <= fp8_max * 2^e, clamped to [-127, 127], stored as the
+ * byte e + 127 (0 for an all-zero block); a block with a NaN or Inf has byte
+ * 255 and restores as NaN.  Each element is rne_fp8(v / X): nothing finite
+ * saturates, and an element of at least 2^-13 (E4M3; 2^-28 for E5M2) of its
+ * block's largest restores within 2^-4 (2^-3) of itself.  Several `parts` of the
+ * same width side by side (gate | up) each start a block: with W = roundup(
+ * cols, 32), part p's codes are at [row * ld_q + p * W] and its scale bytes
+ * at [row * ld_s + p * W / 32]; codes between cols and W are 0.  q is
+ * 32-byte aligned, ld_q % 32 == 0, ld_q >= parts * W, ld_s >= parts * W / 32.
+ * fmt: FP8_E4M3FN or FP8_E5M2 (FP8_ERR_UNSUPPORTED for the fnuz formats).
+ * ------------------------------------------------------------------------ */
+typedef enum { FP8_DTYPE_BF16 = 0, FP8_DTYPE_F16 = 1, FP8_DTYPE_F32 = 2 } fp8_dtype_t;
+enum { FP8_NORM_LAYER = 0, FP8_NORM_RMS = 1 };
+
+/*
+ * fp8_checkpoint -- store x [rows][ld_x] (parts tensors of cols columns side
+ * by side: part p at column p * cols) as codes and scale bytes.
+ * fp8_checkpoint_restore -- the inverse: x = code * X, rounded to the type
+ * (exact in bf16 and fp32 unless it falls below their range).
+ * rows == 0 returns FP8_OK without touching any buffer.
+ */
+FP8GB_API fp8_status_t fp8_checkpoint(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ld_x, int parts,
+                                      int fmt, uint8_t *q, int64_t ld_q, uint8_t *s, int64_t ld_s, void *stream);
+
+FP8GB_API fp8_status_t fp8_checkpoint_restore(const uint8_t *q, int64_t ld_q, const uint8_t *s, int64_t ld_s, int fmt,
+                                              int64_t rows, int64_t cols, int parts, void *x, int dtype,
+                                              int64_t ld_x, void *stream);
+
+/*
+ * fp8_swiglu_checkpoint -- h = bf16(silu(gate) * up) of gate_up_bf16 [rows][ld]
+ * (gate in columns [0, F), up in [F, 2F)), evaluated as in
+ * fp8_mx_swiglu_quantize, and the 2-part checkpoint of gate_up, in one read.
+ *
+ * fp8_swiglu_backward -- with s = sigma(gate),
+ *   d_gate = dh * up * s * (1 + gate * (1 - s)),  d_up = dh * gate * s,
+ * written side by side into d_gate_up_bf16 [rows][ld_d].  gate and up come
+ * from gate_up_bf16 (q, s NULL) or, with gate_up_bf16 NULL, from their
+ * 2-part checkpoint.  h_bf16: optional, receives bf16(silu(gate) * up) of
+ * the same gate and up (the down projection's input, recomputed).
+ */
+FP8GB_API fp8_status_t fp8_swiglu_checkpoint(const void *gate_up_bf16, int64_t rows, int64_t F, int64_t ld, int fmt,
+                                             void *h_bf16, int64_t ld_h, uint8_t *q, int64_t ld_q, uint8_t *s,
+                                             int64_t ld_s, void *stream);
+
+FP8GB_API fp8_status_t fp8_swiglu_backward(const void *dh_bf16, int64_t ld_dh, const void *gate_up_bf16, int64_t ld,
+                                           const uint8_t *q, int64_t ld_q, const uint8_t *s, int64_t ld_s, int fmt,
+                                           int64_t rows, int64_t F, void *d_gate_up_bf16, int64_t ld_d,
+                                           void *h_bf16, int64_t ld_h, void *stream);
+
+/*
+ * fp8_norm_forward -- per row of n = cols elements, in fp32:
+ *   FP8_NORM_LAYER  mu = sum x / n,  FP8_NORM_RMS  mu = 0;
+ *   r = 1 / sqrt(sum (x - mu)^2 / n + eps),  xh = (x - mu) r,  y = xh w + b.
+ *   x, y           y_dtype is x_dtype, or bf16 / f16 with an f32 x
+ *                  (FP8_ERR_UNSUPPORTED otherwise).
+ *   weight, bias   [cols] of w_dtype; NULL: 1 and 0.
+ *   mean, rstd     fp32 [rows], each optional.
+ *   q, s           optional (both or neither): the checkpoint of xh.
+ *   eps >= 0; a row holding a NaN or Inf gives NaN in that row alone.
+ *
+ * fp8_norm_backward -- with g = dy w, c1 = sum g / n (0 for RMS),
+ *   c2 = sum g xh / n:  dx = r (g - c1 - xh c2),  dweight = sum over rows of
+ *   dy xh,  dbias = sum over rows of dy.
+ *   x              the forward's input (type x_dtype; q, s NULL), or NULL:
+ *                  xh is read from the checkpoint q, s of format fmt.
+ *   mean, rstd     the forward's; mean is read for FP8_NORM_LAYER with x only.
+ *   dweight, dbias [cols] of w_dtype, each optional, summed in fp32 in an
+ *                  order that depends on the shape and device alone; rows ==
+ *                  0 writes zeros.
+ *   workspace      fp8_norm_workspace_bytes(rows, cols) bytes, 16-byte
+ *                  aligned, contents irrelevant; not needed when neither
+ *                  dweight nor dbias is asked for.  Two calls in flight at
+ *                  once need two.
+ */
+FP8GB_API fp8_status_t fp8_norm_forward(const void *x, int x_dtype, int64_t ld_x, int64_t rows, int64_t cols,
+                                        int kind, float eps, const void *weight, const void *bias, int w_dtype,
+                                        void *y, int y_dtype, int64_t ld_y, float *mean, float *rstd, int fmt,
+                                        uint8_t *q, int64_t ld_q, uint8_t *s, int64_t ld_s, void *stream);
+
+/* Bytes of the workspace of fp8_norm_backward on the current device; -1 for
+ * bad arguments. */
+FP8GB_API int64_t fp8_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+FP8GB_API fp8_status_t fp8_norm_backward(const void *dy, int y_dtype, int64_t ld_dy, const void *x, int64_t ld_x,
+                                         const uint8_t *q, int64_t ld_q, const uint8_t *s, int64_t ld_s, int fmt,
+                                         int64_t rows, int64_t cols, int kind, const float *mean, const float *rstd,
+                                         const void *weight, int w_dtype, void *dx, int x_dtype, int64_t ld_dx,
+                                         void *dweight, void *dbias, void *workspace, int64_t workspace_bytes,
+                                         void *stream);
 
 /* Synchronise `stream`, then report and clear a device-side timeout word:
  * FP8_OK, FP8_ERR_TIMEOUT, or FP8_ERR_CUDA. */
