@@ -4,9 +4,14 @@
 //
 // All four are one pass over their tensors and bounded by HBM.
 //
-// One warp works on one block of 32 columns, a lane per element: every
-// alignment, row stride and width is the same code, the block maximum is five
-// shuffles, and a warp's accesses are consecutive.
+// Wide form (addresses and strides multiples of 16 bytes): a thread works on
+// 16 consecutive columns, half a block, so the bf16 side is one 32-byte access,
+// the codes one of 16, and the block maximum one shuffle with the neighbour.
+// A thread issues the loads of UNROLL rows before it works on the first.  The
+// threads of a block cover tx chunks of ty rows, so no thread divides.
+//
+// Narrow form (any other alignment): a lane per element and a warp per block
+// of 32 columns; accesses stay consecutive at every width and stride.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -20,6 +25,13 @@ namespace fp8gb {
 constexpr int CK_THREADS = 256;
 constexpr int CK_WARPS = CK_THREADS / 32;
 
+// How the blocks of the wide kernels cover rows x chunks of 16 columns.
+struct WideGeometry {
+    int lg;             // a block is 2^lg chunks wide and CK_THREADS / 2^lg rows high, times UNROLL
+    uint32_t n_tiles;   // blocks across a row
+    uint32_t grid;
+};
+
 struct CkArgs {
     void *x;  // store: input; restore: output
     int64_t ld_x;
@@ -27,6 +39,8 @@ struct CkArgs {
     int64_t ld_q, ld_s;
     int64_t rows, cols;
     int parts, fmt;
+    WideGeometry geo;
+    int w32;  // x's rows and parts start on 32-byte boundaries
 };
 
 struct SwArgs {
@@ -38,7 +52,171 @@ struct SwArgs {
     int fmt;
     __nv_bfloat16 *h, *d;
     int64_t ld_h, ld_d;
+    WideGeometry geo;
+    int w32;
 };
+
+// A thread's chunk and first row; its later rows are `ty` further each.
+struct WidePlace {
+    int64_t chunk, row;
+    int ty;
+};
+
+template <int UNROLL>
+__device__ __forceinline__ WidePlace wide_place(const WideGeometry &g)
+{
+    const uint32_t rt = blockIdx.x / g.n_tiles, ct = blockIdx.x - rt * g.n_tiles;
+    WidePlace p;
+    p.ty = CK_THREADS >> g.lg;
+    p.chunk = ((int64_t)ct << g.lg) + (threadIdx.x & ((1 << g.lg) - 1));
+    p.row = (int64_t)rt * p.ty * UNROLL + (threadIdx.x >> g.lg);
+    return p;
+}
+
+constexpr int STORE_UNROLL = 4, RESTORE_UNROLL = 4, SWIGLU_UNROLL = 2, BACKWARD_UNROLL = 2;
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(CK_THREADS) checkpoint_wide_kernel(CkArgs a)
+{
+    const WidePlace p = wide_place<STORE_UNROLL>(a.geo);
+    const int64_t cpp = ckpt_width(a.cols) / 16;  // chunks of a part
+    const bool in = p.chunk < a.parts * cpp;
+    const int64_t part = a.parts == 1 ? 0 : p.chunk / cpp, c = (p.chunk - part * cpp) * 16;
+    const T *x = static_cast<const T *>(a.x) + part * a.cols + c;
+    Raw16<T> raw[STORE_UNROLL];
+#pragma unroll
+    for (int k = 0; k < STORE_UNROLL; k++) {
+        const int64_t r = p.row + (int64_t)k * p.ty;
+        load16(x + r * a.ld_x, in && r < a.rows ? a.cols - c : 0, a.w32, raw[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < STORE_UNROLL; k++) {
+        const int64_t r = p.row + (int64_t)k * p.ty;
+        float f[16];
+        unpack16(raw[k], f);
+        const uint32_t code = ckpt_code(block_amax16(f), FMT);
+        if (!in || r >= a.rows) continue;
+        *reinterpret_cast<uint4 *>(a.q + r * a.ld_q + p.chunk * 16) = encode16<FMT>(f, ckpt_inv_scale(code));
+        if (!(p.chunk & 1)) a.s[r * a.ld_s + (p.chunk >> 1)] = (uint8_t)code;
+    }
+}
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(CK_THREADS) restore_wide_kernel(CkArgs a)
+{
+    const WidePlace p = wide_place<RESTORE_UNROLL>(a.geo);
+    const int64_t cpp = ckpt_width(a.cols) / 16;
+    if (p.chunk >= a.parts * cpp) return;
+    const int64_t part = a.parts == 1 ? 0 : p.chunk / cpp, c = (p.chunk - part * cpp) * 16;
+    T *x = static_cast<T *>(a.x) + part * a.cols + c;
+    uint4 q[RESTORE_UNROLL];
+    uint32_t s[RESTORE_UNROLL];
+#pragma unroll
+    for (int k = 0; k < RESTORE_UNROLL; k++) {
+        const int64_t r = p.row + (int64_t)k * p.ty;
+        if (r >= a.rows) break;
+        q[k] = ld_stream_16b(a.q + r * a.ld_q + p.chunk * 16);
+        s[k] = __ldg(a.s + r * a.ld_s + (p.chunk >> 1));
+    }
+#pragma unroll
+    for (int k = 0; k < RESTORE_UNROLL; k++) {
+        const int64_t r = p.row + (int64_t)k * p.ty;
+        if (r >= a.rows) break;
+        float f[16];
+        decode16<FMT>(q[k], ckpt_scale(s[k]), f);
+        store16(x + r * a.ld_x, f, a.cols - c, a.w32);
+    }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(CK_THREADS) swiglu_checkpoint_wide_kernel(SwArgs a)
+{
+    const WidePlace p = wide_place<SWIGLU_UNROLL>(a.geo);
+    const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16;
+    const bool in = p.chunk < cpp;
+    Raw16<__nv_bfloat16> gr[SWIGLU_UNROLL], ur[SWIGLU_UNROLL];
+#pragma unroll
+    for (int k = 0; k < SWIGLU_UNROLL; k++) {
+        const int64_t r = p.row + (int64_t)k * p.ty, n = in && r < a.rows ? a.F - c : 0;
+        load16(a.gate_up + r * a.ld + c, n, a.w32, gr[k]);
+        load16(a.gate_up + r * a.ld + a.F + c, n, a.w32, ur[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < SWIGLU_UNROLL; k++) {
+        const int64_t r = p.row + (int64_t)k * p.ty;
+        float g[16], u[16], h[16];
+        unpack16(gr[k], g);
+        unpack16(ur[k], u);
+        const uint32_t cg = ckpt_code(block_amax16(g), FMT), cu = ckpt_code(block_amax16(u), FMT);
+        if (!in || r >= a.rows) continue;
+#pragma unroll
+        for (int j = 0; j < 16; j++) h[j] = swiglu1(g[j], u[j]);
+        store16(a.h + r * a.ld_h + c, h, a.F - c, a.w32);
+        uint8_t *q = a.q + r * a.ld_q + c;
+        *reinterpret_cast<uint4 *>(q) = encode16<FMT>(g, ckpt_inv_scale(cg));
+        *reinterpret_cast<uint4 *>(q + cpp * 16) = encode16<FMT>(u, ckpt_inv_scale(cu));
+        if (!(p.chunk & 1)) {
+            uint8_t *s = a.s + r * a.ld_s + (p.chunk >> 1);
+            s[0] = (uint8_t)cg;
+            s[cpp >> 1] = (uint8_t)cu;
+        }
+    }
+}
+
+// CKPT: gate and up from the checkpoint, else from bf16.
+template <int FMT, bool CKPT>
+__global__ void __launch_bounds__(CK_THREADS) swiglu_backward_wide_kernel(SwArgs a)
+{
+    const WidePlace p = wide_place<BACKWARD_UNROLL>(a.geo);
+    const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16, n = a.F - c;
+    if (n <= 0) return;
+    Raw16<__nv_bfloat16> gr[BACKWARD_UNROLL], ur[BACKWARD_UNROLL], dr[BACKWARD_UNROLL];
+    uint4 gq[BACKWARD_UNROLL], uq[BACKWARD_UNROLL];
+    uint32_t gs[BACKWARD_UNROLL], us[BACKWARD_UNROLL];
+#pragma unroll
+    for (int k = 0; k < BACKWARD_UNROLL; k++) {
+        const int64_t r = p.row + (int64_t)k * p.ty;
+        if (r >= a.rows) break;
+        if constexpr (CKPT) {
+            const uint8_t *q = a.q + r * a.ld_q + c, *s = a.s + r * a.ld_s + (p.chunk >> 1);
+            gq[k] = ld_stream_16b(q);
+            uq[k] = ld_stream_16b(q + cpp * 16);
+            gs[k] = __ldg(s);
+            us[k] = __ldg(s + (cpp >> 1));
+        } else {
+            load16(a.gate_up + r * a.ld + c, n, a.w32, gr[k]);
+            load16(a.gate_up + r * a.ld + a.F + c, n, a.w32, ur[k]);
+        }
+        load16(a.dh + r * a.ld_dh + c, n, a.w32, dr[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < BACKWARD_UNROLL; k++) {
+        const int64_t r = p.row + (int64_t)k * p.ty;
+        if (r >= a.rows) break;
+        float g[16], u[16], d[16];
+        if constexpr (CKPT) {
+            decode16<FMT>(gq[k], ckpt_scale(gs[k]), g);
+            decode16<FMT>(uq[k], ckpt_scale(us[k]), u);
+        } else {
+            unpack16(gr[k], g);
+            unpack16(ur[k], u);
+        }
+        unpack16(dr[k], d);
+        // the gradients take the places of g and u, h that of dh
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            float2 dg, du, h;
+            swiglu_grad2(make_float2(g[j], g[j + 1]), make_float2(u[j], u[j + 1]), make_float2(d[j], d[j + 1]), dg,
+                         du, h);
+            g[j] = dg.x, g[j + 1] = dg.y;
+            u[j] = du.x, u[j + 1] = du.y;
+            d[j] = h.x, d[j + 1] = h.y;
+        }
+        if (a.h) store16(a.h + r * a.ld_h + c, d, n, a.w32);
+        store16(a.d + r * a.ld_d + c, g, n, a.w32);
+        store16(a.d + r * a.ld_d + a.F + c, u, n, a.w32);
+    }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(CK_THREADS) checkpoint_kernel(CkArgs a)
@@ -101,11 +279,12 @@ __global__ void __launch_bounds__(CK_THREADS) swiglu_backward_kernel(SwArgs a)
                 g = ckpt_load_one(q, s, c, a.fmt);
                 u = ckpt_load_one(q + nb * FP8_MX_BLOCK, s + nb, c, a.fmt);
             }
-            float dg, du;
-            swiglu_grad1(g, u, to_f32(a.dh[r * a.ld_dh + c]), dg, du);
-            a.d[r * a.ld_d + c] = from_f32<__nv_bfloat16>(dg);
-            a.d[r * a.ld_d + a.F + c] = from_f32<__nv_bfloat16>(du);
-            if (a.h) a.h[r * a.ld_h + c] = from_f32<__nv_bfloat16>(swiglu1(g, u));
+            float2 dg, du, h;
+            swiglu_grad2(make_float2(g, 0.0f), make_float2(u, 0.0f),
+                         make_float2(to_f32(a.dh[r * a.ld_dh + c]), 0.0f), dg, du, h);
+            a.d[r * a.ld_d + c] = from_f32<__nv_bfloat16>(dg.x);
+            a.d[r * a.ld_d + a.F + c] = from_f32<__nv_bfloat16>(du.x);
+            if (a.h) a.h[r * a.ld_h + c] = from_f32<__nv_bfloat16>(h.x);
         }
     }
 }
@@ -115,6 +294,30 @@ static unsigned row_grid(int64_t rows)
 {
     const int64_t cap = (int64_t)num_sms() * 8;
     return (unsigned)(rows < cap ? rows : cap);
+}
+
+// The widest block whose tiles cover a row of `chunks` with at most 1/16 of
+// their threads idle (two chunks at least: a block's halves are neighbours).
+static WideGeometry wide_geometry(int64_t rows, int64_t chunks, int unroll)
+{
+    WideGeometry g;
+    g.lg = 8;
+    while (g.lg > 1) {
+        const int64_t covered = ((chunks + (1LL << g.lg) - 1) >> g.lg) << g.lg;
+        if ((covered - chunks) * 16 <= covered) break;
+        g.lg--;
+    }
+    g.n_tiles = (uint32_t)((chunks + (1LL << g.lg) - 1) >> g.lg);
+    const int64_t high = (int64_t)(CK_THREADS >> g.lg) * unroll;
+    const int64_t grid = (rows + high - 1) / high * g.n_tiles;
+    g.grid = grid > INT32_MAX ? 0 : (uint32_t)grid;  // 0: more blocks than a launch holds
+    return g;
+}
+
+// Whether every row (and part) of a tensor starts on an `a`-byte boundary.
+static bool rows_aligned(const void *p, int64_t ld, int64_t offset, int size, int a)
+{
+    return aligned(p, a) && ld * size % a == 0 && offset * size % a == 0;
 }
 
 static fp8_status_t check_format(int fmt)
@@ -149,6 +352,32 @@ static fp8_status_t check_bf16(const void *p, int64_t ld, int64_t cols)
     return aligned(p, 2) ? FP8_OK : FP8_ERR_ALIGNMENT;
 }
 
+// The wide form where every row and part of x is 16-byte aligned.
+template <typename T>
+static bool plan_wide(CkArgs &a, int unroll)
+{
+    const int64_t off = a.parts > 1 ? a.cols : 0;
+    a.geo = wide_geometry(a.rows, a.parts * (ckpt_width(a.cols) / 16), unroll);
+    a.w32 = rows_aligned(a.x, a.ld_x, off, sizeof(T), 32);
+    return a.geo.grid && rows_aligned(a.x, a.ld_x, off, sizeof(T), 16);
+}
+
+template <typename T>
+static void launch_checkpoint(CkArgs a, cudaStream_t st)
+{
+    if (!plan_wide<T>(a, STORE_UNROLL)) checkpoint_kernel<T><<<row_grid(a.rows), CK_THREADS, 0, st>>>(a);
+    else if (a.fmt == FP8_E5M2) checkpoint_wide_kernel<T, FP8_E5M2><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    else checkpoint_wide_kernel<T, FP8_E4M3FN><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+}
+
+template <typename T>
+static void launch_restore(CkArgs a, cudaStream_t st)
+{
+    if (!plan_wide<T>(a, RESTORE_UNROLL)) restore_kernel<T><<<row_grid(a.rows), CK_THREADS, 0, st>>>(a);
+    else if (a.fmt == FP8_E5M2) restore_wide_kernel<T, FP8_E5M2><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    else restore_wide_kernel<T, FP8_E4M3FN><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+}
+
 }  // namespace fp8gb
 
 using namespace fp8gb;
@@ -160,10 +389,9 @@ extern "C" fp8_status_t fp8_checkpoint(const void *x, int dtype, int64_t rows, i
     const fp8_status_t rc = check_ck(a, dtype);
     if (rc != FP8_OK || rows == 0) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned grid = row_grid(rows);
-    if (dtype == FP8_DTYPE_BF16) checkpoint_kernel<__nv_bfloat16><<<grid, CK_THREADS, 0, st>>>(a);
-    else if (dtype == FP8_DTYPE_F16) checkpoint_kernel<__half><<<grid, CK_THREADS, 0, st>>>(a);
-    else checkpoint_kernel<float><<<grid, CK_THREADS, 0, st>>>(a);
+    if (dtype == FP8_DTYPE_BF16) launch_checkpoint<__nv_bfloat16>(a, st);
+    else if (dtype == FP8_DTYPE_F16) launch_checkpoint<__half>(a, st);
+    else launch_checkpoint<float>(a, st);
     return check_launch();
 }
 
@@ -175,10 +403,9 @@ extern "C" fp8_status_t fp8_checkpoint_restore(const uint8_t *q, int64_t ld_q, c
     const fp8_status_t rc = check_ck(a, dtype);
     if (rc != FP8_OK || rows == 0) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned grid = row_grid(rows);
-    if (dtype == FP8_DTYPE_BF16) restore_kernel<__nv_bfloat16><<<grid, CK_THREADS, 0, st>>>(a);
-    else if (dtype == FP8_DTYPE_F16) restore_kernel<__half><<<grid, CK_THREADS, 0, st>>>(a);
-    else restore_kernel<float><<<grid, CK_THREADS, 0, st>>>(a);
+    if (dtype == FP8_DTYPE_BF16) launch_restore<__nv_bfloat16>(a, st);
+    else if (dtype == FP8_DTYPE_F16) launch_restore<__half>(a, st);
+    else launch_restore<float>(a, st);
     return check_launch();
 }
 
@@ -204,7 +431,15 @@ extern "C" fp8_status_t fp8_swiglu_checkpoint(const void *gate_up_bf16, int64_t 
     a.s = s;
     a.ld_q = ld_q;
     a.ld_s = ld_s;
-    swiglu_checkpoint_kernel<<<row_grid(rows), CK_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    a.geo = wide_geometry(rows, ckpt_width(F) / 16, SWIGLU_UNROLL);
+    a.w32 = rows_aligned(a.gate_up, ld, F, 2, 32) && rows_aligned(a.h, ld_h, 0, 2, 32);
+    if (a.geo.grid && rows_aligned(a.gate_up, ld, F, 2, 16) && rows_aligned(a.h, ld_h, 0, 2, 16)) {
+        if (fmt == FP8_E5M2) swiglu_checkpoint_wide_kernel<FP8_E5M2><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+        else swiglu_checkpoint_wide_kernel<FP8_E4M3FN><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    } else {
+        swiglu_checkpoint_kernel<<<row_grid(rows), CK_THREADS, 0, st>>>(a);
+    }
     return check_launch();
 }
 
@@ -238,6 +473,20 @@ extern "C" fp8_status_t fp8_swiglu_backward(const void *dh_bf16, int64_t ld_dh, 
     a.ld_d = ld_d;
     a.h = static_cast<__nv_bfloat16 *>(h_bf16);
     a.ld_h = ld_h;
-    swiglu_backward_kernel<<<row_grid(rows), CK_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    a.geo = wide_geometry(rows, ckpt_width(F) / 16, BACKWARD_UNROLL);
+    const auto all_aligned = [&](int al) {
+        return rows_aligned(a.dh, ld_dh, 0, 2, al) && rows_aligned(a.d, ld_d, F, 2, al) &&
+               rows_aligned(a.h, a.h ? ld_h : 0, 0, 2, al) && rows_aligned(a.gate_up, a.gate_up ? ld : 0, F, 2, al);
+    };
+    a.w32 = all_aligned(32);
+    if (!a.geo.grid || !all_aligned(16))
+        swiglu_backward_kernel<<<row_grid(rows), CK_THREADS, 0, st>>>(a);
+    else if (a.gate_up)
+        swiglu_backward_wide_kernel<FP8_E4M3FN, false><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    else if (fmt == FP8_E5M2)
+        swiglu_backward_wide_kernel<FP8_E5M2, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    else
+        swiglu_backward_wide_kernel<FP8_E4M3FN, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
     return check_launch();
 }

@@ -88,20 +88,10 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 // carries them.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// Maximum over the `width` consecutive lanes a block is spread over.
-template <int WIDTH>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t v)
-{
-#pragma unroll
-    for (int d = WIDTH / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
-}
-
-// One element per lane, a block per warp: store code and scale byte, return
-// what the checkpoint gives back for it.
+// One element per lane, a block per warp: store code and scale byte.
 __device__ __forceinline__ void ckpt_store_lane(float v, int fmt, uint8_t *q, uint8_t *s, int lane)
 {
-    const uint32_t code = ckpt_code(lanes_max<32>(abs_bits(v)), fmt);
+    const uint32_t code = ckpt_code(__reduce_max_sync(0xffffffffu, abs_bits(v)), fmt);
     const float t = v * ckpt_inv_scale(code);
     q[lane] = (uint8_t)(fmt == FP8_E5M2 ? cvt2<FP8_E5M2>(t, 0.0f) : cvt2<FP8_E4M3FN>(t, 0.0f));
     if (lane == 0) *s = (uint8_t)code;
@@ -113,22 +103,248 @@ __device__ __forceinline__ float ckpt_load_one(const uint8_t *q, const uint8_t *
     return v * ckpt_scale(s[col / FP8_MX_BLOCK]);
 }
 
-// SwiGLU backward of one pair, sigma formed as in swiglu1 (t = e^-|g| never
-// overflows; 1 - sigma is the other sign's sigma, so neither cancels):
-//   dg = dh u sigma (1 + g (1 - sigma)),  du = dh g sigma.
-// g = -Inf takes the limit 0 of both sigma and sigma g (t == 0).  The error
-// of sigma and of its complement is a few fp32 ulps, so each gradient is
-// within 2^-9 of itself or 2^-20 |dh u| before its rounding to bf16.
-__device__ __forceinline__ void swiglu_grad1(float g, float u, float dh, float &dg, float &du)
+// ---------------------------------------------------------------------------
+// Sixteen consecutive elements per thread, half a block: 32 bytes of a 16-bit
+// type (one 32-byte access when everything is 32-byte aligned, `w32`, else
+// two of 16), 64 of fp32, 16 bytes of codes.
+// ---------------------------------------------------------------------------
+template <typename T>
+struct Raw16 {
+    uint4 v[sizeof(T)];  // 16 * sizeof(T) bytes
+};
+
+__device__ __forceinline__ void ld_stream_32b(const void *p, uint4 &lo, uint4 &hi)
 {
-    const float t = __expf(-fabsf(g));
-    const float r = __fdividef(1.0f, 1.0f + t);
-    const float near1 = r, near0 = t * r;  // sigma(|g|), sigma(-|g|)
-    const float gc = t == 0.0f ? 0.0f : g * near0;              // g (1 - sigma) for g >= 0, g sigma for g < 0
-    const float gs = g >= 0.0f ? g * near1 : gc;                // silu(g)
-    const float slope = g >= 0.0f ? near1 * (1.0f + gc) : near0 + gc * near1;  // sigma + sigma g (1 - sigma)
-    dg = dh * u * slope;
-    du = dh * gs;
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w)
+                 : "l"(p));
+}
+
+__device__ __forceinline__ uint4 ld_stream_16b(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void st_32b(void *p, const uint4 &lo, const uint4 &hi)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(lo.x), "r"(lo.y),
+                 "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                 : "memory");
+}
+
+// Elements 0 .. n-1 from p (n >= 16: all of them by wide loads), zeros after.
+template <typename T>
+__device__ __forceinline__ void load16(const T *p, int64_t n, bool w32, Raw16<T> &r)
+{
+    if (n >= 16) {
+        if (w32) {
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T); j += 2) ld_stream_32b(p + j * (16 / sizeof(T)), r.v[j], r.v[j + 1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T); j++) r.v[j] = ld_stream_16b(p + j * (16 / sizeof(T)));
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < (int)sizeof(T); j++) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            constexpr int PER = 4 / sizeof(T);  // elements per word
+            const int e = (4 * j + k) * PER;
+            if constexpr (sizeof(T) == 4) {
+                w[k] = e < n ? __float_as_uint(to_f32(p[e])) : 0u;
+            } else {
+                const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+                w[k] = (e < n ? (uint32_t)h[e] : 0u) | (e + 1 < n ? (uint32_t)h[e + 1] << 16 : 0u);
+            }
+        }
+        r.v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Two elements of a 32-bit word.
+template <typename T>
+__device__ __forceinline__ float2 word_to_float2(uint32_t w)
+{
+    if constexpr (sizeof(T) == 2) {
+        if constexpr (__is_same(T, __half)) return __half22float2(*reinterpret_cast<__half2 *>(&w));
+        return make_float2(bf16lo(w), bf16hi(w));
+    }
+    return make_float2(__uint_as_float(w), 0.0f);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t float2_to_word(float lo, float hi)
+{
+    if constexpr (__is_same(T, __half)) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return pack_bf16x2(lo, hi);
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack16(const Raw16<T> &r, float (&f)[16])
+{
+#pragma unroll
+    for (int j = 0; j < (int)sizeof(T); j++) {
+        const uint32_t w[4] = {r.v[j].x, r.v[j].y, r.v[j].z, r.v[j].w};
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            if constexpr (sizeof(T) == 4) {
+                f[4 * j + k] = __uint_as_float(w[k]);
+            } else {
+                const float2 v = word_to_float2<T>(w[k]);
+                f[8 * j + 2 * k] = v.x;
+                f[8 * j + 2 * k + 1] = v.y;
+            }
+        }
+    }
+}
+
+// Elements 0 .. n-1 to p.
+template <typename T>
+__device__ __forceinline__ void store16(T *p, const float (&f)[16], int64_t n, bool w32)
+{
+    if (n >= 16) {
+        uint4 v[sizeof(T)];
+#pragma unroll
+        for (int j = 0; j < (int)sizeof(T); j++) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                if constexpr (sizeof(T) == 4) w[k] = __float_as_uint(f[4 * j + k]);
+                else w[k] = float2_to_word<T>(f[8 * j + 2 * k], f[8 * j + 2 * k + 1]);
+            }
+            v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (w32) {
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T); j += 2) st_32b(p + j * (16 / sizeof(T)), v[j], v[j + 1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T); j++) *reinterpret_cast<uint4 *>(p + j * (16 / sizeof(T))) = v[j];
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j++)
+        if (j < n) p[j] = from_f32<T>(f[j]);
+}
+
+// The largest magnitude of a block whose halves two neighbouring lanes hold.
+__device__ __forceinline__ uint32_t block_amax16(const float (&f)[16])
+{
+    uint32_t m = abs_bits(f[0]);
+#pragma unroll
+    for (int j = 1; j < 16; j++) m = max(m, abs_bits(f[j]));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+}
+
+template <int FMT>
+__device__ __forceinline__ uint4 encode16(const float (&f)[16], float inv)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        float a = f[4 * j], b = f[4 * j + 1], c = f[4 * j + 2], d = f[4 * j + 3];
+        mul2_rn(a, b, inv, inv);
+        mul2_rn(c, d, inv, inv);
+        w[j] = cvt4<FMT>(a, b, c, d);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int FMT>
+__device__ __forceinline__ void decode16(const uint4 &q, float scale, float (&f)[16])
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const float2 a = fp8x2_to_float2<FMT>(w[j] & 0xFFFFu), b = fp8x2_to_float2<FMT>(w[j] >> 16);
+        f[4 * j] = a.x;
+        f[4 * j + 1] = a.y;
+        f[4 * j + 2] = b.x;
+        f[4 * j + 3] = b.y;
+        mul2_rn(f[4 * j], f[4 * j + 1], scale, scale);
+        mul2_rn(f[4 * j + 2], f[4 * j + 3], scale, scale);
+    }
+}
+
+// Packed pairs of fp32, each operation rounded to nearest.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    mul2_rn(a.x, a.y, b.x, b.y);
+    return a;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 y, {%4, %5};\n\t"
+        "mov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\t"
+        "mov.b64 {%0, %1}, w;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)  // NaN if either is
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_fast(float v)  // 1 ulp; 0 where 1 / v is subnormal
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// SwiGLU backward of two pairs (gate, up), with e = e^-gate and sigma =
+// 1 / (1 + e), so that 1 - sigma = e sigma without cancellation:
+//   silu = gate sigma,  d_gate = dh up (sigma + silu (1 - sigma)),
+//   d_up = dh silu,  h = silu up.
+// gate is held at -88 from below: e^88 is finite and its reciprocal flushes to
+// zero, so sigma, silu and the slope are 0 there (they are below 2^-119), also
+// for gate = -Inf, where the formula as written gives NaN.  NaN stays
+// NaN.  e and sigma err by less than 2^-17 relative, far inside the bf16
+// rounding of the results.
+__device__ __forceinline__ void swiglu_grad2(float2 g, float2 u, float2 dh, float2 &dg, float2 &du, float2 &h)
+{
+    g = make_float2(max_nan(g.x, -88.0f), max_nan(g.y, -88.0f));
+    const float2 e = make_float2(__expf(-g.x), __expf(-g.y));
+    const float2 d = add2(e, make_float2(1.0f, 1.0f));
+    const float2 s = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    const float2 silu = mul2(g, s);
+    const float2 slope = fma2(silu, mul2(e, s), s);
+    dg = mul2(mul2(dh, u), slope);
+    du = mul2(dh, silu);
+    h = mul2(silu, u);
 }
 
 }  // namespace fp8gb

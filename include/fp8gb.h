@@ -565,7 +565,9 @@ FP8GB_API fp8_status_t fp8_checkpoint_restore(const uint8_t *q, int64_t ld_q, co
  * written side by side into d_gate_up_bf16 [rows][ld_d].  gate and up come
  * from gate_up_bf16 (q, s NULL) or, with gate_up_bf16 NULL, from their
  * 2-part checkpoint.  h_bf16: optional, receives bf16(silu(gate) * up) of
- * the same gate and up (the down projection's input, recomputed).
+ * the same gate and up (the down projection's input, recomputed).  fp32
+ * arithmetic with the fast exponential, one rounding each; a gate below
+ * about -87, -Inf included, gives zeros (2^-119 of |dh|, |dh up| or |up|).
  */
 FP8GB_API fp8_status_t fp8_swiglu_checkpoint(const void *gate_up_bf16, int64_t rows, int64_t F, int64_t ld, int fmt,
                                              void *h_bf16, int64_t ld_h, uint8_t *q, int64_t ld_q, uint8_t *s,
