@@ -25,7 +25,6 @@ allocate the outputs with torch and call the entry points above.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -169,20 +168,19 @@ def load_library():
     return _lib
 
 
+# Addresses go to ctypes as plain integers (its c_void_p arguments take them);
+# a c_void_p object around each costs a small call microseconds in all.
 def _p(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return ctypes.c_void_p(t)
-    return ctypes.c_void_p(t.data_ptr())
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        # the handle alone: torch.cuda.current_stream() builds a Stream object around it (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _check(status: int, where: str):
@@ -651,17 +649,13 @@ def blockwise_quantize(x: torch.Tensor, fmt: int, block_rows: int, layouts: int 
 
 # --- norms, SwiGLU backward and 8-bit checkpoints -------------------------------
 
-def _require(ok, where: str, detail: str):
-    if not ok:
-        raise Fp8Error(1, where, detail)
+def _refuse(where: str, detail: str):
+    raise Fp8Error(1, where, detail)
 
 
-def _alloc_on(stream):
-    """Context in which torch allocates for `stream`: what is allocated there
-    is reused in that stream's order, so a workspace dropped at return is safe
-    while the launch is still running."""
-    if stream is None:
-        return contextlib.nullcontext()
+def _on(stream):
+    """Context that makes `stream` current: torch then allocates for it, and
+    what is dropped at return (a workspace) is reused in that stream's order."""
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
@@ -669,20 +663,24 @@ def _alloc_on(stream):
 
 def _matrix(t: torch.Tensor, where: str, name: str, rows=None, cols=None, dtype=None) -> int:
     """Check a CUDA matrix; returns its row stride."""
-    _require(t.is_cuda and t.dim() == 2, where, f"{name} must be a CUDA matrix")
-    _require(t.dtype in DTYPES if dtype is None else t.dtype == dtype, where, f"{name} has type {t.dtype}")
+    if not t.is_cuda or t.dim() != 2:
+        _refuse(where, f"{name} must be a CUDA matrix")
+    if t.dtype not in DTYPES if dtype is None else t.dtype != dtype:
+        _refuse(where, f"{name} has type {t.dtype}")
     n, c = t.shape
-    _require((rows is None or n == rows) and (cols is None or c == cols), where,
-             f"{name} is {n} x {c}, not {rows} x {cols}")
-    _require(c > 0 and (c == 1 or t.stride(1) == 1), where, f"{name} must have consecutive columns")
-    return t.stride(0) if n > 1 else max(c, t.stride(0))
+    if (rows is not None and n != rows) or (cols is not None and c != cols):
+        _refuse(where, f"{name} is {n} x {c}, not {rows} x {cols}")
+    ld, col = t.stride()
+    if c == 0 or (col != 1 and c > 1):
+        _refuse(where, f"{name} must have consecutive columns")
+    return ld if n > 1 else max(c, ld)
 
 
 def _vector(t, where: str, name: str, n: int, dtype=None):
-    if t is not None:
-        _require(t.is_cuda and t.dim() == 1 and t.numel() == n and t.is_contiguous(), where,
-                 f"{name} must be a contiguous CUDA vector of {n} elements")
-        _require(t.dtype in DTYPES if dtype is None else t.dtype == dtype, where, f"{name} has type {t.dtype}")
+    if not t.is_cuda or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        _refuse(where, f"{name} must be a contiguous CUDA vector of {n} elements")
+    if t.dtype not in DTYPES if dtype is None else t.dtype != dtype:
+        _refuse(where, f"{name} has type {t.dtype}")
 
 
 @dataclass
@@ -702,59 +700,76 @@ class Checkpoint:
         return self.q.shape[0]
 
 
-def _checkpoint_buffers(rows, cols, parts, dev, fmt) -> Checkpoint:
-    w = (cols + MX_BLOCK - 1) // MX_BLOCK * MX_BLOCK * parts
-    return Checkpoint(torch.empty((rows, w), dtype=torch.uint8, device=dev),
-                      torch.empty((rows, w // MX_BLOCK), dtype=torch.uint8, device=dev), fmt, cols, parts)
+def _blocks(cols: int) -> int:
+    return (cols + MX_BLOCK - 1) // MX_BLOCK
+
+
+def _new_checkpoint(rows, cols, parts, dev, fmt) -> Checkpoint:
+    nb = _blocks(cols) * parts
+    return Checkpoint(torch.empty((rows, nb * MX_BLOCK), dtype=torch.uint8, device=dev),
+                      torch.empty((rows, nb), dtype=torch.uint8, device=dev), fmt, cols, parts)
 
 
 def _checkpoint_strides(c: Checkpoint, where: str, rows=None, cols=None, parts=None):
-    _require((rows is None or c.rows == rows) and (cols is None or c.cols == cols) and
-             (parts is None or c.parts == parts), where,
-             f"the checkpoint holds {c.rows} x {c.parts} x {c.cols}, not {rows} x {parts} x {cols}")
-    w = (c.cols + MX_BLOCK - 1) // MX_BLOCK * MX_BLOCK * c.parts
-    return (_matrix(c.q, where, "checkpoint codes", c.rows, w, torch.uint8),
-            _matrix(c.s, where, "checkpoint scales", c.rows, w // MX_BLOCK, torch.uint8))
+    n = c.q.shape[0]
+    if (rows is not None and n != rows) or (cols is not None and c.cols != cols) or \
+            (parts is not None and c.parts != parts):
+        _refuse(where, f"the checkpoint holds {n} x {c.parts} x {c.cols}, not {rows} x {parts} x {cols}")
+    nb = _blocks(c.cols) * c.parts
+    return (_matrix(c.q, where, "checkpoint codes", n, nb * MX_BLOCK, torch.uint8),
+            _matrix(c.s, where, "checkpoint scales", n, nb, torch.uint8))
 
 
 def checkpoint(x: torch.Tensor, fmt: int = E4M3FN, parts: int = 1, stream=None) -> Checkpoint:
     """Keep a [rows, parts * cols] bf16 / fp16 / fp32 activation in 8 bits."""
+    if stream is not None:
+        with _on(stream):
+            return checkpoint(x, fmt, parts)
     where = "checkpoint"
     ld = _matrix(x, where, "x")
     rows, total = x.shape
-    _require(parts >= 1 and total % parts == 0, where, f"{total} columns are not {parts} equal parts")
-    with _alloc_on(stream):
-        c = _checkpoint_buffers(rows, total // parts, parts, x.device, fmt)
-    fp8_checkpoint(x, DTYPES[x.dtype], rows, c.cols, ld, parts, fmt, c.q, c.q.shape[1], c.s, c.s.shape[1], stream)
+    if parts < 1 or total % parts:
+        _refuse(where, f"{total} columns are not {parts} equal parts")
+    c = _new_checkpoint(rows, total // parts, parts, x.device, fmt)
+    fp8_checkpoint(x, DTYPES[x.dtype], rows, c.cols, ld, parts, fmt, c.q, c.q.shape[1], c.s, c.s.shape[1])
     return c
 
 
 def checkpoint_restore(c: Checkpoint, dtype: torch.dtype = torch.bfloat16, out=None, stream=None) -> torch.Tensor:
     """The [rows, parts * cols] activation a checkpoint stands for."""
+    if stream is not None:
+        with _on(stream):
+            return checkpoint_restore(c, dtype, out)
     where = "checkpoint_restore"
     ld_q, ld_s = _checkpoint_strides(c, where)
+    rows = c.q.shape[0]
     if out is None:
-        _require(dtype in DTYPES, where, f"cannot restore to {dtype}")
-        with _alloc_on(stream):
-            out = torch.empty((c.rows, c.parts * c.cols), dtype=dtype, device=c.q.device)
-    ld = _matrix(out, where, "out", c.rows, c.parts * c.cols)
-    fp8_checkpoint_restore(c.q, ld_q, c.s, ld_s, c.fmt, c.rows, c.cols, c.parts, out, DTYPES[out.dtype], ld, stream)
+        if dtype not in DTYPES:
+            _refuse(where, f"cannot restore to {dtype}")
+        out = torch.empty((rows, c.parts * c.cols), dtype=dtype, device=c.q.device)
+    ld = _matrix(out, where, "out", rows, c.parts * c.cols)
+    fp8_checkpoint_restore(c.q, ld_q, c.s, ld_s, c.fmt, rows, c.cols, c.parts, out, DTYPES[out.dtype], ld)
     return out
 
 
 def swiglu_checkpoint(gate_up: torch.Tensor, fmt: int = E4M3FN, h_out=None, stream=None):
     """h = bf16(silu(gate) * up) of a bf16 [rows, 2F] gate|up tensor, and its
     2-part 8-bit checkpoint, from one read.  Returns (h, checkpoint)."""
+    if stream is not None:
+        with _on(stream):
+            return swiglu_checkpoint(gate_up, fmt, h_out)
     where = "swiglu_checkpoint"
     ld = _matrix(gate_up, where, "gate_up", dtype=torch.bfloat16)
     rows, total = gate_up.shape
-    _require(total % 2 == 0, where, "gate_up must have an even number of columns")
+    if total % 2:
+        _refuse(where, "gate_up must have an even number of columns")
     F = total // 2
-    with _alloc_on(stream):
-        h = torch.empty((rows, F), dtype=torch.bfloat16, device=gate_up.device) if h_out is None else h_out
-        c = _checkpoint_buffers(rows, F, 2, gate_up.device, fmt)
-    ld_h = _matrix(h, where, "h_out", rows, F, torch.bfloat16)
-    fp8_swiglu_checkpoint(gate_up, rows, F, ld, fmt, h, ld_h, c.q, c.q.shape[1], c.s, c.s.shape[1], stream)
+    if h_out is None:
+        h, ld_h = torch.empty((rows, F), dtype=torch.bfloat16, device=gate_up.device), F
+    else:
+        h, ld_h = h_out, _matrix(h_out, where, "h_out", rows, F, torch.bfloat16)
+    c = _new_checkpoint(rows, F, 2, gate_up.device, fmt)
+    fp8_swiglu_checkpoint(gate_up, rows, F, ld, fmt, h, ld_h, c.q, c.q.shape[1], c.s, c.s.shape[1])
     return h, c
 
 
@@ -762,22 +777,27 @@ def swiglu_backward(dh: torch.Tensor, src, out=None, return_h: bool = False, str
     """Gradient of gate|up from dh (bf16 [rows, F]) and src: the bf16
     [rows, 2F] gate|up tensor or its checkpoint.  With return_h also
     h = bf16(silu(gate) * up) of what src holds: (d_gate_up, h)."""
+    if stream is not None:
+        with _on(stream):
+            return swiglu_backward(dh, src, out, return_h)
     where = "swiglu_backward"
     ld_dh = _matrix(dh, where, "dh", dtype=torch.bfloat16)
     rows, F = dh.shape
-    gate_up = q = s = None
+    gate_up = q = s = h = None
     ld = ld_q = ld_s = fmt = 0
     if isinstance(src, Checkpoint):
         ld_q, ld_s = _checkpoint_strides(src, where, rows, F, 2)
         q, s, fmt = src.q, src.s, src.fmt
     else:
         gate_up, ld = src, _matrix(src, where, "gate_up", rows, 2 * F, torch.bfloat16)
-    with _alloc_on(stream):
-        d = torch.empty((rows, 2 * F), dtype=torch.bfloat16, device=dh.device) if out is None else out
-        h = torch.empty((rows, F), dtype=torch.bfloat16, device=dh.device) if return_h else None
-    ld_d = _matrix(d, where, "out", rows, 2 * F, torch.bfloat16)
-    fp8_swiglu_backward(dh, ld_dh, gate_up, ld, q, ld_q, s, ld_s, fmt, rows, F, d, ld_d, h, F, stream)
-    return (d, h) if return_h else d
+    if out is None:
+        out, ld_d = torch.empty((rows, 2 * F), dtype=torch.bfloat16, device=dh.device), 2 * F
+    else:
+        ld_d = _matrix(out, where, "out", rows, 2 * F, torch.bfloat16)
+    if return_h:
+        h = torch.empty((rows, F), dtype=torch.bfloat16, device=dh.device)
+    fp8_swiglu_backward(dh, ld_dh, gate_up, ld, q, ld_q, s, ld_s, fmt, rows, F, out, ld_d, h, F)
+    return (out, h) if return_h else out
 
 
 @dataclass
@@ -801,24 +821,38 @@ def norm_forward(x: torch.Tensor, weight=None, bias=None, kind: int = LAYER_NORM
     y = xhat * weight + bias, in x's type or, for an fp32 x, out_dtype.  With
     checkpoint_fmt (E4M3FN or E5M2) xhat is kept in 8 bits for norm_backward,
     which then needs neither x nor the mean."""
+    if stream is not None:
+        with _on(stream):
+            return norm_forward(x, weight, bias, kind, eps, out_dtype, checkpoint_fmt, out)
     where = "norm_forward"
     ld = _matrix(x, where, "x")
     rows, cols = x.shape
-    _vector(weight, where, "weight", cols)
-    _vector(bias, where, "bias", cols, None if weight is None else weight.dtype)
-    w = weight if weight is not None else bias
-    out_dtype = out.dtype if out is not None else out_dtype or x.dtype
-    _require(out_dtype in DTYPES, where, f"cannot write {out_dtype}")
-    with _alloc_on(stream):
-        y = torch.empty((rows, cols), dtype=out_dtype, device=x.device) if out is None else out
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device) if kind == LAYER_NORM else None
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-        c = _checkpoint_buffers(rows, cols, 1, x.device, checkpoint_fmt) if checkpoint_fmt is not None else None
-    ld_y = _matrix(y, where, "out", rows, cols)
-    q, s, ld_q, ld_s, fmt = (c.q, c.s, c.q.shape[1], c.s.shape[1], c.fmt) if c else (None, None, 0, 0, 0)
-    fp8_norm_forward(x, DTYPES[x.dtype], ld, rows, cols, kind, eps, weight, bias, 0 if w is None else DTYPES[w.dtype],
-                     y, DTYPES[out_dtype], ld_y, mean, rstd, fmt, q, ld_q, s, ld_s, stream)
-    return NormForward(y, mean, rstd, c)
+    dev = x.device
+    w_dtype = 0
+    if weight is not None:
+        _vector(weight, where, "weight", cols)
+        w_dtype = DTYPES[weight.dtype]
+    if bias is not None:
+        _vector(bias, where, "bias", cols, None if weight is None else weight.dtype)
+        w_dtype = DTYPES[bias.dtype]
+    if out is None:
+        out_dtype = out_dtype or x.dtype
+        if out_dtype not in DTYPES:
+            _refuse(where, f"cannot write {out_dtype}")
+        out, ld_y = torch.empty((rows, cols), dtype=out_dtype, device=dev), cols
+    else:
+        ld_y = _matrix(out, where, "out", rows, cols)
+        out_dtype = out.dtype
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if kind == LAYER_NORM else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    c = q = s = None
+    nb = fmt = 0
+    if checkpoint_fmt is not None:
+        c = _new_checkpoint(rows, cols, 1, dev, checkpoint_fmt)
+        q, s, fmt, nb = c.q, c.s, checkpoint_fmt, _blocks(cols)
+    fp8_norm_forward(x, DTYPES[x.dtype], ld, rows, cols, kind, eps, weight, bias, w_dtype, out, DTYPES[out_dtype], ld_y,
+                     mean, rstd, fmt, q, nb * MX_BLOCK, s, nb)
+    return NormForward(out, mean, rstd, c)
 
 
 def norm_backward(dy: torch.Tensor, src, mean, rstd: torch.Tensor, weight=None, kind: int = LAYER_NORM, dx_dtype=None,
@@ -828,35 +862,46 @@ def norm_backward(dy: torch.Tensor, src, mean, rstd: torch.Tensor, weight=None, 
     the weight's type (fp32 without a weight); bias_grad defaults to whether
     the norm is a layer norm.  dx has x's type; from a checkpoint, dx_dtype,
     by default dy's type."""
+    if stream is not None:
+        with _on(stream):
+            return norm_backward(dy, src, mean, rstd, weight, kind, dx_dtype, weight_grad, bias_grad, out)
     where = "norm_backward"
     ld_dy = _matrix(dy, where, "dy")
     rows, cols = dy.shape
+    dev = dy.device
     _vector(rstd, where, "rstd", rows, torch.float32)
-    _vector(mean, where, "mean", rows, torch.float32)
-    _vector(weight, where, "weight", cols)
+    if mean is not None:
+        _vector(mean, where, "mean", rows, torch.float32)
+    w_dtype = torch.float32
+    if weight is not None:
+        _vector(weight, where, "weight", cols)
+        w_dtype = weight.dtype
     x = q = s = None
     ld_x = ld_q = ld_s = fmt = 0
     if isinstance(src, Checkpoint):
         ld_q, ld_s = _checkpoint_strides(src, where, rows, cols, 1)
         q, s, fmt = src.q, src.s, src.fmt
         dx_dtype = dx_dtype or (dy.dtype if out is None else out.dtype)
+        if dx_dtype not in DTYPES:
+            _refuse(where, f"cannot write {dx_dtype}")
     else:
         x, ld_x = src, _matrix(src, where, "x", rows, cols)
-        _require(dx_dtype is None or dx_dtype == x.dtype, where, f"dx of a {x.dtype} x cannot be {dx_dtype}")
-        _require(kind != LAYER_NORM or mean is not None, where, "a layer norm's backward from x needs its mean")
+        if dx_dtype is not None and dx_dtype != x.dtype:
+            _refuse(where, f"dx of a {x.dtype} x cannot be {dx_dtype}")
+        if kind == LAYER_NORM and mean is None:
+            _refuse(where, "a layer norm's backward from x needs its mean")
         dx_dtype = x.dtype
-    _require(dx_dtype in DTYPES, where, f"cannot write {dx_dtype}")
-    bias_grad = kind == LAYER_NORM if bias_grad is None else bias_grad
-    w_dtype = torch.float32 if weight is None else weight.dtype
-    with _alloc_on(stream):
-        dx = torch.empty((rows, cols), dtype=dx_dtype, device=dy.device) if out is None else out
-        dw = torch.empty(cols, dtype=w_dtype, device=dy.device) if weight_grad else None
-        db = torch.empty(cols, dtype=w_dtype, device=dy.device) if bias_grad else None
-        ws, n = None, 0
-        if weight_grad or bias_grad:
-            n = fp8_norm_workspace_bytes(rows, cols)
-            ws = torch.empty(n, dtype=torch.uint8, device=dy.device)
-    ld_dx = _matrix(dx, where, "out", rows, cols, dx_dtype)
+    if out is None:
+        out, ld_dx = torch.empty((rows, cols), dtype=dx_dtype, device=dev), cols
+    else:
+        ld_dx = _matrix(out, where, "out", rows, cols, dx_dtype)
+    dw = torch.empty(cols, dtype=w_dtype, device=dev) if weight_grad else None
+    db = torch.empty(cols, dtype=w_dtype, device=dev) \
+        if (kind == LAYER_NORM if bias_grad is None else bias_grad) else None
+    ws, n = None, 0
+    if dw is not None or db is not None:
+        n = fp8_norm_workspace_bytes(rows, cols)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
     fp8_norm_backward(dy, DTYPES[dy.dtype], ld_dy, x, ld_x, q, ld_q, s, ld_s, fmt, rows, cols, kind, mean, rstd,
-                      weight, DTYPES[w_dtype], dx, DTYPES[dx_dtype], ld_dx, dw, db, ws, n, stream)
-    return NormBackward(dx, dw, db)
+                      weight, DTYPES[w_dtype], out, DTYPES[dx_dtype], ld_dx, dw, db, ws, n)
+    return NormBackward(out, dw, db)

@@ -137,8 +137,8 @@ __device__ __forceinline__ void st_32b(void *p, const uint4 &lo, const uint4 &hi
 }
 
 // Elements 0 .. n-1 from p (n >= 16: all of them by wide loads), zeros after.
-template <typename T>
-__device__ __forceinline__ void load16(const T *p, int64_t n, bool w32, Raw16<T> &r)
+template <typename T, typename N>
+__device__ __forceinline__ void load16(const T *p, N n, bool w32, Raw16<T> &r)
 {
     if (n >= 16) {
         if (w32) {
@@ -209,8 +209,8 @@ __device__ __forceinline__ void unpack16(const Raw16<T> &r, float (&f)[16])
 }
 
 // Elements 0 .. n-1 to p.
-template <typename T>
-__device__ __forceinline__ void store16(T *p, const float (&f)[16], int64_t n, bool w32)
+template <typename T, typename N>
+__device__ __forceinline__ void store16(T *p, const float (&f)[16], N n, bool w32)
 {
     if (n >= 16) {
         uint4 v[sizeof(T)];

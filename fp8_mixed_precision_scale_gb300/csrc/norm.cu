@@ -12,10 +12,22 @@
 // keeps xh, not x: its 8 bits then resolve xh itself however large the mean
 // is against the spread, and the backward needs no mean.
 //
-// The row kernels give a block one row at a time and sweep it once per sum
-// (the later sweeps hit L1/L2); dw and db are column sums over row slices
-// into the caller's workspace, added in a fixed order by a second kernel: no
-// atomics, the same bits every time.
+// Wide form (16-byte aligned rows and parameters, limited widths): a row stays
+// in the registers of its group of threads, 16 consecutive columns (a chunk) per
+// thread and step; the group is a part of a warp or several warps with a named
+// barrier of their own.  One persistent block per SM holds as many groups as
+// its registers allow and one fp32 copy of the parameters in shared memory.
+// A group issues the loads of its next row before it reduces the current one.
+// The backward accumulates dw and db of its columns in registers over all its
+// rows; wider rows (more columns than NM_MAX_FUSED) take a second read of dy
+// and x by columns instead.
+//
+// Narrow form (anything else): a block takes one row at a time and sweeps it
+// once per sum (the later sweeps hit L1/L2).
+//
+// dw and db are left as column sums over row slices in the caller's workspace
+// and added in a fixed order by a last kernel: no atomics, the same bits every
+// time.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -30,6 +42,12 @@ constexpr int NM_THREADS = 256;
 constexpr int NM_WARPS = NM_THREADS / 32;
 constexpr int NM_COLS = 32;   // columns of a column-sum block
 constexpr int NM_LANES = NM_THREADS / NM_COLS;  // its row lanes
+
+constexpr int NM_BLOCK = 512;          // threads of a wide block at most: 128 registers each
+constexpr int NM_MAX_GROUPS = 15;      // row groups with a named barrier each
+constexpr int NM_GROUP_WARPS = 16;     // warps of a row group at most
+constexpr int NM_MAX_WIDE = 2 * 16 * 32 * NM_GROUP_WARPS;  // columns of two chunks a thread
+constexpr int NM_MAX_FUSED = 16 * 32 * NM_GROUP_WARPS;     // of one
 
 struct NormArgs {
     const void *x, *dy;  // x: forward input; backward: NULL when the checkpoint is read
@@ -49,6 +67,9 @@ struct NormArgs {
     float *part;  // [splits][2][cols] dw and db sums of row slices
     int splits;
     void *dweight, *dbias;
+    // wide forms
+    int G;    // threads of a row group
+    int w32;  // every row of the tensors starts on a 32-byte boundary
 };
 
 // Element i of a parameter vector; NULL gives `absent`.
@@ -87,6 +108,445 @@ __device__ __forceinline__ float2 block_sum(float a, float b)
         t.y += part[w].y;
     }
     return t;
+}
+
+// Parameters c .. c + 15 (p 16-byte aligned), `absent` past the row.
+__device__ __forceinline__ void param16(const void *p, int dtype, int c, int cols, float absent, float (&f)[16])
+{
+    if (!p || c + 16 > cols) {
+#pragma unroll
+        for (int j = 0; j < 16; j++) f[j] = c + j < cols ? param(p, dtype, c + j, absent) : absent;
+    } else if (dtype == FP8_DTYPE_F32) {
+        Raw16<float> r;
+        load16(static_cast<const float *>(p) + c, 16, false, r);
+        unpack16(r, f);
+    } else if (dtype == FP8_DTYPE_F16) {
+        Raw16<__half> r;
+        load16(static_cast<const __half *>(p) + c, 16, false, r);
+        unpack16(r, f);
+    } else {
+        Raw16<__nv_bfloat16> r;
+        load16(static_cast<const __nv_bfloat16 *>(p) + c, 16, false, r);
+        unpack16(r, f);
+    }
+}
+
+// A parameter vector in shared memory as fp32, in the order the row threads
+// read it: quad q of chunk i is at quad q * chunks + i, so the 16-byte reads of
+// a warp are consecutive.
+__device__ __forceinline__ void params_to_shared(float *dst, const void *p, int dtype, int cols, int chunks,
+                                                 float absent)
+{
+    for (int i = threadIdx.x; i < chunks; i += blockDim.x) {
+        float f[16];
+        param16(p, dtype, i * 16, cols, absent, f);
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            reinterpret_cast<float4 *>(dst)[q * chunks + i] =
+                make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+    }
+}
+
+__device__ __forceinline__ float4 param4(const float *src, int chunks, int i, int q)
+{
+    return reinterpret_cast<const float4 *>(src)[q * chunks + i];
+}
+
+// Where a thread of a wide kernel stands: its row group in the block, its place
+// in the group, and the group's shared slots for the sums.
+struct Group {
+    int id, t;
+    float2 *part;  // [2][NM_GROUP_WARPS], zero beyond the group's warps
+};
+
+template <bool MULTI>
+__device__ __forceinline__ Group group_of(int G, float2 *parts)
+{
+    Group g;
+    if constexpr (MULTI) {
+        g.id = threadIdx.x / G;
+        g.t = threadIdx.x - g.id * G;
+    } else {  // G is a power of two
+        g.id = threadIdx.x >> (31 - __clz(G));
+        g.t = threadIdx.x & (G - 1);
+    }
+    g.part = parts + g.id * 2 * NM_GROUP_WARPS;
+    return g;
+}
+
+// Sum of a pair over the threads of a row group; every thread gets the same
+// bits.  MULTI: through slot `slot` of the group's shared sums, one group
+// barrier; two uses in a row take different slots.
+template <bool MULTI>
+__device__ __forceinline__ float2 row_sum(float2 v, int G, const Group &g, int slot)
+{
+    if constexpr (!MULTI) {
+        for (int d = G >> 1; d > 0; d >>= 1)
+            v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d)));
+        return v;
+    } else {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d)));
+        float2 *part = g.part + slot * NM_GROUP_WARPS;
+        if ((g.t & 31) == 0) part[g.t >> 5] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(G) : "memory");
+        v = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < NM_GROUP_WARPS; w += 2) {
+            const float4 q = reinterpret_cast<const float4 *>(part)[w >> 1];
+            v = add2(v, add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+        }
+        return v;
+    }
+}
+
+template <bool MULTI>
+__device__ __forceinline__ float row_sum(float v, int G, const Group &g, int slot)
+{
+    if constexpr (!MULTI) {
+        for (int d = G >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        return v;
+    } else {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        float *part = reinterpret_cast<float *>(g.part + slot * NM_GROUP_WARPS);
+        if ((g.t & 31) == 0) part[g.t >> 5] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(G) : "memory");
+        float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < NM_GROUP_WARPS; w += 4) {  // all slots: a loop over the group's own took 25 % longer
+            const float4 q = reinterpret_cast<const float4 *>(part)[w >> 2];
+            s = add2(s, add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+        }
+        return s.x + s.y;
+    }
+}
+
+__device__ __forceinline__ float sum16(const float (&f)[16])
+{
+    float2 t[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        t[j] = add2(make_float2(f[4 * j], f[4 * j + 1]), make_float2(f[4 * j + 2], f[4 * j + 3]));
+    const float2 s = add2(add2(t[0], t[1]), add2(t[2], t[3]));
+    return s.x + s.y;
+}
+
+// A row in the registers of its group: thread t of G holds columns (k G + t) 16
+// .. + 15 for k < CH.
+template <typename TX, typename TY, int CH, bool MULTI>
+__global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
+{
+    extern __shared__ __align__(16) float shared[];  // weight, bias
+    __shared__ __align__(16) float2 parts[MULTI ? NM_MAX_GROUPS * 2 * NM_GROUP_WARPS : 1];
+    const int cols = (int)a.cols, G = a.G, chunks = CH * G;
+    const Group g = group_of<MULTI>(G, parts);
+    const int groups = MULTI ? blockDim.x / G : blockDim.x >> (31 - __clz(G));
+    const int64_t step = (int64_t)gridDim.x * groups;
+    const float inv_n = 1.0f / (float)cols;
+    int n[CH];  // columns of the row in each chunk, from 16 down to 0
+#pragma unroll
+    for (int k = 0; k < CH; k++) n[k] = max(0, min(16, cols - (k * G + g.t) * 16));
+
+    // the threads of a group (of a warp, where it holds several) run the same
+    // iterations: `first` is the row of the first group among them
+    int64_t r = (int64_t)blockIdx.x * groups + g.id;
+    int64_t first = MULTI ? r : r - (threadIdx.x & 31) / G;
+    const TX *x = static_cast<const TX *>(a.x) + r * a.ld_x + g.t * 16;
+    TY *y = static_cast<TY *>(a.out) + r * a.ld_out + g.t * 16;
+    Raw16<TX> raw[CH];
+#pragma unroll
+    for (int k = 0; k < CH; k++) load16(x + k * G * 16, r < a.rows ? n[k] : 0, a.w32, raw[k]);
+    params_to_shared(shared, a.weight, a.w_dtype, cols, chunks, 1.0f);
+    if (a.bias) params_to_shared(shared + chunks * 16, a.bias, a.w_dtype, cols, chunks, 0.0f);
+    if (MULTI)
+        for (int i = threadIdx.x; i < NM_MAX_GROUPS * 2 * NM_GROUP_WARPS; i += blockDim.x)
+            parts[i] = make_float2(0.0f, 0.0f);
+    __syncthreads();
+
+    int slot = 0;
+    for (; first < a.rows; first += step, r += step) {
+        float f[CH][16];
+        float v = 0.0f;
+        x += step * a.ld_x;
+#pragma unroll
+        for (int k = 0; k < CH; k++) {
+            unpack16(raw[k], f[k]);
+            v += sum16(f[k]);
+            if (r + step < a.rows) load16(x + k * G * 16, n[k], a.w32, raw[k]);
+        }
+        float mean = 0.0f;
+        if (!a.rms) {
+            mean = row_sum<MULTI>(v, G, g, slot) * inv_n;
+            slot ^= 1;
+        }
+        v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < CH; k++) {
+            float2 acc[2] = {};
+            if (n[k] < 16) {  // columns past the row are as far from the mean as the mean is
+#pragma unroll
+                for (int j = 0; j < 16; j++) f[k][j] = j < n[k] ? f[k][j] : mean;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                const float2 d = add2(make_float2(f[k][j], f[k][j + 1]), make_float2(-mean, -mean));
+                acc[j / 2 % 2] = fma2(d, d, acc[j / 2 % 2]);
+                f[k][j] = d.x, f[k][j + 1] = d.y;
+            }
+            v += (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<MULTI>(v, G, g, slot) * inv_n + a.eps);
+        slot ^= 1;
+        const bool live = r < a.rows;
+        if (g.t == 0 && live) {
+            if (a.mean_out) a.mean_out[r] = mean;
+            if (a.rstd_out) a.rstd_out[r] = rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < CH; k++) {
+            const int i = k * G + g.t;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                const float2 d = mul2(make_float2(f[k][j], f[k][j + 1]), make_float2(rstd, rstd));
+                f[k][j] = d.x, f[k][j + 1] = d.y;
+            }
+            if (a.q) {
+                const uint32_t code = ckpt_code(block_amax16(f[k]), a.fmt);
+                if (live && (i & ~1) * 16 < cols) {
+                    const float inv = ckpt_inv_scale(code);
+                    *reinterpret_cast<uint4 *>(a.q + r * a.ld_q + i * 16) =
+                        a.fmt == FP8_E5M2 ? encode16<FP8_E5M2>(f[k], inv) : encode16<FP8_E4M3FN>(f[k], inv);
+                    if (!(i & 1)) a.s[r * a.ld_s + (i >> 1)] = (uint8_t)code;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const float4 w = param4(shared, chunks, i, q);
+                float2 lo = make_float2(f[k][4 * q], f[k][4 * q + 1]), hi = make_float2(f[k][4 * q + 2], f[k][4 * q + 3]);
+                if (a.bias) {
+                    const float4 b = param4(shared + chunks * 16, chunks, i, q);
+                    lo = fma2(lo, make_float2(w.x, w.y), make_float2(b.x, b.y));
+                    hi = fma2(hi, make_float2(w.z, w.w), make_float2(b.z, b.w));
+                } else {
+                    lo = mul2(lo, make_float2(w.x, w.y));
+                    hi = mul2(hi, make_float2(w.z, w.w));
+                }
+                f[k][4 * q] = lo.x, f[k][4 * q + 1] = lo.y, f[k][4 * q + 2] = hi.x, f[k][4 * q + 3] = hi.y;
+            }
+            store16(y + k * G * 16, f[k], live ? n[k] : 0, a.w32);
+        }
+        y += step * a.ld_out;
+    }
+}
+
+// What a thread reads of a row in the backward: dy, and x or its checkpoint.
+template <typename TX, typename TY, bool CKPT>
+struct RawBackward {
+    Raw16<TY> dy;
+    Raw16<TX> x;
+    uint4 q;
+    uint32_t s;
+};
+
+template <typename TX, typename TY>
+struct RawBackward<TX, TY, true> {
+    Raw16<TY> dy;
+    uint4 q;
+    uint32_t s;
+};
+
+// Chunk i (n columns of it) of row r.
+template <typename TX, typename TY, bool CKPT>
+__device__ __forceinline__ void load_backward(const NormArgs &a, int64_t r, int i, int n, RawBackward<TX, TY, CKPT> &v)
+{
+    load16(static_cast<const TY *>(a.dy) + r * a.ld_dy + i * 16, n, a.w32, v.dy);
+    if constexpr (CKPT) {
+        v.q = make_uint4(0, 0, 0, 0);
+        v.s = 127;
+        if (n > 0) {
+            v.q = ld_stream_16b(a.q + r * a.ld_q + i * 16);
+            v.s = __ldg(a.s + r * a.ld_s + (i >> 1));
+        }
+    } else {
+        load16(static_cast<const TX *>(a.x) + r * a.ld_x + i * 16, n, a.w32, v.x);
+    }
+}
+
+// xh of a chunk; 0 past the row.
+template <typename TX, typename TY, bool CKPT>
+__device__ __forceinline__ void xhat16(const NormArgs &a, const RawBackward<TX, TY, CKPT> &v, int n, float mean,
+                                       float rstd, float (&xh)[16])
+{
+    if constexpr (CKPT) {
+        if (a.fmt == FP8_E5M2) decode16<FP8_E5M2>(v.q, ckpt_scale(v.s), xh);
+        else decode16<FP8_E4M3FN>(v.q, ckpt_scale(v.s), xh);
+    } else {
+        unpack16(v.x, xh);
+        if (n < 16) {
+#pragma unroll
+            for (int j = 0; j < 16; j++) xh[j] = j < n ? xh[j] : mean;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const float2 d = mul2(add2(make_float2(xh[j], xh[j + 1]), make_float2(-mean, -mean)),
+                                  make_float2(rstd, rstd));
+            xh[j] = d.x, xh[j + 1] = d.y;
+        }
+    }
+}
+
+// dx of whole rows; with ACC also this block's share of dw and db, in
+// registers until the last row and then added over the block's groups in
+// shared memory (in group order) into the block's slice of the workspace.
+template <typename TX, typename TY, int CH, bool MULTI, bool CKPT, bool ACC>
+__global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a)
+{
+    extern __shared__ __align__(16) float shared[];  // weight; at the end dw and db
+    __shared__ __align__(16) float2 parts[MULTI ? NM_MAX_GROUPS * 2 * NM_GROUP_WARPS : 1];
+    const int cols = (int)a.cols, G = a.G, chunks = CH * G;
+    const Group g = group_of<MULTI>(G, parts);
+    const int groups = MULTI ? blockDim.x / G : blockDim.x >> (31 - __clz(G));
+    const int64_t step = (int64_t)gridDim.x * groups;
+    const float inv_n = 1.0f / (float)cols;
+    int n[CH];
+#pragma unroll
+    for (int k = 0; k < CH; k++) n[k] = max(0, min(16, cols - (k * G + g.t) * 16));
+
+    int64_t r = (int64_t)blockIdx.x * groups + g.id;
+    int64_t first = MULTI ? r : r - (threadIdx.x & 31) / G;
+    RawBackward<TX, TY, CKPT> raw[CH];
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    const auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < CH; k++) load_backward(a, row, k * G + g.t, row < a.rows ? n[k] : 0, raw[k]);
+        if (row < a.rows) {
+            next_rstd = __ldg(a.rstd + row);
+            if (!CKPT && !a.rms) next_mean = __ldg(a.mean + row);
+        }
+    };
+    fetch(r);
+    params_to_shared(shared, a.weight, a.w_dtype, cols, chunks, 1.0f);
+    if (MULTI)
+        for (int i = threadIdx.x; i < NM_MAX_GROUPS * 2 * NM_GROUP_WARPS; i += blockDim.x)
+            parts[i] = make_float2(0.0f, 0.0f);
+    __syncthreads();
+
+    float2 dw[ACC ? CH : 1][8] = {}, db[ACC ? CH : 1][8] = {};
+    int slot = 0;
+    for (; first < a.rows; first += step, r += step) {
+        float gr[CH][16], xh[CH][16];
+        float2 sum = make_float2(0.0f, 0.0f);
+        const float rstd = next_rstd;
+#pragma unroll
+        for (int k = 0; k < CH; k++) {
+            unpack16(raw[k].dy, gr[k]);
+            xhat16(a, raw[k], n[k], next_mean, rstd, xh[k]);
+        }
+        if (first + step < a.rows) fetch(r + step);
+#pragma unroll
+        for (int k = 0; k < CH; k++) {
+            float2 s1[2] = {}, s2[2] = {};
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const float4 w = param4(shared, chunks, k * G + g.t, q);
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int j = 4 * q + 2 * h;
+                    const float2 d = make_float2(gr[k][j], gr[k][j + 1]), x2 = make_float2(xh[k][j], xh[k][j + 1]);
+                    if constexpr (ACC) {
+                        dw[k][j / 2] = fma2(d, x2, dw[k][j / 2]);
+                        db[k][j / 2] = add2(db[k][j / 2], d);
+                    }
+                    const float2 p = mul2(d, h ? make_float2(w.z, w.w) : make_float2(w.x, w.y));
+                    s1[h] = add2(s1[h], p);
+                    s2[h] = fma2(p, x2, s2[h]);
+                    gr[k][j] = p.x, gr[k][j + 1] = p.y;
+                }
+            }
+            s1[0] = add2(s1[0], s1[1]);
+            s2[0] = add2(s2[0], s2[1]);
+            sum = add2(sum, make_float2(s1[0].x + s1[0].y, s2[0].x + s2[0].y));
+        }
+        sum = row_sum<MULTI>(sum, G, g, slot);
+        slot ^= 1;
+        const float c1 = a.rms ? 0.0f : -sum.x * inv_n * rstd, c2 = -sum.y * inv_n * rstd;
+        TX *dx = static_cast<TX *>(a.out) + r * a.ld_out;
+#pragma unroll
+        for (int k = 0; k < CH; k++) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                float2 o = fma2(make_float2(gr[k][j], gr[k][j + 1]), make_float2(rstd, rstd), make_float2(c1, c1));
+                o = fma2(make_float2(xh[k][j], xh[k][j + 1]), make_float2(c2, c2), o);
+                gr[k][j] = o.x, gr[k][j + 1] = o.y;
+            }
+            store16(dx + (k * G + g.t) * 16, gr[k], r < a.rows ? n[k] : 0, a.w32);
+        }
+    }
+    if constexpr (ACC) {
+        if (!a.part) return;
+        const int lanes = MULTI ? 32 : G;  // lanes that hold different columns
+        if (!MULTI)
+            for (int d = 16; d >= G; d >>= 1)
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    dw[0][j] = add2(dw[0][j], make_float2(__shfl_xor_sync(0xffffffffu, dw[0][j].x, d),
+                                                          __shfl_xor_sync(0xffffffffu, dw[0][j].y, d)));
+                    db[0][j] = add2(db[0][j], make_float2(__shfl_xor_sync(0xffffffffu, db[0][j].x, d),
+                                                          __shfl_xor_sync(0xffffffffu, db[0][j].y, d)));
+                }
+        // turns: the groups, or the warps of groups already added up in lanes
+        const int turns = MULTI ? groups : blockDim.x >> 5, mine = MULTI ? g.id : threadIdx.x >> 5;
+        float2 *sw = reinterpret_cast<float2 *>(shared), *sb = sw + chunks * 8;
+        for (int turn = 0; turn < turns; turn++) {
+            __syncthreads();
+            if (turn == mine && (threadIdx.x & 31) < lanes) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) {  // pair j of every chunk together: no bank conflicts
+                    const int at = j * chunks + g.t;
+                    sw[at] = turn ? add2(sw[at], dw[0][j]) : dw[0][j];
+                    sb[at] = turn ? add2(sb[at], db[0][j]) : db[0][j];
+                }
+            }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+            const int at = ((c >> 1 & 7) * chunks + (c >> 4)) * 2 + (c & 1);
+            a.part[((int64_t)blockIdx.x * 2) * cols + c] = shared[at];
+            a.part[((int64_t)blockIdx.x * 2 + 1) * cols + c] = shared[chunks * 16 + at];
+        }
+    }
+}
+
+// Column sums of rows too wide for the accumulators: a thread takes chunk i of
+// the rows of slice blockIdx.y.
+template <typename TX, typename TY, bool CKPT>
+__global__ void __launch_bounds__(NM_THREADS) norm_dw_wide_kernel(NormArgs a)
+{
+    const int cols = (int)a.cols, i = blockIdx.x * NM_THREADS + threadIdx.x;
+    const int n = max(0, min(16, cols - i * 16));
+    if (n == 0) return;
+    float2 dw[8] = {}, db[8] = {};
+    for (int64_t r = blockIdx.y; r < a.rows; r += a.splits) {
+        RawBackward<TX, TY, CKPT> raw;
+        load_backward(a, r, i, n, raw);
+        float d[16], xh[16];
+        unpack16(raw.dy, d);
+        xhat16(a, raw, n, CKPT || a.rms ? 0.0f : __ldg(a.mean + r), CKPT ? 1.0f : __ldg(a.rstd + r), xh);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            dw[j] = fma2(make_float2(d[2 * j], d[2 * j + 1]), make_float2(xh[2 * j], xh[2 * j + 1]), dw[j]);
+            db[j] = add2(db[j], make_float2(d[2 * j], d[2 * j + 1]));
+        }
+    }
+    float *pw = a.part + ((int64_t)blockIdx.y * 2) * cols + i * 16, *pb = pw + cols;
+#pragma unroll
+    for (int j = 0; j < 16; j++)
+        if (j < n) {
+            pw[j] = j & 1 ? dw[j / 2].y : dw[j / 2].x;
+            pb[j] = j & 1 ? db[j / 2].y : db[j / 2].x;
+        }
 }
 
 template <typename TX, typename TY>
@@ -184,27 +644,50 @@ __global__ void __launch_bounds__(NM_THREADS) norm_dw_kernel(NormArgs a)
     }
 }
 
+// The slices' sums: 32 columns a block, eight threads a column that each add
+// every eighth slice.
 __global__ void __launch_bounds__(NM_THREADS) norm_dw_sum_kernel(NormArgs a)
 {
-    const int64_t c = (int64_t)blockIdx.x * NM_THREADS + threadIdx.x;
-    if (c >= a.cols) return;
+    __shared__ float2 part[NM_LANES][NM_COLS];
+    const int tc = threadIdx.x % NM_COLS, tr = threadIdx.x / NM_COLS;
+    const int64_t c = (int64_t)blockIdx.x * NM_COLS + tc;
     float dw = 0.0f, db = 0.0f;
-    for (int i = 0; i < a.splits; i++) {
-        dw += a.part[((int64_t)i * 2) * a.cols + c];
-        db += a.part[((int64_t)i * 2 + 1) * a.cols + c];
+    if (c < a.cols) {
+#pragma unroll 8
+        for (int i = tr; i < a.splits; i += NM_LANES) {
+            dw += a.part[((int64_t)i * 2) * a.cols + c];
+            db += a.part[((int64_t)i * 2 + 1) * a.cols + c];
+        }
+    }
+    part[tr][tc] = make_float2(dw, db);
+    __syncthreads();
+    if (tr != 0 || c >= a.cols) return;
+#pragma unroll
+    for (int i = 1; i < NM_LANES; i++) {
+        dw += part[i][tc].x;
+        db += part[i][tc].y;
     }
     set_param(a.dweight, a.w_dtype, c, dw);
     set_param(a.dbias, a.w_dtype, c, db);
 }
 
-// Row slices of the column sums: enough blocks for eight per SM, at least
-// NM_LANES rows each.
-static int norm_splits(int64_t rows, int64_t cols)
+// Row slices of the narrow column sums: enough blocks for eight per SM, at
+// least NM_LANES rows each.
+static int narrow_splits(int64_t rows, int64_t cols)
 {
     const int64_t tiles = (cols + NM_COLS - 1) / NM_COLS;
     int64_t want = ((int64_t)num_sms() * 8 + tiles - 1) / tiles;
     const int64_t most = (rows + NM_LANES - 1) / NM_LANES;
     if (want > most) want = most;
+    return want < 1 ? 1 : (int)want;
+}
+
+// Row slices of the wide column sums: four blocks per SM, 16 rows a slice.
+static int wide_splits(int64_t rows, int64_t cols)
+{
+    const int64_t tiles = (cols + 16 * NM_THREADS - 1) / (16 * NM_THREADS);
+    int64_t want = ((int64_t)num_sms() * 4 + tiles - 1) / tiles;
+    if (want > rows / 16) want = rows / 16;
     return want < 1 ? 1 : (int)want;
 }
 
@@ -214,20 +697,113 @@ static unsigned row_grid(int64_t rows)
     return (unsigned)(rows < cap ? rows : cap);
 }
 
-template <typename TX, typename TY>
-static void launch_backward(const NormArgs &a, cudaStream_t st)
+static bool rows_aligned(const void *p, int64_t ld, int size, int al)
 {
-    if (a.rows > 0) norm_dx_kernel<TX, TY><<<row_grid(a.rows), NM_THREADS, 0, st>>>(a);
-    if (!a.dweight && !a.dbias) return;
-    const dim3 grid((unsigned)((a.cols + NM_COLS - 1) / NM_COLS), (unsigned)a.splits);
-    norm_dw_kernel<TX, TY><<<grid, NM_THREADS, 0, st>>>(a);
-    norm_dw_sum_kernel<<<(unsigned)((a.cols + NM_THREADS - 1) / NM_THREADS), NM_THREADS, 0, st>>>(a);
+    return !p || (aligned(p, al) && ld * size % al == 0);
+}
+
+// Row groups and blocks of a wide kernel.
+struct WidePlan {
+    bool multi;       // groups of several warps
+    int chunks, G;    // chunks a thread, threads a group
+    unsigned threads, grid;
+};
+
+// `chunks` chunks a thread where a warp's lanes do not cover the row (one where
+// they do), at most `most` threads a block.  Few rows are spread over the SMs
+// before a second group joins a block.
+static WidePlan wide_plan(int64_t rows, int64_t cols, int chunks, int most)
+{
+    WidePlan p;
+    const int64_t need = (cols + 15) / 16;
+    p.chunks = need > 32 ? chunks : 1;
+    p.multi = need > 32 * p.chunks;
+    int groups;
+    if (p.multi) {
+        p.G = (int)((need + 32 * p.chunks - 1) / (32 * p.chunks)) * 32;
+        groups = most / p.G;
+        if (groups > NM_MAX_GROUPS) groups = NM_MAX_GROUPS;
+    } else {
+        p.G = 2;  // at least two lanes: a checkpoint block's halves
+        while (p.G * p.chunks < need) p.G *= 2;
+        groups = most / p.G;
+    }
+    const int64_t per_sm = (rows + num_sms() - 1) / num_sms();
+    if (groups > per_sm) groups = (int)per_sm;
+    if (!p.multi) groups = (groups * p.G + 31) / 32 * 32 / p.G;  // whole warps
+    if (groups < 1) groups = 1;
+    p.threads = (unsigned)(groups * p.G);
+    const int64_t blocks = (rows + groups - 1) / groups;
+    p.grid = (unsigned)(blocks < num_sms() ? blocks : num_sms());
+    return p;
+}
+
+template <typename K>
+static void launch_wide(K kernel, const WidePlan &p, int smem, const NormArgs &a, cudaStream_t st)
+{
+    // 48 KB without asking, the kernel's own few KB among them
+    if (smem > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    kernel<<<p.grid, p.threads, smem, st>>>(a);
 }
 
 template <typename TX, typename TY>
-static void launch_forward(const NormArgs &a, cudaStream_t st)
+static void launch_forward(NormArgs a, cudaStream_t st)
 {
-    norm_forward_kernel<TX, TY><<<row_grid(a.rows), NM_THREADS, 0, st>>>(a);
+    if (a.cols > NM_MAX_WIDE || !rows_aligned(a.x, a.ld_x, sizeof(TX), 16) ||
+        !rows_aligned(a.out, a.ld_out, sizeof(TY), 16) || !aligned(a.weight, 16) || !aligned(a.bias, 16)) {
+        norm_forward_kernel<TX, TY><<<row_grid(a.rows), NM_THREADS, 0, st>>>(a);
+        return;
+    }
+    a.w32 = rows_aligned(a.x, a.ld_x, sizeof(TX), 32) && rows_aligned(a.out, a.ld_out, sizeof(TY), 32);
+    const WidePlan p = wide_plan(a.rows, a.cols, 2, NM_BLOCK);
+    a.G = p.G;
+    const int smem = p.chunks * p.G * 16 * (int)sizeof(float) * (a.bias ? 2 : 1);
+    if (p.chunks == 1) launch_wide(norm_forward_wide_kernel<TX, TY, 1, false>, p, smem, a, st);
+    else if (!p.multi) launch_wide(norm_forward_wide_kernel<TX, TY, 2, false>, p, smem, a, st);
+    else launch_wide(norm_forward_wide_kernel<TX, TY, 2, true>, p, smem, a, st);
+}
+
+template <typename TX, typename TY, bool CKPT>
+static void launch_backward_wide(NormArgs a, cudaStream_t st)
+{
+    const bool grads = a.dweight || a.dbias, fused = a.cols <= NM_MAX_FUSED;
+    const WidePlan p = wide_plan(a.rows, a.cols, fused ? 1 : 2, NM_BLOCK);
+    const int vec = p.chunks * p.G * 16 * (int)sizeof(float);
+    a.G = p.G;
+    if (fused) {
+        a.splits = (int)p.grid;
+        if (!grads) a.part = nullptr;
+        if (p.multi) launch_wide(norm_backward_wide_kernel<TX, TY, 1, true, CKPT, true>, p, 2 * vec, a, st);
+        else launch_wide(norm_backward_wide_kernel<TX, TY, 1, false, CKPT, true>, p, 2 * vec, a, st);
+    } else {
+        launch_wide(norm_backward_wide_kernel<TX, TY, 2, true, CKPT, false>, p, vec, a, st);
+        if (!grads) return;
+        a.splits = wide_splits(a.rows, a.cols);
+        const dim3 grid((unsigned)((a.cols + 16 * NM_THREADS - 1) / (16 * NM_THREADS)), (unsigned)a.splits);
+        norm_dw_wide_kernel<TX, TY, CKPT><<<grid, NM_THREADS, 0, st>>>(a);
+    }
+    if (grads) norm_dw_sum_kernel<<<(unsigned)((a.cols + NM_COLS - 1) / NM_COLS), NM_THREADS, 0, st>>>(a);
+}
+
+template <typename TX, typename TY>
+static void launch_backward(NormArgs a, cudaStream_t st)
+{
+    const auto all_aligned = [&](int al) {
+        return rows_aligned(a.dy, a.ld_dy, sizeof(TY), al) && rows_aligned(a.out, a.ld_out, sizeof(TX), al) &&
+               rows_aligned(a.x, a.ld_x, sizeof(TX), al);
+    };
+    if (a.rows > 0 && a.cols <= NM_MAX_WIDE && all_aligned(16) && aligned(a.weight, 16)) {
+        a.w32 = all_aligned(32);
+        if (a.x) launch_backward_wide<TX, TY, false>(a, st);
+        else launch_backward_wide<TX, TY, true>(a, st);
+        return;
+    }
+    if (a.rows > 0) norm_dx_kernel<TX, TY><<<row_grid(a.rows), NM_THREADS, 0, st>>>(a);
+    if (!a.dweight && !a.dbias) return;
+    a.splits = narrow_splits(a.rows, a.cols);
+    const dim3 grid((unsigned)((a.cols + NM_COLS - 1) / NM_COLS), (unsigned)a.splits);
+    norm_dw_kernel<TX, TY><<<grid, NM_THREADS, 0, st>>>(a);
+    norm_dw_sum_kernel<<<(unsigned)((a.cols + NM_COLS - 1) / NM_COLS), NM_THREADS, 0, st>>>(a);
 }
 
 static bool good_dtype(int d) { return d >= FP8_DTYPE_BF16 && d <= FP8_DTYPE_F32; }
@@ -318,7 +894,13 @@ extern "C" fp8_status_t fp8_norm_forward(const void *x, int x_dtype, int64_t ld_
 extern "C" int64_t fp8_norm_workspace_bytes(int64_t rows, int64_t cols)
 {
     if (rows < 0 || cols < 1 || rows > INT32_MAX || cols > INT32_MAX - FP8_MX_BLOCK) return -1;
-    return (int64_t)norm_splits(rows, cols) * 2 * cols * (int64_t)sizeof(float);
+    // the most row slices that any form makes: the wide fused kernel's blocks,
+    // or the slices of either column kernel
+    int64_t most = num_sms();
+    if (narrow_splits(rows, cols) > most) most = narrow_splits(rows, cols);
+    if (wide_splits(rows, cols) > most) most = wide_splits(rows, cols);
+    if (most > rows) most = rows > 0 ? rows : 1;  // a slice has a row at least
+    return most * 2 * cols * (int64_t)sizeof(float);
 }
 
 extern "C" fp8_status_t fp8_norm_backward(const void *dy, int y_dtype, int64_t ld_dy, const void *x, int64_t ld_x,
@@ -368,7 +950,6 @@ extern "C" fp8_status_t fp8_norm_backward(const void *dy, int y_dtype, int64_t l
     a.dweight = dweight;
     a.dbias = dbias;
     a.part = static_cast<float *>(workspace);
-    a.splits = norm_splits(rows, cols);
     NORM_TYPES(launch_backward, x_dtype, y_dtype, a, static_cast<cudaStream_t>(stream));
     return check_launch();
 }
