@@ -4,14 +4,12 @@
 //
 // All four are one pass over their tensors and bounded by HBM.
 //
-// Wide form (addresses and strides multiples of 16 bytes): a thread works on
-// 16 consecutive columns, half a block, so the bf16 side is one 32-byte access,
-// the codes one of 16, and the block maximum one shuffle with the neighbour.
-// A thread issues the loads of UNROLL rows before it works on the first.  The
-// threads of a block cover tx chunks of ty rows, so no thread divides.
-//
-// Narrow form (any other alignment): a lane per element and a warp per block
-// of 32 columns; accesses stay consecutive at every width and stride.
+// A thread works on 16 consecutive columns, half a block: the bf16 side is one
+// 32-byte access, the codes one of 16, and the block maximum one shuffle with the
+// neighbour.  It issues the loads of UNROLL rows before it works on the first.
+// The threads of a block cover 2^lg chunks of CK_THREADS >> lg rows, so no thread
+// divides.  Rows that are no multiple of 16 bytes apart (ANY) are read and
+// written in the aligned words that cover them, shifted into place.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -23,7 +21,6 @@
 namespace fp8gb {
 
 constexpr int CK_THREADS = 256;
-constexpr int CK_WARPS = CK_THREADS / 32;
 
 // How the blocks of the wide kernels cover rows x chunks of 16 columns.
 struct WideGeometry {
@@ -73,27 +70,33 @@ __device__ __forceinline__ WidePlace wide_place(const WideGeometry &g)
     return p;
 }
 
+// Columns of a part from column c on, and how many of them are in c's chunk.
+__device__ __forceinline__ int chunk_rest(int64_t cols, int64_t c) { return (int)(cols - c); }
+__device__ __forceinline__ int chunk_columns(int64_t cols, int64_t c) { return max(0, min(16, chunk_rest(cols, c))); }
+
 constexpr int STORE_UNROLL = 4, RESTORE_UNROLL = 4, SWIGLU_UNROLL = 2, BACKWARD_UNROLL = 2;
 
-template <typename T, int FMT>
-__global__ void __launch_bounds__(CK_THREADS) checkpoint_wide_kernel(CkArgs a)
+template <typename T, int FMT, bool ANY>
+__global__ void __launch_bounds__(CK_THREADS) checkpoint_kernel(CkArgs a)
 {
     const WidePlace p = wide_place<STORE_UNROLL>(a.geo);
     const int64_t cpp = ckpt_width(a.cols) / 16;  // chunks of a part
     const bool in = p.chunk < a.parts * cpp;
     const int64_t part = a.parts == 1 ? 0 : p.chunk / cpp, c = (p.chunk - part * cpp) * 16;
-    const T *x = static_cast<const T *>(a.x) + part * a.cols + c;
-    Raw16<T> raw[STORE_UNROLL];
+    const int n = in ? chunk_columns(a.cols, c) : 0;
+    const Rows<const T> x = rows_of(static_cast<const T *>(a.x), a.ld_x, a.rows, a.parts * a.cols);
+    Raw<T, ANY> raw[STORE_UNROLL];
 #pragma unroll
     for (int k = 0; k < STORE_UNROLL; k++) {
         const int64_t r = p.row + (int64_t)k * p.ty;
-        load16(x + r * a.ld_x, in && r < a.rows ? a.cols - c : 0, a.w32, raw[k]);
+        load_chunk<ANY>(x, r, part * a.cols + c, r < a.rows ? n : 0, a.w32, raw[k]);
     }
 #pragma unroll
     for (int k = 0; k < STORE_UNROLL; k++) {
         const int64_t r = p.row + (int64_t)k * p.ty;
         float f[16];
         unpack16(raw[k], f);
+        if (ANY) fill_from(f, n, 0.0f);
         const uint32_t code = ckpt_code(block_amax16(f), FMT);
         if (!in || r >= a.rows) continue;
         *reinterpret_cast<uint4 *>(a.q + r * a.ld_q + p.chunk * 16) = encode16<FMT>(f, ckpt_inv_scale(code));
@@ -101,45 +104,55 @@ __global__ void __launch_bounds__(CK_THREADS) checkpoint_wide_kernel(CkArgs a)
     }
 }
 
-template <typename T, int FMT>
-__global__ void __launch_bounds__(CK_THREADS) restore_wide_kernel(CkArgs a)
+template <typename T, int FMT, bool ANY>
+__global__ void __launch_bounds__(CK_THREADS) restore_kernel(CkArgs a)
 {
     const WidePlace p = wide_place<RESTORE_UNROLL>(a.geo);
     const int64_t cpp = ckpt_width(a.cols) / 16;
-    if (p.chunk >= a.parts * cpp) return;
+    const bool in = p.chunk < a.parts * cpp;
     const int64_t part = a.parts == 1 ? 0 : p.chunk / cpp, c = (p.chunk - part * cpp) * 16;
-    T *x = static_cast<T *>(a.x) + part * a.cols + c;
+    const int rest = in ? chunk_rest(a.cols, c) : 0;
+    // a part's first and last chunk have no neighbours, whatever the lanes beside them hold
+    const int lanes = 1 << a.geo.lg, t = threadIdx.x & (lanes - 1);
+    const Rows<T> x{static_cast<T *>(a.x), a.ld_x, 0};
     uint4 q[RESTORE_UNROLL];
     uint32_t s[RESTORE_UNROLL];
 #pragma unroll
     for (int k = 0; k < RESTORE_UNROLL; k++) {
         const int64_t r = p.row + (int64_t)k * p.ty;
-        if (r >= a.rows) break;
+        q[k] = make_uint4(0, 0, 0, 0);
+        s[k] = 0;
+        if (rest <= 0 || r >= a.rows) continue;
         q[k] = ld_stream_16b(a.q + r * a.ld_q + p.chunk * 16);
         s[k] = __ldg(a.s + r * a.ld_s + (p.chunk >> 1));
     }
 #pragma unroll
     for (int k = 0; k < RESTORE_UNROLL; k++) {
         const int64_t r = p.row + (int64_t)k * p.ty;
-        if (r >= a.rows) break;
         float f[16];
         decode16<FMT>(q[k], ckpt_scale(s[k]), f);
-        store16(x + r * a.ld_x, f, a.cols - c, a.w32);
+        store_chunk<ANY>(x, r, part * a.cols + c, f, r < a.rows ? rest : 0, a.w32, c == 0 ? 0 : t,
+                         rest <= 16 ? t + 1 : lanes);
     }
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(CK_THREADS) swiglu_checkpoint_wide_kernel(SwArgs a)
+template <int FMT, bool ANY>
+__global__ void __launch_bounds__(CK_THREADS) swiglu_checkpoint_kernel(SwArgs a)
 {
+    using T = __nv_bfloat16;
     const WidePlace p = wide_place<SWIGLU_UNROLL>(a.geo);
     const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16;
     const bool in = p.chunk < cpp;
-    Raw16<__nv_bfloat16> gr[SWIGLU_UNROLL], ur[SWIGLU_UNROLL];
+    const int n = in ? chunk_columns(a.F, c) : 0, rest = in ? chunk_rest(a.F, c) : 0;
+    const int lanes = 1 << a.geo.lg, t = threadIdx.x & (lanes - 1);
+    const Rows<const T> gu = rows_of(a.gate_up, a.ld, a.rows, 2 * a.F);
+    const Rows<T> hd{a.h, a.ld_h, 0};
+    Raw<T, ANY> gr[SWIGLU_UNROLL], ur[SWIGLU_UNROLL];
 #pragma unroll
     for (int k = 0; k < SWIGLU_UNROLL; k++) {
-        const int64_t r = p.row + (int64_t)k * p.ty, n = in && r < a.rows ? a.F - c : 0;
-        load16(a.gate_up + r * a.ld + c, n, a.w32, gr[k]);
-        load16(a.gate_up + r * a.ld + a.F + c, n, a.w32, ur[k]);
+        const int64_t r = p.row + (int64_t)k * p.ty;
+        load_chunk<ANY>(gu, r, c, r < a.rows ? n : 0, a.w32, gr[k]);
+        load_chunk<ANY>(gu, r, a.F + c, r < a.rows ? n : 0, a.w32, ur[k]);
     }
 #pragma unroll
     for (int k = 0; k < SWIGLU_UNROLL; k++) {
@@ -147,11 +160,15 @@ __global__ void __launch_bounds__(CK_THREADS) swiglu_checkpoint_wide_kernel(SwAr
         float g[16], u[16], h[16];
         unpack16(gr[k], g);
         unpack16(ur[k], u);
+        if (ANY) {
+            fill_from(g, n, 0.0f);
+            fill_from(u, n, 0.0f);
+        }
         const uint32_t cg = ckpt_code(block_amax16(g), FMT), cu = ckpt_code(block_amax16(u), FMT);
-        if (!in || r >= a.rows) continue;
 #pragma unroll
         for (int j = 0; j < 16; j++) h[j] = swiglu1(g[j], u[j]);
-        store16(a.h + r * a.ld_h + c, h, a.F - c, a.w32);
+        store_chunk<ANY>(hd, r, c, h, r < a.rows ? rest : 0, a.w32, t, lanes);
+        if (!in || r >= a.rows) continue;
         uint8_t *q = a.q + r * a.ld_q + c;
         *reinterpret_cast<uint4 *>(q) = encode16<FMT>(g, ckpt_inv_scale(cg));
         *reinterpret_cast<uint4 *>(q + cpp * 16) = encode16<FMT>(u, ckpt_inv_scale(cu));
@@ -164,35 +181,42 @@ __global__ void __launch_bounds__(CK_THREADS) swiglu_checkpoint_wide_kernel(SwAr
 }
 
 // CKPT: gate and up from the checkpoint, else from bf16.
-template <int FMT, bool CKPT>
-__global__ void __launch_bounds__(CK_THREADS) swiglu_backward_wide_kernel(SwArgs a)
+template <int FMT, bool CKPT, bool ANY>
+__global__ void __launch_bounds__(CK_THREADS) swiglu_backward_kernel(SwArgs a)
 {
+    using T = __nv_bfloat16;
     const WidePlace p = wide_place<BACKWARD_UNROLL>(a.geo);
-    const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16, n = a.F - c;
-    if (n <= 0) return;
-    Raw16<__nv_bfloat16> gr[BACKWARD_UNROLL], ur[BACKWARD_UNROLL], dr[BACKWARD_UNROLL];
+    const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16;
+    const int n = chunk_columns(a.F, c), rest = chunk_rest(a.F, c);  // nothing past the row
+    const int lanes = 1 << a.geo.lg, t = threadIdx.x & (lanes - 1);
+    const Rows<const T> gu = rows_of(a.gate_up, a.ld, a.rows, 2 * a.F), dhs = rows_of(a.dh, a.ld_dh, a.rows, a.F);
+    const Rows<T> dd{a.d, a.ld_d, 0}, hd{a.h, a.ld_h, 0};
+    Raw<T, ANY> gr[BACKWARD_UNROLL], ur[BACKWARD_UNROLL], dr[BACKWARD_UNROLL];
     uint4 gq[BACKWARD_UNROLL], uq[BACKWARD_UNROLL];
     uint32_t gs[BACKWARD_UNROLL], us[BACKWARD_UNROLL];
 #pragma unroll
     for (int k = 0; k < BACKWARD_UNROLL; k++) {
         const int64_t r = p.row + (int64_t)k * p.ty;
-        if (r >= a.rows) break;
+        const int have = r < a.rows ? n : 0;
         if constexpr (CKPT) {
-            const uint8_t *q = a.q + r * a.ld_q + c, *s = a.s + r * a.ld_s + (p.chunk >> 1);
-            gq[k] = ld_stream_16b(q);
-            uq[k] = ld_stream_16b(q + cpp * 16);
-            gs[k] = __ldg(s);
-            us[k] = __ldg(s + (cpp >> 1));
+            gq[k] = uq[k] = make_uint4(0, 0, 0, 0);
+            gs[k] = us[k] = 0;
+            if (have > 0) {
+                const uint8_t *q = a.q + r * a.ld_q + c, *s = a.s + r * a.ld_s + (p.chunk >> 1);
+                gq[k] = ld_stream_16b(q);
+                uq[k] = ld_stream_16b(q + cpp * 16);
+                gs[k] = __ldg(s);
+                us[k] = __ldg(s + (cpp >> 1));
+            }
         } else {
-            load16(a.gate_up + r * a.ld + c, n, a.w32, gr[k]);
-            load16(a.gate_up + r * a.ld + a.F + c, n, a.w32, ur[k]);
+            load_chunk<ANY>(gu, r, c, have, a.w32, gr[k]);
+            load_chunk<ANY>(gu, r, a.F + c, have, a.w32, ur[k]);
         }
-        load16(a.dh + r * a.ld_dh + c, n, a.w32, dr[k]);
+        load_chunk<ANY>(dhs, r, c, have, a.w32, dr[k]);
     }
 #pragma unroll
     for (int k = 0; k < BACKWARD_UNROLL; k++) {
         const int64_t r = p.row + (int64_t)k * p.ty;
-        if (r >= a.rows) break;
         float g[16], u[16], d[16];
         if constexpr (CKPT) {
             decode16<FMT>(gq[k], ckpt_scale(gs[k]), g);
@@ -212,88 +236,11 @@ __global__ void __launch_bounds__(CK_THREADS) swiglu_backward_wide_kernel(SwArgs
             u[j] = du.x, u[j + 1] = du.y;
             d[j] = h.x, d[j + 1] = h.y;
         }
-        if (a.h) store16(a.h + r * a.ld_h + c, d, n, a.w32);
-        store16(a.d + r * a.ld_d + c, g, n, a.w32);
-        store16(a.d + r * a.ld_d + a.F + c, u, n, a.w32);
+        const int have = r < a.rows ? rest : 0;
+        if (a.h) store_chunk<ANY>(hd, r, c, d, have, a.w32, t, lanes);
+        store_chunk<ANY>(dd, r, c, g, have, a.w32, t, lanes);
+        store_chunk<ANY>(dd, r, a.F + c, u, have, a.w32, t, lanes);
     }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(CK_THREADS) checkpoint_kernel(CkArgs a)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t nb = ckpt_width(a.cols) / FP8_MX_BLOCK;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T *x = static_cast<const T *>(a.x) + r * a.ld_x;
-        for (int p = 0; p < a.parts; p++)
-            for (int64_t b = warp; b < nb; b += CK_WARPS) {
-                const int64_t c = b * FP8_MX_BLOCK + lane;
-                const float v = c < a.cols ? to_f32<T>(x[p * a.cols + c]) : 0.0f;
-                ckpt_store_lane(v, a.fmt, a.q + r * a.ld_q + (p * nb + b) * FP8_MX_BLOCK,
-                                a.s + r * a.ld_s + p * nb + b, lane);
-            }
-    }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(CK_THREADS) restore_kernel(CkArgs a)
-{
-    const int64_t nb = ckpt_width(a.cols) / FP8_MX_BLOCK;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        T *x = static_cast<T *>(a.x) + r * a.ld_x;
-        for (int p = 0; p < a.parts; p++)
-            for (int64_t c = threadIdx.x; c < a.cols; c += CK_THREADS)
-                x[p * a.cols + c] = from_f32<T>(
-                    ckpt_load_one(a.q + r * a.ld_q + p * nb * FP8_MX_BLOCK, a.s + r * a.ld_s + p * nb, c, a.fmt));
-    }
-}
-
-__global__ void __launch_bounds__(CK_THREADS) swiglu_checkpoint_kernel(SwArgs a)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t nb = ckpt_width(a.F) / FP8_MX_BLOCK;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const __nv_bfloat16 *x = a.gate_up + r * a.ld;
-        uint8_t *q = a.q + r * a.ld_q, *s = a.s + r * a.ld_s;
-        for (int64_t b = warp; b < nb; b += CK_WARPS) {
-            const int64_t c = b * FP8_MX_BLOCK + lane;
-            const float g = c < a.F ? to_f32(x[c]) : 0.0f, u = c < a.F ? to_f32(x[a.F + c]) : 0.0f;
-            if (c < a.F) a.h[r * a.ld_h + c] = from_f32<__nv_bfloat16>(swiglu1(g, u));
-            ckpt_store_lane(g, a.fmt, q + b * FP8_MX_BLOCK, s + b, lane);
-            ckpt_store_lane(u, a.fmt, q + (nb + b) * FP8_MX_BLOCK, s + nb + b, lane);
-        }
-    }
-}
-
-__global__ void __launch_bounds__(CK_THREADS) swiglu_backward_kernel(SwArgs a)
-{
-    const int64_t nb = ckpt_width(a.F) / FP8_MX_BLOCK;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const uint8_t *q = a.q + r * a.ld_q, *s = a.s + r * a.ld_s;
-        for (int64_t c = threadIdx.x; c < a.F; c += CK_THREADS) {
-            float g, u;
-            if (a.gate_up) {
-                g = to_f32(a.gate_up[r * a.ld + c]);
-                u = to_f32(a.gate_up[r * a.ld + a.F + c]);
-            } else {
-                g = ckpt_load_one(q, s, c, a.fmt);
-                u = ckpt_load_one(q + nb * FP8_MX_BLOCK, s + nb, c, a.fmt);
-            }
-            float2 dg, du, h;
-            swiglu_grad2(make_float2(g, 0.0f), make_float2(u, 0.0f),
-                         make_float2(to_f32(a.dh[r * a.ld_dh + c]), 0.0f), dg, du, h);
-            a.d[r * a.ld_d + c] = from_f32<__nv_bfloat16>(dg.x);
-            a.d[r * a.ld_d + a.F + c] = from_f32<__nv_bfloat16>(du.x);
-            if (a.h) a.h[r * a.ld_h + c] = from_f32<__nv_bfloat16>(h.x);
-        }
-    }
-}
-
-// Blocks of a grid that covers `rows` rows, eight resident per SM.
-static unsigned row_grid(int64_t rows)
-{
-    const int64_t cap = (int64_t)num_sms() * 8;
-    return (unsigned)(rows < cap ? rows : cap);
 }
 
 // The widest block whose tiles cover a row of `chunks` with at most 1/16 of
@@ -309,8 +256,8 @@ static WideGeometry wide_geometry(int64_t rows, int64_t chunks, int unroll)
     }
     g.n_tiles = (uint32_t)((chunks + (1LL << g.lg) - 1) >> g.lg);
     const int64_t high = (int64_t)(CK_THREADS >> g.lg) * unroll;
-    const int64_t grid = (rows + high - 1) / high * g.n_tiles;
-    g.grid = grid > INT32_MAX ? 0 : (uint32_t)grid;  // 0: more blocks than a launch holds
+    // below 2^31 for anything a device can hold: a block covers 2^12 elements at least
+    g.grid = (uint32_t)((rows + high - 1) / high * g.n_tiles);
     return g;
 }
 
@@ -352,30 +299,57 @@ static fp8_status_t check_bf16(const void *p, int64_t ld, int64_t cols)
     return aligned(p, 2) ? FP8_OK : FP8_ERR_ALIGNMENT;
 }
 
-// The wide form where every row and part of x is 16-byte aligned.
+// Geometry and alignment of x; whether its rows and parts take 16-byte accesses.
 template <typename T>
-static bool plan_wide(CkArgs &a, int unroll)
+static bool plan(CkArgs &a, int unroll)
 {
     const int64_t off = a.parts > 1 ? a.cols : 0;
     a.geo = wide_geometry(a.rows, a.parts * (ckpt_width(a.cols) / 16), unroll);
     a.w32 = rows_aligned(a.x, a.ld_x, off, sizeof(T), 32);
-    return a.geo.grid && rows_aligned(a.x, a.ld_x, off, sizeof(T), 16);
+    return rows_aligned(a.x, a.ld_x, off, sizeof(T), 16);
 }
 
 template <typename T>
 static void launch_checkpoint(CkArgs a, cudaStream_t st)
 {
-    if (!plan_wide<T>(a, STORE_UNROLL)) checkpoint_kernel<T><<<row_grid(a.rows), CK_THREADS, 0, st>>>(a);
-    else if (a.fmt == FP8_E5M2) checkpoint_wide_kernel<T, FP8_E5M2><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
-    else checkpoint_wide_kernel<T, FP8_E4M3FN><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    const bool wide = plan<T>(a, STORE_UNROLL);
+    const auto run = [&](auto kernel) { kernel<<<a.geo.grid, CK_THREADS, 0, st>>>(a); };
+    if (a.fmt == FP8_E5M2) wide ? run(checkpoint_kernel<T, FP8_E5M2, false>) : run(checkpoint_kernel<T, FP8_E5M2, true>);
+    else wide ? run(checkpoint_kernel<T, FP8_E4M3FN, false>) : run(checkpoint_kernel<T, FP8_E4M3FN, true>);
 }
 
 template <typename T>
 static void launch_restore(CkArgs a, cudaStream_t st)
 {
-    if (!plan_wide<T>(a, RESTORE_UNROLL)) restore_kernel<T><<<row_grid(a.rows), CK_THREADS, 0, st>>>(a);
-    else if (a.fmt == FP8_E5M2) restore_wide_kernel<T, FP8_E5M2><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
-    else restore_wide_kernel<T, FP8_E4M3FN><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    const bool wide = plan<T>(a, RESTORE_UNROLL);
+    const auto run = [&](auto kernel) { kernel<<<a.geo.grid, CK_THREADS, 0, st>>>(a); };
+    if (a.fmt == FP8_E5M2) wide ? run(restore_kernel<T, FP8_E5M2, false>) : run(restore_kernel<T, FP8_E5M2, true>);
+    else wide ? run(restore_kernel<T, FP8_E4M3FN, false>) : run(restore_kernel<T, FP8_E4M3FN, true>);
+}
+
+template <int FMT>
+static void launch_swiglu_checkpoint(SwArgs a, cudaStream_t st)
+{
+    const auto all_aligned = [&](int al) {
+        return rows_aligned(a.gate_up, a.ld, a.F, 2, al) && rows_aligned(a.h, a.ld_h, 0, 2, al);
+    };
+    a.geo = wide_geometry(a.rows, ckpt_width(a.F) / 16, SWIGLU_UNROLL);
+    a.w32 = all_aligned(32);
+    if (all_aligned(16)) swiglu_checkpoint_kernel<FMT, false><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    else swiglu_checkpoint_kernel<FMT, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+}
+
+template <int FMT, bool CKPT>
+static void launch_swiglu_backward(SwArgs a, cudaStream_t st)
+{
+    const auto all_aligned = [&](int al) {
+        return rows_aligned(a.dh, a.ld_dh, 0, 2, al) && rows_aligned(a.d, a.ld_d, a.F, 2, al) &&
+               rows_aligned(a.h, a.h ? a.ld_h : 0, 0, 2, al) && (CKPT || rows_aligned(a.gate_up, a.ld, a.F, 2, al));
+    };
+    a.geo = wide_geometry(a.rows, ckpt_width(a.F) / 16, BACKWARD_UNROLL);
+    a.w32 = all_aligned(32);
+    if (all_aligned(16)) swiglu_backward_kernel<FMT, CKPT, false><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    else swiglu_backward_kernel<FMT, CKPT, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
 }
 
 }  // namespace fp8gb
@@ -432,14 +406,8 @@ extern "C" fp8_status_t fp8_swiglu_checkpoint(const void *gate_up_bf16, int64_t 
     a.ld_q = ld_q;
     a.ld_s = ld_s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    a.geo = wide_geometry(rows, ckpt_width(F) / 16, SWIGLU_UNROLL);
-    a.w32 = rows_aligned(a.gate_up, ld, F, 2, 32) && rows_aligned(a.h, ld_h, 0, 2, 32);
-    if (a.geo.grid && rows_aligned(a.gate_up, ld, F, 2, 16) && rows_aligned(a.h, ld_h, 0, 2, 16)) {
-        if (fmt == FP8_E5M2) swiglu_checkpoint_wide_kernel<FP8_E5M2><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
-        else swiglu_checkpoint_wide_kernel<FP8_E4M3FN><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
-    } else {
-        swiglu_checkpoint_kernel<<<row_grid(rows), CK_THREADS, 0, st>>>(a);
-    }
+    if (fmt == FP8_E5M2) launch_swiglu_checkpoint<FP8_E5M2>(a, st);
+    else launch_swiglu_checkpoint<FP8_E4M3FN>(a, st);
     return check_launch();
 }
 
@@ -474,19 +442,8 @@ extern "C" fp8_status_t fp8_swiglu_backward(const void *dh_bf16, int64_t ld_dh, 
     a.h = static_cast<__nv_bfloat16 *>(h_bf16);
     a.ld_h = ld_h;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    a.geo = wide_geometry(rows, ckpt_width(F) / 16, BACKWARD_UNROLL);
-    const auto all_aligned = [&](int al) {
-        return rows_aligned(a.dh, ld_dh, 0, 2, al) && rows_aligned(a.d, ld_d, F, 2, al) &&
-               rows_aligned(a.h, a.h ? ld_h : 0, 0, 2, al) && rows_aligned(a.gate_up, a.gate_up ? ld : 0, F, 2, al);
-    };
-    a.w32 = all_aligned(32);
-    if (!a.geo.grid || !all_aligned(16))
-        swiglu_backward_kernel<<<row_grid(rows), CK_THREADS, 0, st>>>(a);
-    else if (a.gate_up)
-        swiglu_backward_wide_kernel<FP8_E4M3FN, false><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
-    else if (fmt == FP8_E5M2)
-        swiglu_backward_wide_kernel<FP8_E5M2, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
-    else
-        swiglu_backward_wide_kernel<FP8_E4M3FN, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    if (gate_up_bf16) launch_swiglu_backward<FP8_E4M3FN, false>(a, st);
+    else if (fmt == FP8_E5M2) launch_swiglu_backward<FP8_E5M2, true>(a, st);
+    else launch_swiglu_backward<FP8_E4M3FN, true>(a, st);
     return check_launch();
 }

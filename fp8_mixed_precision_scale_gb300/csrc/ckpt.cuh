@@ -137,8 +137,8 @@ __device__ __forceinline__ void st_32b(void *p, const uint4 &lo, const uint4 &hi
 }
 
 // Elements 0 .. n-1 from p (n >= 16: all of them by wide loads), zeros after.
-template <typename T, typename N>
-__device__ __forceinline__ void load16(const T *p, N n, bool w32, Raw16<T> &r)
+template <typename T>
+__device__ __forceinline__ void load16(const T *p, int n, bool w32, Raw16<T> &r)
 {
     if (n >= 16) {
         if (w32) {
@@ -209,8 +209,8 @@ __device__ __forceinline__ void unpack16(const Raw16<T> &r, float (&f)[16])
 }
 
 // Elements 0 .. n-1 to p.
-template <typename T, typename N>
-__device__ __forceinline__ void store16(T *p, const float (&f)[16], N n, bool w32)
+template <typename T>
+__device__ __forceinline__ void store16(T *p, const float (&f)[16], int n, bool w32)
 {
     if (n >= 16) {
         uint4 v[sizeof(T)];
@@ -236,6 +236,182 @@ __device__ __forceinline__ void store16(T *p, const float (&f)[16], N n, bool w3
 #pragma unroll
     for (int j = 0; j < 16; j++)
         if (j < n) p[j] = from_f32<T>(f[j]);
+}
+
+// ---------------------------------------------------------------------------
+// The same sixteen elements at any element alignment.  Every lane of a row's
+// segment stands at the same offset from a 16-byte boundary, since lanes are 32
+// (64) bytes apart.
+//
+// Load: the aligned 16-byte words that cover the elements, one more than
+// aligned data takes, moved into place when they are used (realign16).  They
+// reach up to 14 bytes past the elements on either side, so only a caller that
+// knows these to lie inside the tensor says `inside`; the others load element
+// by element.  Elements from n on are whatever lies there.
+//
+// Store: a lane shifts its elements and the first ones of the next lane into
+// aligned words; what has no neighbour to do that with (a row's or a warp's
+// ends) goes element by element.
+// ---------------------------------------------------------------------------
+template <typename T>
+struct RawAny {
+    uint4 v[sizeof(T) + 1];
+    uint32_t shift;  // bytes from v to the first element
+};
+
+template <typename T>
+__device__ __forceinline__ void load16(const T *p, int n, bool inside, RawAny<T> &r)
+{
+    r.shift = 0;
+    if (n > 0 && inside) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        const uint4 *w = reinterpret_cast<const uint4 *>(at & ~(uintptr_t)15);
+        r.shift = (uint32_t)at & 15u;
+        // through L1: neighbouring lanes read the words between them twice
+#pragma unroll
+        for (int j = 0; j <= (int)sizeof(T); j++) r.v[j] = __ldg(w + j);
+    } else {
+        Raw16<T> e;
+        const T *own = p;
+        load16(own, n < 16 ? n : 15, false, e);
+        if (n >= 16) {  // the last element by itself: load16 would take wide accesses for all sixteen
+            if constexpr (sizeof(T) == 4) e.v[sizeof(T) - 1].w = __float_as_uint(to_f32(p[15]));
+            else e.v[sizeof(T) - 1].w |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[15] << 16;
+        }
+#pragma unroll
+        for (int j = 0; j < (int)sizeof(T); j++) r.v[j] = e.v[j];
+        r.v[sizeof(T)] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// Words a[0 ..] shifted down by `shift` bytes (0 .. 14, even), N of them.
+template <int N>
+__device__ __forceinline__ void shift_words(const uint32_t (&a)[N + 4], uint32_t shift, uint32_t (&out)[N])
+{
+    uint32_t b[N + 2], c[N + 1];
+#pragma unroll
+    for (int j = 0; j < N + 2; j++) b[j] = shift & 8u ? a[j + 2] : a[j];
+#pragma unroll
+    for (int j = 0; j < N + 1; j++) c[j] = shift & 4u ? b[j + 1] : b[j];
+#pragma unroll
+    for (int j = 0; j < N; j++) out[j] = __funnelshift_r(c[j], c[j + 1], (shift & 2u) * 8u);
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack16(const RawAny<T> &r, float (&f)[16])
+{
+    constexpr int N = 4 * sizeof(T);
+    uint32_t a[N + 4], w[N];
+#pragma unroll
+    for (int j = 0; j <= (int)sizeof(T); j++) {
+        a[4 * j] = r.v[j].x, a[4 * j + 1] = r.v[j].y, a[4 * j + 2] = r.v[j].z, a[4 * j + 3] = r.v[j].w;
+    }
+    shift_words<N>(a, r.shift, w);
+    Raw16<T> e;
+#pragma unroll
+    for (int j = 0; j < (int)sizeof(T); j++) e.v[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    unpack16(e, f);
+}
+
+// Elements 0 .. min(16, rest) - 1 to p, `rest` being what the row has from
+// here on (<= 0: nothing).  `first` / `last`: the lane before / after does not
+// hold the row's elements before / after these.  All lanes of a warp call it.
+template <typename T>
+__device__ __forceinline__ void store16_any(T *p, const float (&f)[16], int rest, bool first, bool last)
+{
+    constexpr int N = 4 * sizeof(T), PER = 16 / sizeof(T);  // words of a lane, elements of a 16-byte word
+    uint32_t a[N + 4], w[N];
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+        if constexpr (sizeof(T) == 4) a[j] = __float_as_uint(f[j]);
+        else a[j] = float2_to_word<T>(f[2 * j], f[2 * j + 1]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) a[N + j] = __shfl_down_sync(0xffffffffu, a[j], 1);
+    const uint32_t o = (16u - (uint32_t)reinterpret_cast<uintptr_t>(p)) & 15u;  // bytes to the first aligned word
+    const int head = (int)(o / sizeof(T));
+    shift_words<N>(a, o, w);
+    int lo = 0, hi = 0;  // elements that go one by one
+    if (rest >= 16) {
+        uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<uintptr_t>(p) + o);
+#pragma unroll
+        for (int j = 0; j < (int)sizeof(T) - 1; j++)
+            dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        if (head == 0 || (!last && rest - 16 >= head))
+            dst[sizeof(T) - 1] = make_uint4(w[N - 4], w[N - 3], w[N - 2], w[N - 1]);
+        else
+            lo = head + 16 - PER, hi = 16;
+        if (first) {
+#pragma unroll
+            for (int j = 0; j < PER - 1; j++)
+                if (j < head) p[j] = from_f32<T>(f[j]);
+        }
+    } else if (rest > 0) {
+        lo = !first && rest >= head ? head : 0, hi = rest;
+    }
+    if (lo < hi) {
+#pragma unroll
+        for (int j = 0; j < 16; j++)
+            if (j >= lo && j < hi) p[j] = from_f32<T>(f[j]);
+    }
+}
+
+// Either form of the loads and stores as a template parameter: ANY alignment,
+// or multiples of 16 bytes.
+template <typename T, bool ANY>
+struct RawOf {
+    using type = Raw16<T>;
+};
+template <typename T>
+struct RawOf<T, true> {
+    using type = RawAny<T>;
+};
+template <typename T, bool ANY>
+using Raw = typename RawOf<T, ANY>::type;
+
+// A tensor whose rows threads read or write in chunks of 16 elements.
+template <typename T>
+struct Rows {
+    T *p;
+    int64_t ld, end;  // row stride; elements from p to the end of the last row
+};
+
+template <typename T>
+__host__ __device__ __forceinline__ Rows<T> rows_of(T *p, int64_t ld, int64_t rows, int64_t width)
+{
+    return Rows<T>{p, ld, (rows - 1) * ld + width};
+}
+
+// Elements c .. c + min(n, 16) - 1 of row r.
+template <bool ANY, typename T>
+__device__ __forceinline__ void load_chunk(const Rows<const T> &t, int64_t r, int64_t c, int n, bool w32,
+                                           Raw<T, ANY> &raw)
+{
+    const int64_t at = r * t.ld + c;
+    if constexpr (ANY) load16(t.p + at, n, at >= 8 && at + 24 <= t.end, raw);
+    else load16(t.p + at, n, w32, raw);
+}
+
+// The first min(rest, 16) of f to row r from column c on.  `t` is the thread's
+// place among the `lanes` threads that hold consecutive chunks of the row.
+template <bool ANY, typename T>
+__device__ __forceinline__ void store_chunk(const Rows<T> &d, int64_t r, int64_t c, const float (&f)[16], int rest,
+                                            bool w32, int t, int lanes)
+{
+    T *p = d.p + r * d.ld + c;
+    if constexpr (ANY)
+        store16_any(p, f, rest, t == 0 || (threadIdx.x & 31) == 0, t == lanes - 1 || (threadIdx.x & 31) == 31);
+    else
+        store16(p, f, rest, w32);
+}
+
+// Elements from n on replaced (n >= 16: none).
+__device__ __forceinline__ void fill_from(float (&f)[16], int n, float v)
+{
+    if (n < 16) {
+#pragma unroll
+        for (int j = 0; j < 16; j++) f[j] = j < n ? f[j] : v;
+    }
 }
 
 // The largest magnitude of a block whose halves two neighbouring lanes hold.

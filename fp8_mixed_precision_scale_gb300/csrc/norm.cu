@@ -12,8 +12,7 @@
 // keeps xh, not x: its 8 bits then resolve xh itself however large the mean
 // is against the spread, and the backward needs no mean.
 //
-// Wide form (16-byte aligned rows and parameters, limited widths): a row stays
-// in the registers of its group of threads, 16 consecutive columns (a chunk) per
+// Wide form (up to NM_MAX_WIDE columns): a row stays in the registers of its group of threads, 16 consecutive columns (a chunk) per
 // thread and step; the group is a part of a warp or several warps with a named
 // barrier of their own.  One persistent block per SM holds as many groups as
 // its registers allow and one fp32 copy of the parameters in shared memory.
@@ -22,8 +21,8 @@
 // rows; wider rows (more columns than NM_MAX_FUSED) take a second read of dy
 // and x by columns instead.
 //
-// Narrow form (anything else): a block takes one row at a time and sweeps it
-// once per sum (the later sweeps hit L1/L2).
+// Wider rows still: a block takes one row at a time and sweeps it once per sum
+// (the later sweeps hit L1/L2).
 //
 // dw and db are left as column sums over row slices in the caller's workspace
 // and added in a fixed order by a last kernel: no atomics, the same bits every
@@ -110,10 +109,10 @@ __device__ __forceinline__ float2 block_sum(float a, float b)
     return t;
 }
 
-// Parameters c .. c + 15 (p 16-byte aligned), `absent` past the row.
+// Parameters c .. c + 15, `absent` past the row.
 __device__ __forceinline__ void param16(const void *p, int dtype, int c, int cols, float absent, float (&f)[16])
 {
-    if (!p || c + 16 > cols) {
+    if (!p || c + 16 > cols || (reinterpret_cast<uintptr_t>(p) & 15)) {
 #pragma unroll
         for (int j = 0; j < 16; j++) f[j] = c + j < cols ? param(p, dtype, c + j, absent) : absent;
     } else if (dtype == FP8_DTYPE_F32) {
@@ -235,7 +234,7 @@ __device__ __forceinline__ float sum16(const float (&f)[16])
 
 // A row in the registers of its group: thread t of G holds columns (k G + t) 16
 // .. + 15 for k < CH.
-template <typename TX, typename TY, int CH, bool MULTI>
+template <typename TX, typename TY, int CH, bool MULTI, bool ANY>
 __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
 {
     extern __shared__ __align__(16) float shared[];  // weight, bias
@@ -253,11 +252,11 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
     // iterations: `first` is the row of the first group among them
     int64_t r = (int64_t)blockIdx.x * groups + g.id;
     int64_t first = MULTI ? r : r - (threadIdx.x & 31) / G;
-    const TX *x = static_cast<const TX *>(a.x) + r * a.ld_x + g.t * 16;
-    TY *y = static_cast<TY *>(a.out) + r * a.ld_out + g.t * 16;
-    Raw16<TX> raw[CH];
+    const Rows<const TX> x = rows_of(static_cast<const TX *>(a.x), a.ld_x, a.rows, a.cols);
+    const Rows<TY> y{static_cast<TY *>(a.out), a.ld_out, 0};
+    Raw<TX, ANY> raw[CH];
 #pragma unroll
-    for (int k = 0; k < CH; k++) load16(x + k * G * 16, r < a.rows ? n[k] : 0, a.w32, raw[k]);
+    for (int k = 0; k < CH; k++) load_chunk<ANY>(x, r, (k * G + g.t) * 16, r < a.rows ? n[k] : 0, a.w32, raw[k]);
     params_to_shared(shared, a.weight, a.w_dtype, cols, chunks, 1.0f);
     if (a.bias) params_to_shared(shared + chunks * 16, a.bias, a.w_dtype, cols, chunks, 0.0f);
     if (MULTI)
@@ -269,12 +268,12 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
     for (; first < a.rows; first += step, r += step) {
         float f[CH][16];
         float v = 0.0f;
-        x += step * a.ld_x;
 #pragma unroll
         for (int k = 0; k < CH; k++) {
             unpack16(raw[k], f[k]);
+            if (ANY) fill_from(f[k], n[k], 0.0f);
             v += sum16(f[k]);
-            if (r + step < a.rows) load16(x + k * G * 16, n[k], a.w32, raw[k]);
+            if (r + step < a.rows) load_chunk<ANY>(x, r + step, (k * G + g.t) * 16, n[k], a.w32, raw[k]);
         }
         float mean = 0.0f;
         if (!a.rms) {
@@ -285,10 +284,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
 #pragma unroll
         for (int k = 0; k < CH; k++) {
             float2 acc[2] = {};
-            if (n[k] < 16) {  // columns past the row are as far from the mean as the mean is
-#pragma unroll
-                for (int j = 0; j < 16; j++) f[k][j] = j < n[k] ? f[k][j] : mean;
-            }
+            fill_from(f[k], n[k], mean);  // what is past the row adds nothing
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
                 const float2 d = add2(make_float2(f[k][j], f[k][j + 1]), make_float2(-mean, -mean));
@@ -335,33 +331,31 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
                 }
                 f[k][4 * q] = lo.x, f[k][4 * q + 1] = lo.y, f[k][4 * q + 2] = hi.x, f[k][4 * q + 3] = hi.y;
             }
-            store16(y + k * G * 16, f[k], live ? n[k] : 0, a.w32);
+            store_chunk<ANY>(y, r, i * 16, f[k], live ? cols - i * 16 : 0, a.w32, g.t, G);
         }
-        y += step * a.ld_out;
     }
 }
 
 // What a thread reads of a row in the backward: dy, and x or its checkpoint.
-template <typename TX, typename TY, bool CKPT>
+template <typename TX, typename TY, bool CKPT, bool ANY>
 struct RawBackward {
-    Raw16<TY> dy;
-    Raw16<TX> x;
-    uint4 q;
-    uint32_t s;
+    Raw<TY, ANY> dy;
+    Raw<TX, ANY> x;
 };
 
-template <typename TX, typename TY>
-struct RawBackward<TX, TY, true> {
-    Raw16<TY> dy;
+template <typename TX, typename TY, bool ANY>
+struct RawBackward<TX, TY, true, ANY> {
+    Raw<TY, ANY> dy;
     uint4 q;
     uint32_t s;
 };
 
 // Chunk i (n columns of it) of row r.
-template <typename TX, typename TY, bool CKPT>
-__device__ __forceinline__ void load_backward(const NormArgs &a, int64_t r, int i, int n, RawBackward<TX, TY, CKPT> &v)
+template <typename TX, typename TY, bool CKPT, bool ANY>
+__device__ __forceinline__ void load_backward(const NormArgs &a, int64_t r, int i, int n,
+                                              RawBackward<TX, TY, CKPT, ANY> &v)
 {
-    load16(static_cast<const TY *>(a.dy) + r * a.ld_dy + i * 16, n, a.w32, v.dy);
+    load_chunk<ANY>(rows_of(static_cast<const TY *>(a.dy), a.ld_dy, a.rows, a.cols), r, i * 16, n, a.w32, v.dy);
     if constexpr (CKPT) {
         v.q = make_uint4(0, 0, 0, 0);
         v.s = 127;
@@ -370,13 +364,20 @@ __device__ __forceinline__ void load_backward(const NormArgs &a, int64_t r, int 
             v.s = __ldg(a.s + r * a.ld_s + (i >> 1));
         }
     } else {
-        load16(static_cast<const TX *>(a.x) + r * a.ld_x + i * 16, n, a.w32, v.x);
+        load_chunk<ANY>(rows_of(static_cast<const TX *>(a.x), a.ld_x, a.rows, a.cols), r, i * 16, n, a.w32, v.x);
     }
 }
 
+template <typename TX, typename TY, bool CKPT, bool ANY>
+__device__ __forceinline__ void dy16(const RawBackward<TX, TY, CKPT, ANY> &v, int n, float (&d)[16])
+{
+    unpack16(v.dy, d);
+    if (ANY) fill_from(d, n, 0.0f);
+}
+
 // xh of a chunk; 0 past the row.
-template <typename TX, typename TY, bool CKPT>
-__device__ __forceinline__ void xhat16(const NormArgs &a, const RawBackward<TX, TY, CKPT> &v, int n, float mean,
+template <typename TX, typename TY, bool CKPT, bool ANY>
+__device__ __forceinline__ void xhat16(const NormArgs &a, const RawBackward<TX, TY, CKPT, ANY> &v, int n, float mean,
                                        float rstd, float (&xh)[16])
 {
     if constexpr (CKPT) {
@@ -384,10 +385,7 @@ __device__ __forceinline__ void xhat16(const NormArgs &a, const RawBackward<TX, 
         else decode16<FP8_E4M3FN>(v.q, ckpt_scale(v.s), xh);
     } else {
         unpack16(v.x, xh);
-        if (n < 16) {
-#pragma unroll
-            for (int j = 0; j < 16; j++) xh[j] = j < n ? xh[j] : mean;
-        }
+        fill_from(xh, n, mean);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
             const float2 d = mul2(add2(make_float2(xh[j], xh[j + 1]), make_float2(-mean, -mean)),
@@ -400,7 +398,7 @@ __device__ __forceinline__ void xhat16(const NormArgs &a, const RawBackward<TX, 
 // dx of whole rows; with ACC also this block's share of dw and db, in
 // registers until the last row and then added over the block's groups in
 // shared memory (in group order) into the block's slice of the workspace.
-template <typename TX, typename TY, int CH, bool MULTI, bool CKPT, bool ACC>
+template <typename TX, typename TY, int CH, bool MULTI, bool CKPT, bool ACC, bool ANY>
 __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a)
 {
     extern __shared__ __align__(16) float shared[];  // weight; at the end dw and db
@@ -416,7 +414,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
 
     int64_t r = (int64_t)blockIdx.x * groups + g.id;
     int64_t first = MULTI ? r : r - (threadIdx.x & 31) / G;
-    RawBackward<TX, TY, CKPT> raw[CH];
+    RawBackward<TX, TY, CKPT, ANY> raw[CH];
     float next_mean = 0.0f, next_rstd = 0.0f;
     const auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -441,7 +439,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
         const float rstd = next_rstd;
 #pragma unroll
         for (int k = 0; k < CH; k++) {
-            unpack16(raw[k].dy, gr[k]);
+            dy16(raw[k], n[k], gr[k]);
             xhat16(a, raw[k], n[k], next_mean, rstd, xh[k]);
         }
         if (first + step < a.rows) fetch(r + step);
@@ -472,7 +470,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
         sum = row_sum<MULTI>(sum, G, g, slot);
         slot ^= 1;
         const float c1 = a.rms ? 0.0f : -sum.x * inv_n * rstd, c2 = -sum.y * inv_n * rstd;
-        TX *dx = static_cast<TX *>(a.out) + r * a.ld_out;
+        const Rows<TX> dx{static_cast<TX *>(a.out), a.ld_out, 0};
 #pragma unroll
         for (int k = 0; k < CH; k++) {
 #pragma unroll
@@ -481,7 +479,8 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
                 o = fma2(make_float2(xh[k][j], xh[k][j + 1]), make_float2(c2, c2), o);
                 gr[k][j] = o.x, gr[k][j + 1] = o.y;
             }
-            store16(dx + (k * G + g.t) * 16, gr[k], r < a.rows ? n[k] : 0, a.w32);
+            const int c = (k * G + g.t) * 16;
+            store_chunk<ANY>(dx, r, c, gr[k], r < a.rows ? cols - c : 0, a.w32, g.t, G);
         }
     }
     if constexpr (ACC) {
@@ -521,7 +520,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
 
 // Column sums of rows too wide for the accumulators: a thread takes chunk i of
 // the rows of slice blockIdx.y.
-template <typename TX, typename TY, bool CKPT>
+template <typename TX, typename TY, bool CKPT, bool ANY>
 __global__ void __launch_bounds__(NM_THREADS) norm_dw_wide_kernel(NormArgs a)
 {
     const int cols = (int)a.cols, i = blockIdx.x * NM_THREADS + threadIdx.x;
@@ -529,10 +528,10 @@ __global__ void __launch_bounds__(NM_THREADS) norm_dw_wide_kernel(NormArgs a)
     if (n == 0) return;
     float2 dw[8] = {}, db[8] = {};
     for (int64_t r = blockIdx.y; r < a.rows; r += a.splits) {
-        RawBackward<TX, TY, CKPT> raw;
+        RawBackward<TX, TY, CKPT, ANY> raw;
         load_backward(a, r, i, n, raw);
         float d[16], xh[16];
-        unpack16(raw.dy, d);
+        dy16(raw, n, d);
         xhat16(a, raw, n, CKPT || a.rms ? 0.0f : __ldg(a.mean + r), CKPT ? 1.0f : __ldg(a.rstd + r), xh);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
@@ -746,24 +745,30 @@ static void launch_wide(K kernel, const WidePlan &p, int smem, const NormArgs &a
     kernel<<<p.grid, p.threads, smem, st>>>(a);
 }
 
-template <typename TX, typename TY>
-static void launch_forward(NormArgs a, cudaStream_t st)
+template <typename TX, typename TY, bool ANY>
+static void launch_forward_wide(NormArgs a, cudaStream_t st)
 {
-    if (a.cols > NM_MAX_WIDE || !rows_aligned(a.x, a.ld_x, sizeof(TX), 16) ||
-        !rows_aligned(a.out, a.ld_out, sizeof(TY), 16) || !aligned(a.weight, 16) || !aligned(a.bias, 16)) {
-        norm_forward_kernel<TX, TY><<<row_grid(a.rows), NM_THREADS, 0, st>>>(a);
-        return;
-    }
-    a.w32 = rows_aligned(a.x, a.ld_x, sizeof(TX), 32) && rows_aligned(a.out, a.ld_out, sizeof(TY), 32);
     const WidePlan p = wide_plan(a.rows, a.cols, 2, NM_BLOCK);
     a.G = p.G;
     const int smem = p.chunks * p.G * 16 * (int)sizeof(float) * (a.bias ? 2 : 1);
-    if (p.chunks == 1) launch_wide(norm_forward_wide_kernel<TX, TY, 1, false>, p, smem, a, st);
-    else if (!p.multi) launch_wide(norm_forward_wide_kernel<TX, TY, 2, false>, p, smem, a, st);
-    else launch_wide(norm_forward_wide_kernel<TX, TY, 2, true>, p, smem, a, st);
+    if (p.chunks == 1) launch_wide(norm_forward_wide_kernel<TX, TY, 1, false, ANY>, p, smem, a, st);
+    else if (!p.multi) launch_wide(norm_forward_wide_kernel<TX, TY, 2, false, ANY>, p, smem, a, st);
+    else launch_wide(norm_forward_wide_kernel<TX, TY, 2, true, ANY>, p, smem, a, st);
 }
 
-template <typename TX, typename TY, bool CKPT>
+template <typename TX, typename TY>
+static void launch_forward(NormArgs a, cudaStream_t st)
+{
+    const auto all_aligned = [&](int al) {
+        return rows_aligned(a.x, a.ld_x, sizeof(TX), al) && rows_aligned(a.out, a.ld_out, sizeof(TY), al);
+    };
+    a.w32 = all_aligned(32);
+    if (a.cols > NM_MAX_WIDE) norm_forward_kernel<TX, TY><<<row_grid(a.rows), NM_THREADS, 0, st>>>(a);
+    else if (all_aligned(16)) launch_forward_wide<TX, TY, false>(a, st);
+    else launch_forward_wide<TX, TY, true>(a, st);
+}
+
+template <typename TX, typename TY, bool CKPT, bool ANY>
 static void launch_backward_wide(NormArgs a, cudaStream_t st)
 {
     const bool grads = a.dweight || a.dbias, fused = a.cols <= NM_MAX_FUSED;
@@ -773,14 +778,14 @@ static void launch_backward_wide(NormArgs a, cudaStream_t st)
     if (fused) {
         a.splits = (int)p.grid;
         if (!grads) a.part = nullptr;
-        if (p.multi) launch_wide(norm_backward_wide_kernel<TX, TY, 1, true, CKPT, true>, p, 2 * vec, a, st);
-        else launch_wide(norm_backward_wide_kernel<TX, TY, 1, false, CKPT, true>, p, 2 * vec, a, st);
+        if (p.multi) launch_wide(norm_backward_wide_kernel<TX, TY, 1, true, CKPT, true, ANY>, p, 2 * vec, a, st);
+        else launch_wide(norm_backward_wide_kernel<TX, TY, 1, false, CKPT, true, ANY>, p, 2 * vec, a, st);
     } else {
-        launch_wide(norm_backward_wide_kernel<TX, TY, 2, true, CKPT, false>, p, vec, a, st);
+        launch_wide(norm_backward_wide_kernel<TX, TY, 2, true, CKPT, false, ANY>, p, vec, a, st);
         if (!grads) return;
         a.splits = wide_splits(a.rows, a.cols);
         const dim3 grid((unsigned)((a.cols + 16 * NM_THREADS - 1) / (16 * NM_THREADS)), (unsigned)a.splits);
-        norm_dw_wide_kernel<TX, TY, CKPT><<<grid, NM_THREADS, 0, st>>>(a);
+        norm_dw_wide_kernel<TX, TY, CKPT, ANY><<<grid, NM_THREADS, 0, st>>>(a);
     }
     if (grads) norm_dw_sum_kernel<<<(unsigned)((a.cols + NM_COLS - 1) / NM_COLS), NM_THREADS, 0, st>>>(a);
 }
@@ -792,10 +797,13 @@ static void launch_backward(NormArgs a, cudaStream_t st)
         return rows_aligned(a.dy, a.ld_dy, sizeof(TY), al) && rows_aligned(a.out, a.ld_out, sizeof(TX), al) &&
                rows_aligned(a.x, a.ld_x, sizeof(TX), al);
     };
-    if (a.rows > 0 && a.cols <= NM_MAX_WIDE && all_aligned(16) && aligned(a.weight, 16)) {
+    if (a.rows > 0 && a.cols <= NM_MAX_WIDE) {
         a.w32 = all_aligned(32);
-        if (a.x) launch_backward_wide<TX, TY, false>(a, st);
-        else launch_backward_wide<TX, TY, true>(a, st);
+        const bool any = !all_aligned(16);
+        if (a.x && any) launch_backward_wide<TX, TY, false, true>(a, st);
+        else if (a.x) launch_backward_wide<TX, TY, false, false>(a, st);
+        else if (any) launch_backward_wide<TX, TY, true, true>(a, st);
+        else launch_backward_wide<TX, TY, true, false>(a, st);
         return;
     }
     if (a.rows > 0) norm_dx_kernel<TX, TY><<<row_grid(a.rows), NM_THREADS, 0, st>>>(a);
