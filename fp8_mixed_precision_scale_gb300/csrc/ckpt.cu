@@ -84,12 +84,14 @@ __global__ void __launch_bounds__(CK_THREADS) checkpoint_kernel(CkArgs a)
     const bool in = p.chunk < a.parts * cpp;
     const int64_t part = a.parts == 1 ? 0 : p.chunk / cpp, c = (p.chunk - part * cpp) * 16;
     const int n = in ? chunk_columns(a.cols, c) : 0;
-    const Rows<const T> x = rows_of(static_cast<const T *>(a.x), a.ld_x, a.rows, a.parts * a.cols);
+    const T *x = static_cast<const T *>(a.x);
+    const int64_t end = rows_end(a.ld_x, a.rows, a.parts * a.cols);
     Raw<T, ANY> raw[STORE_UNROLL];
 #pragma unroll
     for (int k = 0; k < STORE_UNROLL; k++) {
         const int64_t r = p.row + (int64_t)k * p.ty;
-        load_chunk<ANY>(x, r, part * a.cols + c, r < a.rows ? n : 0, a.w32, raw[k]);
+        const int64_t at = r * a.ld_x + part * a.cols + c;
+        load_chunk<ANY>(x + at, r < a.rows ? n : 0, a.w32, at, end, raw[k]);
     }
 #pragma unroll
     for (int k = 0; k < STORE_UNROLL; k++) {
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(CK_THREADS) restore_kernel(CkArgs a)
     const int rest = in ? chunk_rest(a.cols, c) : 0;
     // a part's first and last chunk have no neighbours, whatever the lanes beside them hold
     const int lanes = 1 << a.geo.lg, t = threadIdx.x & (lanes - 1);
-    const Rows<T> x{static_cast<T *>(a.x), a.ld_x, 0};
+    T *x = static_cast<T *>(a.x) + part * a.cols + c;
     uint4 q[RESTORE_UNROLL];
     uint32_t s[RESTORE_UNROLL];
 #pragma unroll
@@ -131,8 +133,7 @@ __global__ void __launch_bounds__(CK_THREADS) restore_kernel(CkArgs a)
         const int64_t r = p.row + (int64_t)k * p.ty;
         float f[16];
         decode16<FMT>(q[k], ckpt_scale(s[k]), f);
-        store_chunk<ANY>(x, r, part * a.cols + c, f, r < a.rows ? rest : 0, a.w32, c == 0 ? 0 : t,
-                         rest <= 16 ? t + 1 : lanes);
+        store_chunk<ANY>(x + r * a.ld_x, f, r < a.rows ? rest : 0, a.w32, c == 0 ? 0 : t, rest <= 16 ? t + 1 : lanes);
     }
 }
 
@@ -145,14 +146,14 @@ __global__ void __launch_bounds__(CK_THREADS) swiglu_checkpoint_kernel(SwArgs a)
     const bool in = p.chunk < cpp;
     const int n = in ? chunk_columns(a.F, c) : 0, rest = in ? chunk_rest(a.F, c) : 0;
     const int lanes = 1 << a.geo.lg, t = threadIdx.x & (lanes - 1);
-    const Rows<const T> gu = rows_of(a.gate_up, a.ld, a.rows, 2 * a.F);
-    const Rows<T> hd{a.h, a.ld_h, 0};
+    const int64_t end = rows_end(a.ld, a.rows, 2 * a.F);
     Raw<T, ANY> gr[SWIGLU_UNROLL], ur[SWIGLU_UNROLL];
 #pragma unroll
     for (int k = 0; k < SWIGLU_UNROLL; k++) {
         const int64_t r = p.row + (int64_t)k * p.ty;
-        load_chunk<ANY>(gu, r, c, r < a.rows ? n : 0, a.w32, gr[k]);
-        load_chunk<ANY>(gu, r, a.F + c, r < a.rows ? n : 0, a.w32, ur[k]);
+        const int64_t at = r * a.ld + c;
+        load_chunk<ANY>(a.gate_up + at, r < a.rows ? n : 0, a.w32, at, end, gr[k]);
+        load_chunk<ANY>(a.gate_up + at + a.F, r < a.rows ? n : 0, a.w32, at + a.F, end, ur[k]);
     }
 #pragma unroll
     for (int k = 0; k < SWIGLU_UNROLL; k++) {
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(CK_THREADS) swiglu_checkpoint_kernel(SwArgs a)
         const uint32_t cg = ckpt_code(block_amax16(g), FMT), cu = ckpt_code(block_amax16(u), FMT);
 #pragma unroll
         for (int j = 0; j < 16; j++) h[j] = swiglu1(g[j], u[j]);
-        store_chunk<ANY>(hd, r, c, h, r < a.rows ? rest : 0, a.w32, t, lanes);
+        store_chunk<ANY>(a.h + r * a.ld_h + c, h, r < a.rows ? rest : 0, a.w32, t, lanes);
         if (!in || r >= a.rows) continue;
         uint8_t *q = a.q + r * a.ld_q + c;
         *reinterpret_cast<uint4 *>(q) = encode16<FMT>(g, ckpt_inv_scale(cg));
@@ -189,8 +190,7 @@ __global__ void __launch_bounds__(CK_THREADS) swiglu_backward_kernel(SwArgs a)
     const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16;
     const int n = chunk_columns(a.F, c), rest = chunk_rest(a.F, c);  // nothing past the row
     const int lanes = 1 << a.geo.lg, t = threadIdx.x & (lanes - 1);
-    const Rows<const T> gu = rows_of(a.gate_up, a.ld, a.rows, 2 * a.F), dhs = rows_of(a.dh, a.ld_dh, a.rows, a.F);
-    const Rows<T> dd{a.d, a.ld_d, 0}, hd{a.h, a.ld_h, 0};
+    const int64_t end = rows_end(a.ld, a.rows, 2 * a.F), end_dh = rows_end(a.ld_dh, a.rows, a.F);
     Raw<T, ANY> gr[BACKWARD_UNROLL], ur[BACKWARD_UNROLL], dr[BACKWARD_UNROLL];
     uint4 gq[BACKWARD_UNROLL], uq[BACKWARD_UNROLL];
     uint32_t gs[BACKWARD_UNROLL], us[BACKWARD_UNROLL];
@@ -209,10 +209,12 @@ __global__ void __launch_bounds__(CK_THREADS) swiglu_backward_kernel(SwArgs a)
                 us[k] = __ldg(s + (cpp >> 1));
             }
         } else {
-            load_chunk<ANY>(gu, r, c, have, a.w32, gr[k]);
-            load_chunk<ANY>(gu, r, a.F + c, have, a.w32, ur[k]);
+            const int64_t at = r * a.ld + c;
+            load_chunk<ANY>(a.gate_up + at, have, a.w32, at, end, gr[k]);
+            load_chunk<ANY>(a.gate_up + at + a.F, have, a.w32, at + a.F, end, ur[k]);
         }
-        load_chunk<ANY>(dhs, r, c, have, a.w32, dr[k]);
+        const int64_t at = r * a.ld_dh + c;
+        load_chunk<ANY>(a.dh + at, have, a.w32, at, end_dh, dr[k]);
     }
 #pragma unroll
     for (int k = 0; k < BACKWARD_UNROLL; k++) {
@@ -237,9 +239,10 @@ __global__ void __launch_bounds__(CK_THREADS) swiglu_backward_kernel(SwArgs a)
             d[j] = h.x, d[j + 1] = h.y;
         }
         const int have = r < a.rows ? rest : 0;
-        if (a.h) store_chunk<ANY>(hd, r, c, d, have, a.w32, t, lanes);
-        store_chunk<ANY>(dd, r, c, g, have, a.w32, t, lanes);
-        store_chunk<ANY>(dd, r, a.F + c, u, have, a.w32, t, lanes);
+        T *out = a.d + r * a.ld_d + c;
+        if (a.h) store_chunk<ANY>(a.h + r * a.ld_h + c, d, have, a.w32, t, lanes);
+        store_chunk<ANY>(out, g, have, a.w32, t, lanes);
+        store_chunk<ANY>(out + a.F, u, have, a.w32, t, lanes);
     }
 }
 

@@ -369,36 +369,29 @@ struct RawOf<T, true> {
 template <typename T, bool ANY>
 using Raw = typename RawOf<T, ANY>::type;
 
-// A tensor whose rows threads read or write in chunks of 16 elements.
-template <typename T>
-struct Rows {
-    T *p;
-    int64_t ld, end;  // row stride; elements from p to the end of the last row
-};
+// Whether the 16 elements from `at` on (counted from a tensor's first) have 16
+// bytes of the tensor before and after them; `end`: elements of the tensor
+// from its first to its last row's end.
+__device__ __forceinline__ bool well_inside(int64_t at, int64_t end) { return at >= 8 && at + 24 <= end; }
 
-template <typename T>
-__host__ __device__ __forceinline__ Rows<T> rows_of(T *p, int64_t ld, int64_t rows, int64_t width)
+__host__ __device__ __forceinline__ int64_t rows_end(int64_t ld, int64_t rows, int64_t width)
 {
-    return Rows<T>{p, ld, (rows - 1) * ld + width};
+    return (rows - 1) * ld + width;
 }
 
-// Elements c .. c + min(n, 16) - 1 of row r.
+// min(n, 16) elements from p on; `at` and `end` as in well_inside.
 template <bool ANY, typename T>
-__device__ __forceinline__ void load_chunk(const Rows<const T> &t, int64_t r, int64_t c, int n, bool w32,
-                                           Raw<T, ANY> &raw)
+__device__ __forceinline__ void load_chunk(const T *p, int n, bool w32, int64_t at, int64_t end, Raw<T, ANY> &raw)
 {
-    const int64_t at = r * t.ld + c;
-    if constexpr (ANY) load16(t.p + at, n, at >= 8 && at + 24 <= t.end, raw);
-    else load16(t.p + at, n, w32, raw);
+    if constexpr (ANY) load16(p, n, well_inside(at, end), raw);
+    else load16(p, n, w32, raw);
 }
 
-// The first min(rest, 16) of f to row r from column c on.  `t` is the thread's
-// place among the `lanes` threads that hold consecutive chunks of the row.
+// The first min(rest, 16) of f to p.  `t` is the thread's place among the
+// `lanes` threads that hold consecutive chunks of the row.
 template <bool ANY, typename T>
-__device__ __forceinline__ void store_chunk(const Rows<T> &d, int64_t r, int64_t c, const float (&f)[16], int rest,
-                                            bool w32, int t, int lanes)
+__device__ __forceinline__ void store_chunk(T *p, const float (&f)[16], int rest, bool w32, int t, int lanes)
 {
-    T *p = d.p + r * d.ld + c;
     if constexpr (ANY)
         store16_any(p, f, rest, t == 0 || (threadIdx.x & 31) == 0, t == lanes - 1 || (threadIdx.x & 31) == 31);
     else

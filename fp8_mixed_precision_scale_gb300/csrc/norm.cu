@@ -252,11 +252,14 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
     // iterations: `first` is the row of the first group among them
     int64_t r = (int64_t)blockIdx.x * groups + g.id;
     int64_t first = MULTI ? r : r - (threadIdx.x & 31) / G;
-    const Rows<const TX> x = rows_of(static_cast<const TX *>(a.x), a.ld_x, a.rows, a.cols);
-    const Rows<TY> y{static_cast<TY *>(a.out), a.ld_out, 0};
+    int64_t at = r * a.ld_x + g.t * 16;  // of the row to load next, in x
+    const int64_t end = rows_end(a.ld_x, a.rows, a.cols);
+    const TX *x = static_cast<const TX *>(a.x) + at;
+    TY *y = static_cast<TY *>(a.out) + r * a.ld_out + g.t * 16;
     Raw<TX, ANY> raw[CH];
 #pragma unroll
-    for (int k = 0; k < CH; k++) load_chunk<ANY>(x, r, (k * G + g.t) * 16, r < a.rows ? n[k] : 0, a.w32, raw[k]);
+    for (int k = 0; k < CH; k++)
+        load_chunk<ANY>(x + k * G * 16, r < a.rows ? n[k] : 0, a.w32, at + k * G * 16, end, raw[k]);
     params_to_shared(shared, a.weight, a.w_dtype, cols, chunks, 1.0f);
     if (a.bias) params_to_shared(shared + chunks * 16, a.bias, a.w_dtype, cols, chunks, 0.0f);
     if (MULTI)
@@ -268,12 +271,15 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
     for (; first < a.rows; first += step, r += step) {
         float f[CH][16];
         float v = 0.0f;
+        x += step * a.ld_x;
+        at += step * a.ld_x;
 #pragma unroll
         for (int k = 0; k < CH; k++) {
             unpack16(raw[k], f[k]);
             if (ANY) fill_from(f[k], n[k], 0.0f);
             v += sum16(f[k]);
-            if (r + step < a.rows) load_chunk<ANY>(x, r + step, (k * G + g.t) * 16, n[k], a.w32, raw[k]);
+            if (r + step < a.rows)
+                load_chunk<ANY>(x + k * G * 16, n[k], a.w32, at + k * G * 16, end, raw[k]);
         }
         float mean = 0.0f;
         if (!a.rms) {
@@ -331,8 +337,9 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
                 }
                 f[k][4 * q] = lo.x, f[k][4 * q + 1] = lo.y, f[k][4 * q + 2] = hi.x, f[k][4 * q + 3] = hi.y;
             }
-            store_chunk<ANY>(y, r, i * 16, f[k], live ? cols - i * 16 : 0, a.w32, g.t, G);
+            store_chunk<ANY>(y + k * G * 16, f[k], live ? cols - i * 16 : 0, a.w32, g.t, G);
         }
+        y += step * a.ld_out;
     }
 }
 
@@ -355,7 +362,8 @@ template <typename TX, typename TY, bool CKPT, bool ANY>
 __device__ __forceinline__ void load_backward(const NormArgs &a, int64_t r, int i, int n,
                                               RawBackward<TX, TY, CKPT, ANY> &v)
 {
-    load_chunk<ANY>(rows_of(static_cast<const TY *>(a.dy), a.ld_dy, a.rows, a.cols), r, i * 16, n, a.w32, v.dy);
+    const int64_t at_dy = r * a.ld_dy + i * 16;
+    load_chunk<ANY>(static_cast<const TY *>(a.dy) + at_dy, n, a.w32, at_dy, rows_end(a.ld_dy, a.rows, a.cols), v.dy);
     if constexpr (CKPT) {
         v.q = make_uint4(0, 0, 0, 0);
         v.s = 127;
@@ -364,7 +372,8 @@ __device__ __forceinline__ void load_backward(const NormArgs &a, int64_t r, int 
             v.s = __ldg(a.s + r * a.ld_s + (i >> 1));
         }
     } else {
-        load_chunk<ANY>(rows_of(static_cast<const TX *>(a.x), a.ld_x, a.rows, a.cols), r, i * 16, n, a.w32, v.x);
+        const int64_t at_x = r * a.ld_x + i * 16;
+        load_chunk<ANY>(static_cast<const TX *>(a.x) + at_x, n, a.w32, at_x, rows_end(a.ld_x, a.rows, a.cols), v.x);
     }
 }
 
@@ -470,7 +479,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
         sum = row_sum<MULTI>(sum, G, g, slot);
         slot ^= 1;
         const float c1 = a.rms ? 0.0f : -sum.x * inv_n * rstd, c2 = -sum.y * inv_n * rstd;
-        const Rows<TX> dx{static_cast<TX *>(a.out), a.ld_out, 0};
+        TX *dx = static_cast<TX *>(a.out) + r * a.ld_out;
 #pragma unroll
         for (int k = 0; k < CH; k++) {
 #pragma unroll
@@ -480,7 +489,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
                 gr[k][j] = o.x, gr[k][j + 1] = o.y;
             }
             const int c = (k * G + g.t) * 16;
-            store_chunk<ANY>(dx, r, c, gr[k], r < a.rows ? cols - c : 0, a.w32, g.t, G);
+            store_chunk<ANY>(dx + c, gr[k], r < a.rows ? cols - c : 0, a.w32, g.t, G);
         }
     }
     if constexpr (ACC) {
@@ -495,6 +504,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
                     db[0][j] = add2(db[0][j], make_float2(__shfl_xor_sync(0xffffffffu, db[0][j].x, d),
                                                           __shfl_xor_sync(0xffffffffu, db[0][j].y, d)));
                 }
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sums' blocks may start
         // turns: the groups, or the warps of groups already added up in lanes
         const int turns = MULTI ? groups : blockDim.x >> 5, mine = MULTI ? g.id : threadIdx.x >> 5;
         float2 *sw = reinterpret_cast<float2 *>(shared), *sb = sw + chunks * 8;
@@ -643,31 +653,52 @@ __global__ void __launch_bounds__(NM_THREADS) norm_dw_kernel(NormArgs a)
     }
 }
 
-// The slices' sums: 32 columns a block, eight threads a column that each add
-// every eighth slice.
-__global__ void __launch_bounds__(NM_THREADS) norm_dw_sum_kernel(NormArgs a)
+// The slices' sums: 32 columns a block, 32 threads a column that each add every
+// 32nd slice, so that a few loads are the whole chain.  Launched while the
+// kernel that writes the slices may still run (programmatic dependent launch):
+// it waits for that kernel's end before it reads them.
+constexpr int NM_SUM_LANES = 32;
+
+__global__ void __launch_bounds__(NM_COLS * NM_SUM_LANES) norm_dw_sum_kernel(NormArgs a)
 {
-    __shared__ float2 part[NM_LANES][NM_COLS];
+    __shared__ float2 part[NM_SUM_LANES][NM_COLS + 1];
     const int tc = threadIdx.x % NM_COLS, tr = threadIdx.x / NM_COLS;
     const int64_t c = (int64_t)blockIdx.x * NM_COLS + tc;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float dw = 0.0f, db = 0.0f;
     if (c < a.cols) {
-#pragma unroll 8
-        for (int i = tr; i < a.splits; i += NM_LANES) {
+#pragma unroll 4
+        for (int i = tr; i < a.splits; i += NM_SUM_LANES) {
             dw += a.part[((int64_t)i * 2) * a.cols + c];
             db += a.part[((int64_t)i * 2 + 1) * a.cols + c];
         }
     }
     part[tr][tc] = make_float2(dw, db);
     __syncthreads();
-    if (tr != 0 || c >= a.cols) return;
+    // warp w adds up column w, its lanes the slices
+    float2 v = part[tc][tr];
 #pragma unroll
-    for (int i = 1; i < NM_LANES; i++) {
-        dw += part[i][tc].x;
-        db += part[i][tc].y;
+    for (int d = 16; d > 0; d >>= 1)
+        v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d)));
+    const int64_t out = (int64_t)blockIdx.x * NM_COLS + tr;
+    if (tc == 0 && out < a.cols) {
+        set_param(a.dweight, a.w_dtype, out, v.x);
+        set_param(a.dbias, a.w_dtype, out, v.y);
     }
-    set_param(a.dweight, a.w_dtype, c, dw);
-    set_param(a.dbias, a.w_dtype, c, db);
+}
+
+static void launch_dw_sum(NormArgs a, cudaStream_t st)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.cols + NM_COLS - 1) / NM_COLS));
+    cfg.blockDim = dim3(NM_COLS * NM_SUM_LANES);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, norm_dw_sum_kernel, a);
 }
 
 // Row slices of the narrow column sums: enough blocks for eight per SM, at
@@ -787,7 +818,7 @@ static void launch_backward_wide(NormArgs a, cudaStream_t st)
         const dim3 grid((unsigned)((a.cols + 16 * NM_THREADS - 1) / (16 * NM_THREADS)), (unsigned)a.splits);
         norm_dw_wide_kernel<TX, TY, CKPT, ANY><<<grid, NM_THREADS, 0, st>>>(a);
     }
-    if (grads) norm_dw_sum_kernel<<<(unsigned)((a.cols + NM_COLS - 1) / NM_COLS), NM_THREADS, 0, st>>>(a);
+    if (grads) launch_dw_sum(a, st);
 }
 
 template <typename TX, typename TY>
@@ -811,7 +842,7 @@ static void launch_backward(NormArgs a, cudaStream_t st)
     a.splits = narrow_splits(a.rows, a.cols);
     const dim3 grid((unsigned)((a.cols + NM_COLS - 1) / NM_COLS), (unsigned)a.splits);
     norm_dw_kernel<TX, TY><<<grid, NM_THREADS, 0, st>>>(a);
-    norm_dw_sum_kernel<<<(unsigned)((a.cols + NM_COLS - 1) / NM_COLS), NM_THREADS, 0, st>>>(a);
+    launch_dw_sum(a, st);
 }
 
 static bool good_dtype(int d) { return d >= FP8_DTYPE_BF16 && d <= FP8_DTYPE_F32; }
