@@ -99,6 +99,8 @@ def format_for(fp8: str, role: str) -> int:
 def load_library():
     """Load libfp8gb.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -648,6 +650,13 @@ def blockwise_quantize(x: torch.Tensor, fmt: int, block_rows: int, layouts: int 
 
 
 # --- norms, SwiGLU backward and 8-bit checkpoints -------------------------------
+# These call the library directly with addresses, not through the mirrors of the
+# entry points above: for a few tokens the host's time is what a call costs, and
+# the extra layer is a fifth of it.
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
 
 def _refuse(where: str, detail: str):
     raise Fp8Error(1, where, detail)
@@ -731,7 +740,9 @@ def checkpoint(x: torch.Tensor, fmt: int = E4M3FN, parts: int = 1, stream=None) 
     if parts < 1 or total % parts:
         _refuse(where, f"{total} columns are not {parts} equal parts")
     c = _new_checkpoint(rows, total // parts, parts, x.device, fmt)
-    fp8_checkpoint(x, DTYPES[x.dtype], rows, c.cols, ld, parts, fmt, c.q, c.q.shape[1], c.s, c.s.shape[1])
+    nb = _blocks(c.cols) * parts
+    _check(load_library().fp8_checkpoint(x.data_ptr(), DTYPES[x.dtype], rows, c.cols, ld, parts, fmt, c.q.data_ptr(),
+                                         nb * MX_BLOCK, c.s.data_ptr(), nb, _stream(None)), where)
     return c
 
 
@@ -746,9 +757,11 @@ def checkpoint_restore(c: Checkpoint, dtype: torch.dtype = torch.bfloat16, out=N
     if out is None:
         if dtype not in DTYPES:
             _refuse(where, f"cannot restore to {dtype}")
-        out = torch.empty((rows, c.parts * c.cols), dtype=dtype, device=c.q.device)
-    ld = _matrix(out, where, "out", rows, c.parts * c.cols)
-    fp8_checkpoint_restore(c.q, ld_q, c.s, ld_s, c.fmt, rows, c.cols, c.parts, out, DTYPES[out.dtype], ld)
+        out, ld = torch.empty((rows, c.parts * c.cols), dtype=dtype, device=c.q.device), c.parts * c.cols
+    else:
+        ld = _matrix(out, where, "out", rows, c.parts * c.cols)
+    _check(load_library().fp8_checkpoint_restore(c.q.data_ptr(), ld_q, c.s.data_ptr(), ld_s, c.fmt, rows, c.cols,
+                                                 c.parts, out.data_ptr(), DTYPES[out.dtype], ld, _stream(None)), where)
     return out
 
 
@@ -769,7 +782,10 @@ def swiglu_checkpoint(gate_up: torch.Tensor, fmt: int = E4M3FN, h_out=None, stre
     else:
         h, ld_h = h_out, _matrix(h_out, where, "h_out", rows, F, torch.bfloat16)
     c = _new_checkpoint(rows, F, 2, gate_up.device, fmt)
-    fp8_swiglu_checkpoint(gate_up, rows, F, ld, fmt, h, ld_h, c.q, c.q.shape[1], c.s, c.s.shape[1])
+    nb = 2 * _blocks(F)
+    _check(load_library().fp8_swiglu_checkpoint(gate_up.data_ptr(), rows, F, ld, fmt, h.data_ptr(), ld_h,
+                                                c.q.data_ptr(), nb * MX_BLOCK, c.s.data_ptr(), nb, _stream(None)),
+           where)
     return h, c
 
 
@@ -796,7 +812,8 @@ def swiglu_backward(dh: torch.Tensor, src, out=None, return_h: bool = False, str
         ld_d = _matrix(out, where, "out", rows, 2 * F, torch.bfloat16)
     if return_h:
         h = torch.empty((rows, F), dtype=torch.bfloat16, device=dh.device)
-    fp8_swiglu_backward(dh, ld_dh, gate_up, ld, q, ld_q, s, ld_s, fmt, rows, F, out, ld_d, h, F)
+    _check(load_library().fp8_swiglu_backward(dh.data_ptr(), ld_dh, _ptr(gate_up), ld, _ptr(q), ld_q, _ptr(s), ld_s,
+                                              fmt, rows, F, out.data_ptr(), ld_d, _ptr(h), F, _stream(None)), where)
     return (out, h) if return_h else out
 
 
@@ -850,8 +867,10 @@ def norm_forward(x: torch.Tensor, weight=None, bias=None, kind: int = LAYER_NORM
     if checkpoint_fmt is not None:
         c = _new_checkpoint(rows, cols, 1, dev, checkpoint_fmt)
         q, s, fmt, nb = c.q, c.s, checkpoint_fmt, _blocks(cols)
-    fp8_norm_forward(x, DTYPES[x.dtype], ld, rows, cols, kind, eps, weight, bias, w_dtype, out, DTYPES[out_dtype], ld_y,
-                     mean, rstd, fmt, q, nb * MX_BLOCK, s, nb)
+    _check(load_library().fp8_norm_forward(x.data_ptr(), DTYPES[x.dtype], ld, rows, cols, kind, eps, _ptr(weight),
+                                           _ptr(bias), w_dtype, out.data_ptr(), DTYPES[out_dtype], ld_y, _ptr(mean),
+                                           rstd.data_ptr(), fmt, _ptr(q), nb * MX_BLOCK, _ptr(s), nb, _stream(None)),
+           where)
     return NormForward(out, mean, rstd, c)
 
 
@@ -900,8 +919,10 @@ def norm_backward(dy: torch.Tensor, src, mean, rstd: torch.Tensor, weight=None, 
         if (kind == LAYER_NORM if bias_grad is None else bias_grad) else None
     ws, n = None, 0
     if dw is not None or db is not None:
-        n = fp8_norm_workspace_bytes(rows, cols)
+        n = load_library().fp8_norm_workspace_bytes(rows, cols)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    fp8_norm_backward(dy, DTYPES[dy.dtype], ld_dy, x, ld_x, q, ld_q, s, ld_s, fmt, rows, cols, kind, mean, rstd,
-                      weight, DTYPES[w_dtype], out, DTYPES[dx_dtype], ld_dx, dw, db, ws, n)
+    _check(load_library().fp8_norm_backward(dy.data_ptr(), DTYPES[dy.dtype], ld_dy, _ptr(x), ld_x, _ptr(q), ld_q,
+                                            _ptr(s), ld_s, fmt, rows, cols, kind, _ptr(mean), rstd.data_ptr(),
+                                            _ptr(weight), DTYPES[w_dtype], out.data_ptr(), DTYPES[dx_dtype], ld_dx,
+                                            _ptr(dw), _ptr(db), _ptr(ws), n, _stream(None)), where)
     return NormBackward(out, dw, db)
