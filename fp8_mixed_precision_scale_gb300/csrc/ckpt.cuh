@@ -129,6 +129,13 @@ __device__ __forceinline__ uint4 ld_stream_16b(const void *p)
     return v;
 }
 
+__device__ __forceinline__ uint4 ld_shared_16b(uint32_t p)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+    return v;
+}
+
 __device__ __forceinline__ void st_32b(void *p, const uint4 &lo, const uint4 &hi)
 {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(lo.x), "r"(lo.y),

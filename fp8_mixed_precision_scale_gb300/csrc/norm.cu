@@ -155,7 +155,7 @@ __device__ __forceinline__ float4 param4(const float *src, int chunks, int i, in
 // in the group, and the group's shared slots for the sums.
 struct Group {
     int id, t;
-    float2 *part;  // [2][NM_GROUP_WARPS], zero beyond the group's warps
+    float2 *part;  // [2][2][NM_GROUP_WARPS], zero beyond the group's warps
 };
 
 template <bool MULTI>
@@ -169,7 +169,7 @@ __device__ __forceinline__ Group group_of(int G, float2 *parts)
         g.id = threadIdx.x >> (31 - __clz(G));
         g.t = threadIdx.x & (G - 1);
     }
-    g.part = parts + g.id * 2 * NM_GROUP_WARPS;
+    g.part = parts + g.id * 4 * NM_GROUP_WARPS;
     return g;
 }
 
@@ -187,7 +187,7 @@ __device__ __forceinline__ float2 row_sum(float2 v, int G, const Group &g, int s
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d)));
-        float2 *part = g.part + slot * NM_GROUP_WARPS;
+        float2 *part = g.part + slot * 2 * NM_GROUP_WARPS;
         if ((g.t & 31) == 0) part[g.t >> 5] = v;
         asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(G) : "memory");
         v = make_float2(0.0f, 0.0f);
@@ -209,7 +209,7 @@ __device__ __forceinline__ float row_sum(float v, int G, const Group &g, int slo
     } else {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-        float *part = reinterpret_cast<float *>(g.part + slot * NM_GROUP_WARPS);
+        float *part = reinterpret_cast<float *>(g.part + slot * 2 * NM_GROUP_WARPS);
         if ((g.t & 31) == 0) part[g.t >> 5] = v;
         asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(G) : "memory");
         float2 s = make_float2(0.0f, 0.0f);
@@ -220,6 +220,43 @@ __device__ __forceinline__ float row_sum(float v, int G, const Group &g, int slo
         }
         return s.x + s.y;
     }
+}
+
+// Sums of two rows' pairs.  In a whole warp the lanes trade values until each
+// holds a part of one, so that six shuffles do instead of twenty, and every
+// lane then adds up a share of the warps' sums.
+template <bool MULTI>
+__device__ __forceinline__ void row_sum(float2 (&v)[2], int G, const Group &g, int slot)
+{
+    if constexpr (!MULTI) {
+        v[0] = row_sum<false>(v[0], G, g, slot);
+        v[1] = row_sum<false>(v[1], G, g, slot);
+    } else {
+        const int lane = g.t & 31;
+        const bool low = (lane & 16) == 0, even = (lane & 8) == 0;
+        // lanes 0-15: row 0's pair, 16-31: row 1's
+        float2 p = low ? v[0] : v[1], o = low ? v[1] : v[0];
+        p = add2(p, make_float2(__shfl_xor_sync(0xffffffffu, o.x, 16), __shfl_xor_sync(0xffffffffu, o.y, 16)));
+        float u = (even ? p.x : p.y) + __shfl_xor_sync(0xffffffffu, even ? p.y : p.x, 8);
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
+        // value lane / 8 of the four, warp by warp
+        float *part = reinterpret_cast<float *>(g.part) + slot * 4 * NM_GROUP_WARPS;
+        if ((lane & 7) == 0) part[(lane >> 3) * NM_GROUP_WARPS + (g.t >> 5)] = u;
+        asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(G) : "memory");
+        const float2 w = reinterpret_cast<const float2 *>(part)[lane];  // two warps' sums of value lane / 8
+        u = w.x + w.y;
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
+        v[0] = make_float2(__shfl_sync(0xffffffffu, u, 0), __shfl_sync(0xffffffffu, u, 8));
+        v[1] = make_float2(__shfl_sync(0xffffffffu, u, 16), __shfl_sync(0xffffffffu, u, 24));
+    }
+}
+
+template <bool MULTI>
+__device__ __forceinline__ void row_sum(float2 (&v)[1], int G, const Group &g, int slot)
+{
+    v[0] = row_sum<MULTI>(v[0], G, g, slot);
 }
 
 __device__ __forceinline__ float sum16(const float (&f)[16])
@@ -238,7 +275,7 @@ template <typename TX, typename TY, int CH, bool MULTI, bool ANY>
 __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
 {
     extern __shared__ __align__(16) float shared[];  // weight, bias
-    __shared__ __align__(16) float2 parts[MULTI ? NM_MAX_GROUPS * 2 * NM_GROUP_WARPS : 1];
+    __shared__ __align__(16) float2 parts[MULTI ? NM_MAX_GROUPS * 4 * NM_GROUP_WARPS : 1];
     const int cols = (int)a.cols, G = a.G, chunks = CH * G;
     const Group g = group_of<MULTI>(G, parts);
     const int groups = MULTI ? blockDim.x / G : blockDim.x >> (31 - __clz(G));
@@ -263,7 +300,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
     params_to_shared(shared, a.weight, a.w_dtype, cols, chunks, 1.0f);
     if (a.bias) params_to_shared(shared + chunks * 16, a.bias, a.w_dtype, cols, chunks, 0.0f);
     if (MULTI)
-        for (int i = threadIdx.x; i < NM_MAX_GROUPS * 2 * NM_GROUP_WARPS; i += blockDim.x)
+        for (int i = threadIdx.x; i < NM_MAX_GROUPS * 4 * NM_GROUP_WARPS; i += blockDim.x)
             parts[i] = make_float2(0.0f, 0.0f);
     __syncthreads();
 
@@ -404,6 +441,63 @@ __device__ __forceinline__ void xhat16(const NormArgs &a, const RawBackward<TX, 
     }
 }
 
+// Rows ahead of the fused backward from x, in shared memory: each warp copies
+// its own columns of dy and x with cp.async into a ring, so the loads in flight
+// cost no registers and no block barrier, and the registers hold two rows at a
+// time, whose sums share one barrier and each other's latencies.  Against one
+// row ahead in registers: bf16 [8192, 5120] 61 -> 56 us, [65536, 1024] 75 -> 71,
+// [32768, 7168] 257 -> 250.  The backward from a checkpoint keeps the registers:
+// with a ring, its scale bytes' loads took [32768, 7168] from 241 to 260 us.
+// A copy instruction takes 512 consecutive bytes (a thread's own 32 as two
+// halves fetched every sector twice, 25 % slower than no ring); 16-byte unit u
+// of a warp's part is kept at u ^ (u / 8 % SLOTS), so that reading a thread's own
+// SLOTS units meets no bank twice.
+template <typename TX, typename TY>
+struct Ring {
+    static constexpr int dy_slots = sizeof(TY), x_slots = sizeof(TX), slots = dy_slots + x_slots;  // of 16 bytes
+    // rows a step, and steps in the ring: what 512 threads and the parameters of 8192 columns leave room for
+    static constexpr int rows = slots <= 4 ? 2 : 1;
+    static constexpr int stages = rows == 2 || slots >= 8 ? 2 : 3;
+};
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, int bytes)  // the rest of the 16: zeros
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// A thread's place in the copies of its warp: `lane` of it, or where the warp
+// holds several rows, place t of G in row `sub`.
+struct CopyPlace {
+    int t, G, sub;
+};
+
+// Bytes 0 .. valid - 1 of the warp's part of a row at `src` (zeros after).
+template <int SLOTS>
+__device__ __forceinline__ void copy_ahead(uint32_t dst, const void *src, int valid, const CopyPlace &c,
+                                           const void *anywhere)
+{
+#pragma unroll
+    for (int j = 0; j < SLOTS; j++) {
+        const int u = j * c.G + c.t, at = c.sub * SLOTS * c.G + u, bytes = max(0, min(16, valid - u * 16));
+        cp_async_16(dst + (at ^ (at >> 3 & (SLOTS - 1))) * 16,
+                    bytes ? static_cast<const char *>(src) + u * 16 : static_cast<const char *>(anywhere), bytes);
+    }
+}
+
+// Unit j of a lane's SLOTS.
+template <int SLOTS>
+__device__ __forceinline__ uint4 copied(uint32_t src, int lane, int j)
+{
+    const int at = SLOTS * lane + j;
+    return ld_shared_16b(src + (at ^ (at >> 3 & (SLOTS - 1))) * 16);
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // dx of whole rows; with ACC also this block's share of dw and db, in
 // registers until the last row and then added over the block's groups in
 // shared memory (in group order) into the block's slice of the workspace.
@@ -411,7 +505,7 @@ template <typename TX, typename TY, int CH, bool MULTI, bool CKPT, bool ACC, boo
 __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a)
 {
     extern __shared__ __align__(16) float shared[];  // weight; at the end dw and db
-    __shared__ __align__(16) float2 parts[MULTI ? NM_MAX_GROUPS * 2 * NM_GROUP_WARPS : 1];
+    __shared__ __align__(16) float2 parts[MULTI ? NM_MAX_GROUPS * 4 * NM_GROUP_WARPS : 1];
     const int cols = (int)a.cols, G = a.G, chunks = CH * G;
     const Group g = group_of<MULTI>(G, parts);
     const int groups = MULTI ? blockDim.x / G : blockDim.x >> (31 - __clz(G));
@@ -423,86 +517,149 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
 
     int64_t r = (int64_t)blockIdx.x * groups + g.id;
     int64_t first = MULTI ? r : r - (threadIdx.x & 31) / G;
-    RawBackward<TX, TY, CKPT, ANY> raw[CH];
-    float next_mean = 0.0f, next_rstd = 0.0f;
-    const auto fetch = [&](int64_t row) {
+    using R = Ring<TX, TY>;
+    constexpr int S = ACC && !CKPT && !ANY ? R::stages : 0;  // 0: one row ahead in registers
+    constexpr int ROWS = S ? R::rows : 1, AHEAD = S ? S - 1 : 1;
+    constexpr int U = ACC ? ROWS : CH;  // what a step works on: rows of a chunk, or chunks of a row
+    RawBackward<TX, TY, CKPT, ANY> raw[U];
+    float mean_q[AHEAD][ROWS] = {}, rstd_q[AHEAD][ROWS] = {};  // of the steps ahead, the next one first
+    const int lane = threadIdx.x & 31, col0 = MULTI ? (g.t >> 5) * 512 : 0;  // of the warp's part of the row
+    const CopyPlace cp{MULTI ? lane : g.t, MULTI ? 32 : G, MULTI ? 0 : lane / G};
+    constexpr int DY = R::dy_slots, X = R::x_slots;
+    // a warp's part of a row: 32 lanes of DY units, then of X
+    const uint32_t ring = smem_u32(shared + 2 * chunks * 16) + (threadIdx.x >> 5) * (R::slots * 512);
+    const uint32_t row_bytes = blockDim.x * R::slots * 16;
+    const auto fetch = [&](int64_t row0, int stage) {
 #pragma unroll
-        for (int k = 0; k < CH; k++) load_backward(a, row, k * G + g.t, row < a.rows ? n[k] : 0, raw[k]);
-        if (row < a.rows) {
-            next_rstd = __ldg(a.rstd + row);
-            if (!CKPT && !a.rms) next_mean = __ldg(a.mean + row);
+        for (int i = 0; i < ROWS; i++) {
+            const int64_t row = row0 + i * step;
+            const bool live = row < a.rows;
+            if constexpr (S == 0) {
+#pragma unroll
+                for (int k = 0; k < CH; k++) load_backward(a, row, k * G + g.t, live ? n[k] : 0, raw[k]);
+            } else {
+                const uint32_t at = ring + (stage * ROWS + i) * row_bytes;
+                const int have = live ? cols - col0 : 0;
+                copy_ahead<DY>(at, static_cast<const TY *>(a.dy) + row * a.ld_dy + col0, have * (int)sizeof(TY), cp,
+                               a.dy);
+                copy_ahead<X>(at + DY * 512, static_cast<const TX *>(a.x) + row * a.ld_x + col0,
+                              have * (int)sizeof(TX), cp, a.x);
+            }
+            if (live) {
+                rstd_q[AHEAD - 1][i] = __ldg(a.rstd + row);
+                if (!CKPT && !a.rms) mean_q[AHEAD - 1][i] = __ldg(a.mean + row);
+            }
         }
+        if constexpr (S > 0) asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(r);
+    const auto advance = [&]() {
+#pragma unroll
+        for (int q = 0; q + 1 < AHEAD; q++)
+#pragma unroll
+            for (int i = 0; i < ROWS; i++) {
+                mean_q[q][i] = mean_q[q + 1][i];
+                rstd_q[q][i] = rstd_q[q + 1][i];
+            }
+    };
+#pragma unroll
+    for (int q = 0; q < AHEAD; q++) {
+        if (q) advance();
+        fetch(r + q * ROWS * step, q);
+    }
     params_to_shared(shared, a.weight, a.w_dtype, cols, chunks, 1.0f);
     if (MULTI)
-        for (int i = threadIdx.x; i < NM_MAX_GROUPS * 2 * NM_GROUP_WARPS; i += blockDim.x)
+        for (int i = threadIdx.x; i < NM_MAX_GROUPS * 4 * NM_GROUP_WARPS; i += blockDim.x)
             parts[i] = make_float2(0.0f, 0.0f);
     __syncthreads();
 
-    float2 dw[ACC ? CH : 1][8] = {}, db[ACC ? CH : 1][8] = {};
-    int slot = 0;
-    for (; first < a.rows; first += step, r += step) {
-        float gr[CH][16], xh[CH][16];
-        float2 sum = make_float2(0.0f, 0.0f);
-        const float rstd = next_rstd;
+    float2 dw[8] = {}, db[8] = {};  // ACC: one chunk a thread
+    int slot = 0, stage = 0;
+    for (; first < a.rows; first += ROWS * step, r += ROWS * step) {
+        float gr[U][16], xh[U][16], rstd[ROWS];
+        if constexpr (S > 0) {
+            cp_async_wait<(S > 0 ? S - 2 : 0)>();
+            __syncwarp();  // every lane's copies of these rows have arrived
 #pragma unroll
-        for (int k = 0; k < CH; k++) {
-            dy16(raw[k], n[k], gr[k]);
-            xhat16(a, raw[k], n[k], next_mean, rstd, xh[k]);
+            for (int i = 0; i < ROWS; i++) {
+                const uint32_t at = ring + (stage * ROWS + i) * row_bytes;
+#pragma unroll
+                for (int j = 0; j < DY; j++) raw[i].dy.v[j] = copied<DY>(at, lane, j);
+#pragma unroll
+                for (int j = 0; j < X; j++) raw[i].x.v[j] = copied<X>(at + DY * 512, lane, j);
+            }
+            __syncwarp();  // and are read before their place is taken, a step later
         }
-        if (first + step < a.rows) fetch(r + step);
 #pragma unroll
-        for (int k = 0; k < CH; k++) {
-            float2 s1[2] = {}, s2[2] = {};
+        for (int k = 0; k < U; k++) {
+            const int i = ACC ? k : 0, c = ACC ? 0 : k;
+            rstd[i] = rstd_q[0][i];
+            dy16(raw[k], n[c], gr[k]);
+            xhat16(a, raw[k], n[c], mean_q[0][i], rstd[i], xh[k]);
+        }
+        advance();
+        if (S > 0 || first + step < a.rows) {
+            // into the place of the step before this one
+            fetch(r + AHEAD * ROWS * step, stage == 0 ? S - 1 : stage - 1);
+            if (S > 0) stage = stage + 1 == S ? 0 : stage + 1;
+        }
+        float2 sum[ROWS] = {};
+        float2 s1[U][2] = {}, s2[U][2] = {};
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const float4 w = param4(shared, chunks, k * G + g.t, q);
+        for (int q = 0; q < 4; q++) {
+            float4 w;
+#pragma unroll
+            for (int k = 0; k < U; k++) {
+                if (k == 0 || !ACC) w = param4(shared, chunks, (ACC ? 0 : k * G) + g.t, q);
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     const int j = 4 * q + 2 * h;
                     const float2 d = make_float2(gr[k][j], gr[k][j + 1]), x2 = make_float2(xh[k][j], xh[k][j + 1]);
                     if constexpr (ACC) {
-                        dw[k][j / 2] = fma2(d, x2, dw[k][j / 2]);
-                        db[k][j / 2] = add2(db[k][j / 2], d);
+                        dw[j / 2] = fma2(d, x2, dw[j / 2]);
+                        db[j / 2] = add2(db[j / 2], d);
                     }
                     const float2 p = mul2(d, h ? make_float2(w.z, w.w) : make_float2(w.x, w.y));
-                    s1[h] = add2(s1[h], p);
-                    s2[h] = fma2(p, x2, s2[h]);
+                    s1[k][h] = add2(s1[k][h], p);
+                    s2[k][h] = fma2(p, x2, s2[k][h]);
                     gr[k][j] = p.x, gr[k][j + 1] = p.y;
                 }
             }
-            s1[0] = add2(s1[0], s1[1]);
-            s2[0] = add2(s2[0], s2[1]);
-            sum = add2(sum, make_float2(s1[0].x + s1[0].y, s2[0].x + s2[0].y));
         }
-        sum = row_sum<MULTI>(sum, G, g, slot);
-        slot ^= 1;
-        const float c1 = a.rms ? 0.0f : -sum.x * inv_n * rstd, c2 = -sum.y * inv_n * rstd;
-        TX *dx = static_cast<TX *>(a.out) + r * a.ld_out;
 #pragma unroll
-        for (int k = 0; k < CH; k++) {
+        for (int k = 0; k < U; k++) {
+            const float2 p = add2(s1[k][0], s1[k][1]), q = add2(s2[k][0], s2[k][1]);
+            sum[ACC ? k : 0] = add2(sum[ACC ? k : 0], make_float2(p.x + p.y, q.x + q.y));
+        }
+        row_sum<MULTI>(sum, G, g, slot);
+        slot ^= 1;
+#pragma unroll
+        for (int k = 0; k < U; k++) {
+            const int i = ACC ? k : 0, c = ACC ? g.t : k * G + g.t;
+            const int64_t row = r + i * step;
+            const float c1 = a.rms ? 0.0f : -sum[i].x * inv_n * rstd[i], c2 = -sum[i].y * inv_n * rstd[i];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-                float2 o = fma2(make_float2(gr[k][j], gr[k][j + 1]), make_float2(rstd, rstd), make_float2(c1, c1));
+                float2 o = fma2(make_float2(gr[k][j], gr[k][j + 1]), make_float2(rstd[i], rstd[i]),
+                                make_float2(c1, c1));
                 o = fma2(make_float2(xh[k][j], xh[k][j + 1]), make_float2(c2, c2), o);
                 gr[k][j] = o.x, gr[k][j + 1] = o.y;
             }
-            const int c = (k * G + g.t) * 16;
-            store_chunk<ANY>(dx + c, gr[k], r < a.rows ? cols - c : 0, a.w32, g.t, G);
+            store_chunk<ANY>(static_cast<TX *>(a.out) + row * a.ld_out + c * 16, gr[k],
+                             row < a.rows ? cols - c * 16 : 0, a.w32, g.t, G);
         }
     }
     if constexpr (ACC) {
+        cp_async_wait<0>();
         if (!a.part) return;
         const int lanes = MULTI ? 32 : G;  // lanes that hold different columns
         if (!MULTI)
             for (int d = 16; d >= G; d >>= 1)
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
-                    dw[0][j] = add2(dw[0][j], make_float2(__shfl_xor_sync(0xffffffffu, dw[0][j].x, d),
-                                                          __shfl_xor_sync(0xffffffffu, dw[0][j].y, d)));
-                    db[0][j] = add2(db[0][j], make_float2(__shfl_xor_sync(0xffffffffu, db[0][j].x, d),
-                                                          __shfl_xor_sync(0xffffffffu, db[0][j].y, d)));
+                    dw[j] = add2(dw[j], make_float2(__shfl_xor_sync(0xffffffffu, dw[j].x, d),
+                                                          __shfl_xor_sync(0xffffffffu, dw[j].y, d)));
+                    db[j] = add2(db[j], make_float2(__shfl_xor_sync(0xffffffffu, db[j].x, d),
+                                                          __shfl_xor_sync(0xffffffffu, db[j].y, d)));
                 }
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sums' blocks may start
         // turns: the groups, or the warps of groups already added up in lanes
@@ -514,8 +671,8 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
 #pragma unroll
                 for (int j = 0; j < 8; j++) {  // pair j of every chunk together: no bank conflicts
                     const int at = j * chunks + g.t;
-                    sw[at] = turn ? add2(sw[at], dw[0][j]) : dw[0][j];
-                    sb[at] = turn ? add2(sb[at], db[0][j]) : db[0][j];
+                    sw[at] = turn ? add2(sw[at], dw[j]) : dw[j];
+                    sb[at] = turn ? add2(sb[at], db[j]) : db[j];
                 }
             }
         }
@@ -809,8 +966,10 @@ static void launch_backward_wide(NormArgs a, cudaStream_t st)
     if (fused) {
         a.splits = (int)p.grid;
         if (!grads) a.part = nullptr;
-        if (p.multi) launch_wide(norm_backward_wide_kernel<TX, TY, 1, true, CKPT, true, ANY>, p, 2 * vec, a, st);
-        else launch_wide(norm_backward_wide_kernel<TX, TY, 1, false, CKPT, true, ANY>, p, 2 * vec, a, st);
+        using R = Ring<TX, TY>;
+        const int ring = CKPT || ANY ? 0 : R::stages * R::rows * R::slots * 16 * (int)p.threads, smem = 2 * vec + ring;
+        if (p.multi) launch_wide(norm_backward_wide_kernel<TX, TY, 1, true, CKPT, true, ANY>, p, smem, a, st);
+        else launch_wide(norm_backward_wide_kernel<TX, TY, 1, false, CKPT, true, ANY>, p, smem, a, st);
     } else {
         launch_wide(norm_backward_wide_kernel<TX, TY, 2, true, CKPT, false, ANY>, p, vec, a, st);
         if (!grads) return;
