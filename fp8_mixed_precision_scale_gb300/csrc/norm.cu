@@ -441,23 +441,21 @@ __device__ __forceinline__ void xhat16(const NormArgs &a, const RawBackward<TX, 
     }
 }
 
-// Rows ahead of the fused backward from x, in shared memory: each warp copies
-// its own columns of dy and x with cp.async into a ring, so the loads in flight
-// cost no registers and no block barrier, and the registers hold two rows at a
-// time, whose sums share one barrier and each other's latencies.  Against one
-// row ahead in registers: bf16 [8192, 5120] 61 -> 56 us, [65536, 1024] 75 -> 71,
-// [32768, 7168] 257 -> 250.  The backward from a checkpoint keeps the registers:
-// with a ring, its scale bytes' loads took [32768, 7168] from 241 to 260 us.
+// Rows ahead of the fused backward, in shared memory: each warp copies its own
+// columns of dy and of x (or the codes) with cp.async into a ring, so the loads
+// in flight cost no registers and no block barrier, and the registers hold two
+// rows at a time, whose sums share one barrier and each other's latencies.
 // A copy instruction takes 512 consecutive bytes (a thread's own 32 as two
 // halves fetched every sector twice, 25 % slower than no ring); 16-byte unit u
 // of a warp's part is kept at u ^ (u / 8 % SLOTS), so that reading a thread's own
 // SLOTS units meets no bank twice.
-template <typename TX, typename TY>
+template <typename TX, typename TY, bool CKPT>
 struct Ring {
-    static constexpr int dy_slots = sizeof(TY), x_slots = sizeof(TX), slots = dy_slots + x_slots;  // of 16 bytes
+    static constexpr int dy_slots = sizeof(TY), x_slots = CKPT ? 1 : (int)sizeof(TX);  // of 16 bytes
+    static constexpr int slots = dy_slots + x_slots;
     // rows a step, and steps in the ring: what 512 threads and the parameters of 8192 columns leave room for
     static constexpr int rows = slots <= 4 ? 2 : 1;
-    static constexpr int stages = rows == 2 || slots >= 8 ? 2 : 3;
+    static constexpr int stages = CKPT && rows == 1 ? 0 : rows == 2 || slots >= 8 ? 2 : 3;  // 0: no ring
 };
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, int bytes)  // the rest of the 16: zeros
@@ -517,12 +515,17 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
 
     int64_t r = (int64_t)blockIdx.x * groups + g.id;
     int64_t first = MULTI ? r : r - (threadIdx.x & 31) / G;
-    using R = Ring<TX, TY>;
-    constexpr int S = ACC && !CKPT && !ANY ? R::stages : 0;  // 0: one row ahead in registers
+    using R = Ring<TX, TY, CKPT>;
+    constexpr int S = ACC && !ANY ? R::stages : 0;  // 0: one row ahead in registers
     constexpr int ROWS = S ? R::rows : 1, AHEAD = S ? S - 1 : 1;
     constexpr int U = ACC ? ROWS : CH;  // what a step works on: rows of a chunk, or chunks of a row
     RawBackward<TX, TY, CKPT, ANY> raw[U];
-    float mean_q[AHEAD][ROWS] = {}, rstd_q[AHEAD][ROWS] = {};  // of the steps ahead, the next one first
+    // statistics of the steps ahead, the next one first.  Two rows in whole
+    // warps: one register, lanes 4 i to 4 i + 3 holding rstd and mean of row 0
+    // and of row 1 (a value that is spilled on arrival is waited for)
+    constexpr bool LANES = MULTI && ROWS == 2;
+    float mean_q[AHEAD][ROWS] = {}, rstd_q[AHEAD][ROWS] = {}, stat = 0.0f;
+    uint32_t scale = 127;
     const int lane = threadIdx.x & 31, col0 = MULTI ? (g.t >> 5) * 512 : 0;  // of the warp's part of the row
     const CopyPlace cp{MULTI ? lane : g.t, MULTI ? 32 : G, MULTI ? 0 : lane / G};
     constexpr int DY = R::dy_slots, X = R::x_slots;
@@ -542,13 +545,25 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
                 const int have = live ? cols - col0 : 0;
                 copy_ahead<DY>(at, static_cast<const TY *>(a.dy) + row * a.ld_dy + col0, have * (int)sizeof(TY), cp,
                                a.dy);
-                copy_ahead<X>(at + DY * 512, static_cast<const TX *>(a.x) + row * a.ld_x + col0,
-                              have * (int)sizeof(TX), cp, a.x);
+                if constexpr (CKPT)
+                    copy_ahead<X>(at + DY * 512, a.q + row * a.ld_q + col0, have > 0 ? have + 15 & ~15 : 0, cp, a.q);
+                else
+                    copy_ahead<X>(at + DY * 512, static_cast<const TX *>(a.x) + row * a.ld_x + col0,
+                                  have * (int)sizeof(TX), cp, a.x);
             }
-            if (live) {
+            if (live && !LANES) {
                 rstd_q[AHEAD - 1][i] = __ldg(a.rstd + row);
                 if (!CKPT && !a.rms) mean_q[AHEAD - 1][i] = __ldg(a.mean + row);
             }
+        }
+        if (LANES) {
+            const int64_t row = row0 + (lane >> 1 & 1) * step;
+            if (row < a.rows) stat = __ldg((lane & 1 && !CKPT && !a.rms ? a.mean : a.rstd) + row);
+        }
+        if (CKPT && S > 0) {
+            // the scale byte of a block's two lanes: the even lane's of row 0, the odd lane's of row 1
+            const int64_t row = row0 + (lane & 1) * step;
+            if (row < a.rows && n[0]) scale = __ldg(a.s + row * a.ld_s + (g.t >> 1));
         }
         if constexpr (S > 0) asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -584,17 +599,28 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
                 const uint32_t at = ring + (stage * ROWS + i) * row_bytes;
 #pragma unroll
                 for (int j = 0; j < DY; j++) raw[i].dy.v[j] = copied<DY>(at, lane, j);
+                if constexpr (CKPT) {
+                    raw[i].q = copied<X>(at + DY * 512, lane, 0);
+                    const uint32_t s = __shfl_sync(0xffffffffu, scale, lane & ~1 | i);
+                    raw[i].s = r + i * step < a.rows ? s : 127u;
+                } else {
 #pragma unroll
-                for (int j = 0; j < X; j++) raw[i].x.v[j] = copied<X>(at + DY * 512, lane, j);
+                    for (int j = 0; j < X; j++) raw[i].x.v[j] = copied<X>(at + DY * 512, lane, j);
+                }
             }
             __syncwarp();  // and are read before their place is taken, a step later
         }
 #pragma unroll
         for (int k = 0; k < U; k++) {
             const int i = ACC ? k : 0, c = ACC ? 0 : k;
+            float mean = mean_q[0][i];
             rstd[i] = rstd_q[0][i];
+            if (LANES) {
+                rstd[i] = __shfl_sync(0xffffffffu, stat, 2 * i);
+                mean = CKPT || a.rms ? 0.0f : __shfl_sync(0xffffffffu, stat, 2 * i + 1);
+            }
             dy16(raw[k], n[c], gr[k]);
-            xhat16(a, raw[k], n[c], mean_q[0][i], rstd[i], xh[k]);
+            xhat16(a, raw[k], n[c], mean, rstd[i], xh[k]);
         }
         advance();
         if (S > 0 || first + step < a.rows) {
@@ -603,7 +629,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
             if (S > 0) stage = stage + 1 == S ? 0 : stage + 1;
         }
         float2 sum[ROWS] = {};
-        float2 s1[U][2] = {}, s2[U][2] = {};
+        float2 s1[U] = {}, s2[U] = {};
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             float4 w;
@@ -619,17 +645,15 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
                         db[j / 2] = add2(db[j / 2], d);
                     }
                     const float2 p = mul2(d, h ? make_float2(w.z, w.w) : make_float2(w.x, w.y));
-                    s1[k][h] = add2(s1[k][h], p);
-                    s2[k][h] = fma2(p, x2, s2[k][h]);
+                    s1[k] = add2(s1[k], p);
+                    s2[k] = fma2(p, x2, s2[k]);
                     gr[k][j] = p.x, gr[k][j + 1] = p.y;
                 }
             }
         }
 #pragma unroll
-        for (int k = 0; k < U; k++) {
-            const float2 p = add2(s1[k][0], s1[k][1]), q = add2(s2[k][0], s2[k][1]);
-            sum[ACC ? k : 0] = add2(sum[ACC ? k : 0], make_float2(p.x + p.y, q.x + q.y));
-        }
+        for (int k = 0; k < U; k++)
+            sum[ACC ? k : 0] = add2(sum[ACC ? k : 0], make_float2(s1[k].x + s1[k].y, s2[k].x + s2[k].y));
         row_sum<MULTI>(sum, G, g, slot);
         slot ^= 1;
 #pragma unroll
@@ -966,8 +990,8 @@ static void launch_backward_wide(NormArgs a, cudaStream_t st)
     if (fused) {
         a.splits = (int)p.grid;
         if (!grads) a.part = nullptr;
-        using R = Ring<TX, TY>;
-        const int ring = CKPT || ANY ? 0 : R::stages * R::rows * R::slots * 16 * (int)p.threads, smem = 2 * vec + ring;
+        using R = Ring<TX, TY, CKPT>;
+        const int ring = ANY ? 0 : R::stages * R::rows * R::slots * 16 * (int)p.threads, smem = 2 * vec + ring;
         if (p.multi) launch_wide(norm_backward_wide_kernel<TX, TY, 1, true, CKPT, true, ANY>, p, smem, a, st);
         else launch_wide(norm_backward_wide_kernel<TX, TY, 1, false, CKPT, true, ANY>, p, smem, a, st);
     } else {
