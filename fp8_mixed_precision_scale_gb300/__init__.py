@@ -920,7 +920,8 @@ def norm_backward(dy: torch.Tensor, src, mean, rstd: torch.Tensor, weight=None, 
     ws, n = None, 0
     if dw is not None or db is not None:
         n = load_library().fp8_norm_workspace_bytes(rows, cols)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        if n > 0:  # -1: a shape that the call refuses
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
     _check(load_library().fp8_norm_backward(dy.data_ptr(), DTYPES[dy.dtype], ld_dy, _ptr(x), ld_x, _ptr(q), ld_q,
                                             _ptr(s), ld_s, fmt, rows, cols, kind, _ptr(mean), rstd.data_ptr(),
                                             _ptr(weight), DTYPES[w_dtype], out.data_ptr(), DTYPES[dx_dtype], ld_dx,

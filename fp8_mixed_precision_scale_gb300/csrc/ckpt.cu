@@ -167,7 +167,12 @@ __global__ void __launch_bounds__(CK_THREADS) swiglu_checkpoint_kernel(SwArgs a)
         }
         const uint32_t cg = ckpt_code(block_amax16(g), FMT), cu = ckpt_code(block_amax16(u), FMT);
 #pragma unroll
-        for (int j = 0; j < 16; j++) h[j] = swiglu1(g[j], u[j]);
+        for (int j = 0; j < 16; j += 2) {
+            float2 e, sigma, silu;
+            silu2(make_float2(g[j], g[j + 1]), e, sigma, silu);
+            const float2 v = mul2(silu, make_float2(u[j], u[j + 1]));
+            h[j] = v.x, h[j + 1] = v.y;
+        }
         store_chunk<ANY>(a.h + r * a.ld_h + c, h, r < a.rows ? rest : 0, a.w32, t, lanes);
         if (!in || r >= a.rows) continue;
         uint8_t *q = a.q + r * a.ld_q + c;

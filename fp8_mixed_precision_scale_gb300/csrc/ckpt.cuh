@@ -501,22 +501,28 @@ __device__ __forceinline__ float rcp_fast(float v)  // 1 ulp; 0 where 1 / v is s
     return r;
 }
 
-// SwiGLU backward of two pairs (gate, up), with e = e^-gate and sigma =
-// 1 / (1 + e), so that 1 - sigma = e sigma without cancellation:
-//   silu = gate sigma,  d_gate = dh up (sigma + silu (1 - sigma)),
-//   d_up = dh silu,  h = silu up.
+// SiLU of two gates with what its derivative needs, from e = e^-gate:
+//   sigma = 1 / (1 + e),  1 - sigma = e sigma (no cancellation),  silu = gate sigma.
 // gate is held at -88 from below: e^88 is finite and its reciprocal flushes to
 // zero, so sigma, silu and the slope are 0 there (they are below 2^-119), also
 // for gate = -Inf, where the formula as written gives NaN.  NaN stays
 // NaN.  e and sigma err by less than 2^-17 relative, far inside the bf16
 // rounding of the results.
-__device__ __forceinline__ void swiglu_grad2(float2 g, float2 u, float2 dh, float2 &dg, float2 &du, float2 &h)
+__device__ __forceinline__ void silu2(float2 g, float2 &e, float2 &sigma, float2 &silu)
 {
     g = make_float2(max_nan(g.x, -88.0f), max_nan(g.y, -88.0f));
-    const float2 e = make_float2(__expf(-g.x), __expf(-g.y));
+    e = make_float2(__expf(-g.x), __expf(-g.y));
     const float2 d = add2(e, make_float2(1.0f, 1.0f));
-    const float2 s = make_float2(rcp_fast(d.x), rcp_fast(d.y));
-    const float2 silu = mul2(g, s);
+    sigma = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    silu = mul2(g, sigma);
+}
+
+// SwiGLU backward of two pairs (gate, up):
+//   d_gate = dh up (sigma + silu (1 - sigma)),  d_up = dh silu,  h = silu up.
+__device__ __forceinline__ void swiglu_grad2(float2 g, float2 u, float2 dh, float2 &dg, float2 &du, float2 &h)
+{
+    float2 e, s, silu;
+    silu2(g, e, s, silu);
     const float2 slope = fma2(silu, mul2(e, s), s);
     dg = mul2(mul2(dh, u), slope);
     du = mul2(dh, silu);

@@ -12,17 +12,14 @@
 // keeps xh, not x: its 8 bits then resolve xh itself however large the mean
 // is against the spread, and the backward needs no mean.
 //
-// Wide form (up to NM_MAX_WIDE columns): a row stays in the registers of its group of threads, 16 consecutive columns (a chunk) per
-// thread and step; the group is a part of a warp or several warps with a named
-// barrier of their own.  One persistent block per SM holds as many groups as
-// its registers allow and one fp32 copy of the parameters in shared memory.
-// A group issues the loads of its next row before it reduces the current one.
+// A row stays in the registers of its group of threads, 16 consecutive columns (a
+// chunk) per thread and step; the group is a part of a warp or several warps with
+// a named barrier of their own.  One persistent block per SM holds as many groups
+// as its registers allow and one fp32 copy of the parameters in shared memory.
+// A group issues the loads of its next rows before it reduces the current ones.
 // The backward accumulates dw and db of its columns in registers over all its
-// rows; wider rows (more columns than NM_MAX_FUSED) take a second read of dy
-// and x by columns instead.
-//
-// Wider rows still: a block takes one row at a time and sweeps it once per sum
-// (the later sweeps hit L1/L2).
+// rows.  A row wider than one block's registers is split over the blocks of a
+// cluster (2, 4 or 8), which trade their sums through distributed shared memory.
 //
 // dw and db are left as column sums over row slices in the caller's workspace
 // and added in a fixed order by a last kernel: no atomics, the same bits every
@@ -37,16 +34,13 @@
 
 namespace fp8gb {
 
-constexpr int NM_THREADS = 256;
-constexpr int NM_WARPS = NM_THREADS / 32;
-constexpr int NM_COLS = 32;   // columns of a column-sum block
-constexpr int NM_LANES = NM_THREADS / NM_COLS;  // its row lanes
-
-constexpr int NM_BLOCK = 512;          // threads of a wide block at most: 128 registers each
+constexpr int NM_COLS = 32;            // columns of a block of the last sums
+constexpr int NM_BLOCK = 512;          // threads of a block at most: 128 registers each
 constexpr int NM_MAX_GROUPS = 15;      // row groups with a named barrier each
 constexpr int NM_GROUP_WARPS = 16;     // warps of a row group at most
-constexpr int NM_MAX_WIDE = 2 * 16 * 32 * NM_GROUP_WARPS;  // columns of two chunks a thread
-constexpr int NM_MAX_FUSED = 16 * 32 * NM_GROUP_WARPS;     // of one
+constexpr int NM_MAX_RANKS = 8;        // blocks of a cluster at most
+constexpr int NM_PART = 16 * 32 * NM_GROUP_WARPS;  // columns one chunk a thread covers in a block
+constexpr int64_t NM_MAX_COLS = (int64_t)NM_PART * NM_MAX_RANKS;
 
 struct NormArgs {
     const void *x, *dy;  // x: forward input; backward: NULL when the checkpoint is read
@@ -66,9 +60,11 @@ struct NormArgs {
     float *part;  // [splits][2][cols] dw and db sums of row slices
     int splits;
     void *dweight, *dbias;
-    // wide forms
-    int G;    // threads of a row group
+    int G;          // threads of a row group
+    int ranks;      // blocks that share a row
+    int part_cols;  // columns of each of them but the last
     int w32;  // every row of the tensors starts on a 32-byte boundary
+    int64_t end_x, end_dy;  // elements from their start to the end of their last row
 };
 
 // Element i of a parameter vector; NULL gives `absent`.
@@ -86,27 +82,6 @@ __device__ __forceinline__ void set_param(void *p, int dtype, int64_t i, float v
     if (dtype == FP8_DTYPE_F32) static_cast<float *>(p)[i] = v;
     else if (dtype == FP8_DTYPE_F16) static_cast<__half *>(p)[i] = from_f32<__half>(v);
     else static_cast<__nv_bfloat16 *>(p)[i] = from_f32<__nv_bfloat16>(v);
-}
-
-// Sum of a pair over the block; every thread gets it.
-__device__ __forceinline__ float2 block_sum(float a, float b)
-{
-    __shared__ float2 part[NM_WARPS];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, d);
-        b += __shfl_xor_sync(0xffffffffu, b, d);
-    }
-    __syncthreads();  // the previous call's readers are done
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    float2 t = part[0];
-#pragma unroll
-    for (int w = 1; w < NM_WARPS; w++) {
-        t.x += part[w].x;
-        t.y += part[w].y;
-    }
-    return t;
 }
 
 // Parameters c .. c + 15, `absent` past the row.
@@ -259,6 +234,46 @@ __device__ __forceinline__ void row_sum(float2 (&v)[1], int G, const Group &g, i
     v[0] = row_sum<MULTI>(v[0], G, g, slot);
 }
 
+// A block's columns of a row that a cluster shares: the arguments as if they
+// were the whole row.
+template <typename TX, typename TY>
+__device__ __forceinline__ int take_part(NormArgs &a, int rank)
+{
+    const int base = rank * a.part_cols, cols = min(a.part_cols, (int)a.cols - base);
+    const int pb = base * (a.w_dtype == FP8_DTYPE_F32 ? 4 : 2);
+    if (a.x) a.x = static_cast<const TX *>(a.x) + base;
+    if (a.weight) a.weight = static_cast<const char *>(a.weight) + pb;
+    if (a.bias) a.bias = static_cast<const char *>(a.bias) + pb;
+    if (a.q) {
+        a.q += base;
+        a.s += base / FP8_MX_BLOCK;
+    }
+    if (a.part) a.part += base;
+    return cols;
+}
+
+// Sums of N values over the blocks of a cluster, in rank order; every thread
+// gets the same bits.  Called by all threads of every block equally often,
+// with alternating slots: a slot is written again only after every block has
+// passed the barrier in between, and so has read it.
+template <int N>
+__device__ __forceinline__ void cluster_sum(float (&v)[N], float (*trade)[NM_MAX_RANKS][4], int slot, int rank,
+                                            int ranks)
+{
+    if (threadIdx.x < ranks) {
+        const uint32_t dst = mapa_shared(smem_u32(trade[slot][rank]), threadIdx.x);
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + 4 * i), "f"(v[i]) : "memory");
+    }
+    cluster_sync();
+#pragma unroll
+    for (int i = 0; i < N; i++) v[i] = 0.0f;
+    for (int k = 0; k < ranks; k++)
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] += trade[slot][k][i];
+}
+
 __device__ __forceinline__ float sum16(const float (&f)[16])
 {
     float2 t[4];
@@ -271,26 +286,30 @@ __device__ __forceinline__ float sum16(const float (&f)[16])
 
 // A row in the registers of its group: thread t of G holds columns (k G + t) 16
 // .. + 15 for k < CH.
-template <typename TX, typename TY, int CH, bool MULTI, bool ANY>
-__global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
+template <typename TX, typename TY, int CH, bool MULTI, bool ANY, bool CLUSTER>
+__global__ void __launch_bounds__(NM_BLOCK) norm_forward_kernel(NormArgs a)
 {
     extern __shared__ __align__(16) float shared[];  // weight, bias
     __shared__ __align__(16) float2 parts[MULTI ? NM_MAX_GROUPS * 4 * NM_GROUP_WARPS : 1];
-    const int cols = (int)a.cols, G = a.G, chunks = CH * G;
+    __shared__ float trade[2][NM_MAX_RANKS][4];
+    const float inv_n = 1.0f / (float)a.cols;
+    const int rank = CLUSTER ? (int)cluster_ctarank() : 0;
+    const int64_t end = rows_end(a.ld_x, a.rows, a.cols) - (CLUSTER ? rank * a.part_cols : 0);
+    if (CLUSTER && a.out) a.out = static_cast<TY *>(a.out) + rank * a.part_cols;
+    const int cols = CLUSTER ? take_part<TX, TY>(a, rank) : (int)a.cols, G = a.G, chunks = CH * G;
     const Group g = group_of<MULTI>(G, parts);
-    const int groups = MULTI ? blockDim.x / G : blockDim.x >> (31 - __clz(G));
-    const int64_t step = (int64_t)gridDim.x * groups;
-    const float inv_n = 1.0f / (float)cols;
+    // one group of a block where the row has several
+    const int groups = CLUSTER ? 1 : MULTI ? blockDim.x / G : blockDim.x >> (31 - __clz(G));
+    const int64_t step = (int64_t)(CLUSTER ? gridDim.x / a.ranks : gridDim.x) * groups;
     int n[CH];  // columns of the row in each chunk, from 16 down to 0
 #pragma unroll
     for (int k = 0; k < CH; k++) n[k] = max(0, min(16, cols - (k * G + g.t) * 16));
 
     // the threads of a group (of a warp, where it holds several) run the same
     // iterations: `first` is the row of the first group among them
-    int64_t r = (int64_t)blockIdx.x * groups + g.id;
+    int64_t r = (int64_t)(CLUSTER ? blockIdx.x / a.ranks : blockIdx.x) * groups + g.id;
     int64_t first = MULTI ? r : r - (threadIdx.x & 31) / G;
     int64_t at = r * a.ld_x + g.t * 16;  // of the row to load next, in x
-    const int64_t end = rows_end(a.ld_x, a.rows, a.cols);
     const TX *x = static_cast<const TX *>(a.x) + at;
     TY *y = static_cast<TY *>(a.out) + r * a.ld_out + g.t * 16;
     Raw<TX, ANY> raw[CH];
@@ -320,7 +339,9 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
         }
         float mean = 0.0f;
         if (!a.rms) {
-            mean = row_sum<MULTI>(v, G, g, slot) * inv_n;
+            float t[1] = {row_sum<MULTI>(v, G, g, slot)};
+            if (CLUSTER) cluster_sum(t, trade, slot, rank, a.ranks);
+            mean = t[0] * inv_n;
             slot ^= 1;
         }
         v = 0.0f;
@@ -336,10 +357,12 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_forward_wide_kernel(NormArgs a)
             }
             v += (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
         }
-        const float rstd = 1.0f / sqrtf(row_sum<MULTI>(v, G, g, slot) * inv_n + a.eps);
+        float t[1] = {row_sum<MULTI>(v, G, g, slot)};
+        if (CLUSTER) cluster_sum(t, trade, slot, rank, a.ranks);
         slot ^= 1;
+        const float rstd = 1.0f / sqrtf(t[0] * inv_n + a.eps);
         const bool live = r < a.rows;
-        if (g.t == 0 && live) {
+        if (g.t == 0 && rank == 0 && live) {
             if (a.mean_out) a.mean_out[r] = mean;
             if (a.rstd_out) a.rstd_out[r] = rstd;
         }
@@ -400,7 +423,7 @@ __device__ __forceinline__ void load_backward(const NormArgs &a, int64_t r, int 
                                               RawBackward<TX, TY, CKPT, ANY> &v)
 {
     const int64_t at_dy = r * a.ld_dy + i * 16;
-    load_chunk<ANY>(static_cast<const TY *>(a.dy) + at_dy, n, a.w32, at_dy, rows_end(a.ld_dy, a.rows, a.cols), v.dy);
+    load_chunk<ANY>(static_cast<const TY *>(a.dy) + at_dy, n, a.w32, at_dy, a.end_dy, v.dy);
     if constexpr (CKPT) {
         v.q = make_uint4(0, 0, 0, 0);
         v.s = 127;
@@ -410,7 +433,7 @@ __device__ __forceinline__ void load_backward(const NormArgs &a, int64_t r, int 
         }
     } else {
         const int64_t at_x = r * a.ld_x + i * 16;
-        load_chunk<ANY>(static_cast<const TX *>(a.x) + at_x, n, a.w32, at_x, rows_end(a.ld_x, a.rows, a.cols), v.x);
+        load_chunk<ANY>(static_cast<const TX *>(a.x) + at_x, n, a.w32, at_x, a.end_x, v.x);
     }
 }
 
@@ -496,30 +519,36 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// dx of whole rows; with ACC also this block's share of dw and db, in
-// registers until the last row and then added over the block's groups in
-// shared memory (in group order) into the block's slice of the workspace.
-template <typename TX, typename TY, int CH, bool MULTI, bool CKPT, bool ACC, bool ANY>
-__global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a)
+// dx, and the block's share of dw and db: in registers until the last row, then
+// added over the block's groups in shared memory (in group order) into the
+// block's slice of the workspace.
+template <typename TX, typename TY, bool MULTI, bool CKPT, bool ANY, bool CLUSTER>
+__global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
 {
     extern __shared__ __align__(16) float shared[];  // weight; at the end dw and db
     __shared__ __align__(16) float2 parts[MULTI ? NM_MAX_GROUPS * 4 * NM_GROUP_WARPS : 1];
-    const int cols = (int)a.cols, G = a.G, chunks = CH * G;
+    __shared__ float trade[2][NM_MAX_RANKS][4];
+    const float inv_n = 1.0f / (float)a.cols;
+    const int rank = CLUSTER ? (int)cluster_ctarank() : 0, row_cols = (int)a.cols;
+    if (CLUSTER) {
+        a.end_x -= rank * a.part_cols;
+        a.end_dy -= rank * a.part_cols;
+        a.dy = static_cast<const TY *>(a.dy) + rank * a.part_cols;
+        a.out = static_cast<TX *>(a.out) + rank * a.part_cols;
+    }
+    const int cols = CLUSTER ? take_part<TX, TY>(a, rank) : (int)a.cols, G = a.G;
     const Group g = group_of<MULTI>(G, parts);
-    const int groups = MULTI ? blockDim.x / G : blockDim.x >> (31 - __clz(G));
-    const int64_t step = (int64_t)gridDim.x * groups;
-    const float inv_n = 1.0f / (float)cols;
-    int n[CH];
-#pragma unroll
-    for (int k = 0; k < CH; k++) n[k] = max(0, min(16, cols - (k * G + g.t) * 16));
+    const int groups = CLUSTER ? 1 : MULTI ? blockDim.x / G : blockDim.x >> (31 - __clz(G));
+    const int block = CLUSTER ? blockIdx.x / a.ranks : blockIdx.x;  // of those that split the rows
+    const int64_t step = (int64_t)(CLUSTER ? gridDim.x / a.ranks : gridDim.x) * groups;
+    const int n = max(0, min(16, cols - g.t * 16));  // columns of the row in this thread's chunk
 
-    int64_t r = (int64_t)blockIdx.x * groups + g.id;
+    int64_t r = (int64_t)block * groups + g.id;
     int64_t first = MULTI ? r : r - (threadIdx.x & 31) / G;
     using R = Ring<TX, TY, CKPT>;
-    constexpr int S = ACC && !ANY ? R::stages : 0;  // 0: one row ahead in registers
+    constexpr int S = ANY ? 0 : R::stages;  // 0: one row ahead in registers
     constexpr int ROWS = S ? R::rows : 1, AHEAD = S ? S - 1 : 1;
-    constexpr int U = ACC ? ROWS : CH;  // what a step works on: rows of a chunk, or chunks of a row
-    RawBackward<TX, TY, CKPT, ANY> raw[U];
+    RawBackward<TX, TY, CKPT, ANY> raw[ROWS];
     // statistics of the steps ahead, the next one first.  Two rows in whole
     // warps: one register, lanes 4 i to 4 i + 3 holding rstd and mean of row 0
     // and of row 1 (a value that is spilled on arrival is waited for)
@@ -530,7 +559,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
     const CopyPlace cp{MULTI ? lane : g.t, MULTI ? 32 : G, MULTI ? 0 : lane / G};
     constexpr int DY = R::dy_slots, X = R::x_slots;
     // a warp's part of a row: 32 lanes of DY units, then of X
-    const uint32_t ring = smem_u32(shared + 2 * chunks * 16) + (threadIdx.x >> 5) * (R::slots * 512);
+    const uint32_t ring = smem_u32(shared + 2 * G * 16) + (threadIdx.x >> 5) * (R::slots * 512);
     const uint32_t row_bytes = blockDim.x * R::slots * 16;
     const auto fetch = [&](int64_t row0, int stage) {
 #pragma unroll
@@ -538,8 +567,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
             const int64_t row = row0 + i * step;
             const bool live = row < a.rows;
             if constexpr (S == 0) {
-#pragma unroll
-                for (int k = 0; k < CH; k++) load_backward(a, row, k * G + g.t, live ? n[k] : 0, raw[k]);
+                load_backward(a, row, g.t, live ? n : 0, raw[0]);
             } else {
                 const uint32_t at = ring + (stage * ROWS + i) * row_bytes;
                 const int have = live ? cols - col0 : 0;
@@ -562,8 +590,9 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
         }
         if (CKPT && S > 0) {
             // the scale byte of a block's two lanes: the even lane's of row 0, the odd lane's of row 1
+            // (also where the odd lane's own columns are past the row)
             const int64_t row = row0 + (lane & 1) * step;
-            if (row < a.rows && n[0]) scale = __ldg(a.s + row * a.ld_s + (g.t >> 1));
+            if (row < a.rows && (g.t & ~1) * 16 < cols) scale = __ldg(a.s + row * a.ld_s + (g.t >> 1));
         }
         if constexpr (S > 0) asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -581,7 +610,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
         if (q) advance();
         fetch(r + q * ROWS * step, q);
     }
-    params_to_shared(shared, a.weight, a.w_dtype, cols, chunks, 1.0f);
+    params_to_shared(shared, a.weight, a.w_dtype, cols, G, 1.0f);
     if (MULTI)
         for (int i = threadIdx.x; i < NM_MAX_GROUPS * 4 * NM_GROUP_WARPS; i += blockDim.x)
             parts[i] = make_float2(0.0f, 0.0f);
@@ -590,7 +619,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
     float2 dw[8] = {}, db[8] = {};  // ACC: one chunk a thread
     int slot = 0, stage = 0;
     for (; first < a.rows; first += ROWS * step, r += ROWS * step) {
-        float gr[U][16], xh[U][16], rstd[ROWS];
+        float gr[ROWS][16], xh[ROWS][16], rstd[ROWS];
         if constexpr (S > 0) {
             cp_async_wait<(S > 0 ? S - 2 : 0)>();
             __syncwarp();  // every lane's copies of these rows have arrived
@@ -611,16 +640,15 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
             __syncwarp();  // and are read before their place is taken, a step later
         }
 #pragma unroll
-        for (int k = 0; k < U; k++) {
-            const int i = ACC ? k : 0, c = ACC ? 0 : k;
+        for (int i = 0; i < ROWS; i++) {
             float mean = mean_q[0][i];
             rstd[i] = rstd_q[0][i];
             if (LANES) {
                 rstd[i] = __shfl_sync(0xffffffffu, stat, 2 * i);
                 mean = CKPT || a.rms ? 0.0f : __shfl_sync(0xffffffffu, stat, 2 * i + 1);
             }
-            dy16(raw[k], n[c], gr[k]);
-            xhat16(a, raw[k], n[c], mean, rstd[i], xh[k]);
+            dy16(raw[i], n, gr[i]);
+            xhat16(a, raw[i], n, mean, rstd[i], xh[i]);
         }
         advance();
         if (S > 0 || first + step < a.rows) {
@@ -628,209 +656,85 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_wide_kernel(NormArgs a
             fetch(r + AHEAD * ROWS * step, stage == 0 ? S - 1 : stage - 1);
             if (S > 0) stage = stage + 1 == S ? 0 : stage + 1;
         }
-        float2 sum[ROWS] = {};
-        float2 s1[U] = {}, s2[U] = {};
+        float2 sum[ROWS], s1[ROWS] = {}, s2[ROWS] = {};
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            float4 w;
+            const float4 w = param4(shared, G, g.t, q);
 #pragma unroll
-            for (int k = 0; k < U; k++) {
-                if (k == 0 || !ACC) w = param4(shared, chunks, (ACC ? 0 : k * G) + g.t, q);
+            for (int i = 0; i < ROWS; i++) {
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     const int j = 4 * q + 2 * h;
-                    const float2 d = make_float2(gr[k][j], gr[k][j + 1]), x2 = make_float2(xh[k][j], xh[k][j + 1]);
-                    if constexpr (ACC) {
-                        dw[j / 2] = fma2(d, x2, dw[j / 2]);
-                        db[j / 2] = add2(db[j / 2], d);
-                    }
+                    const float2 d = make_float2(gr[i][j], gr[i][j + 1]), x2 = make_float2(xh[i][j], xh[i][j + 1]);
+                    dw[j / 2] = fma2(d, x2, dw[j / 2]);
+                    db[j / 2] = add2(db[j / 2], d);
                     const float2 p = mul2(d, h ? make_float2(w.z, w.w) : make_float2(w.x, w.y));
-                    s1[k] = add2(s1[k], p);
-                    s2[k] = fma2(p, x2, s2[k]);
-                    gr[k][j] = p.x, gr[k][j + 1] = p.y;
+                    s1[i] = add2(s1[i], p);
+                    s2[i] = fma2(p, x2, s2[i]);
+                    gr[i][j] = p.x, gr[i][j + 1] = p.y;
                 }
             }
         }
 #pragma unroll
-        for (int k = 0; k < U; k++)
-            sum[ACC ? k : 0] = add2(sum[ACC ? k : 0], make_float2(s1[k].x + s1[k].y, s2[k].x + s2[k].y));
+        for (int i = 0; i < ROWS; i++) sum[i] = make_float2(s1[i].x + s1[i].y, s2[i].x + s2[i].y);
         row_sum<MULTI>(sum, G, g, slot);
+        if constexpr (CLUSTER) {
+            float t[2 * ROWS];
+#pragma unroll
+            for (int i = 0; i < ROWS; i++) t[2 * i] = sum[i].x, t[2 * i + 1] = sum[i].y;
+            cluster_sum(t, trade, slot, rank, a.ranks);
+#pragma unroll
+            for (int i = 0; i < ROWS; i++) sum[i] = make_float2(t[2 * i], t[2 * i + 1]);
+        }
         slot ^= 1;
 #pragma unroll
-        for (int k = 0; k < U; k++) {
-            const int i = ACC ? k : 0, c = ACC ? g.t : k * G + g.t;
+        for (int i = 0; i < ROWS; i++) {
             const int64_t row = r + i * step;
             const float c1 = a.rms ? 0.0f : -sum[i].x * inv_n * rstd[i], c2 = -sum[i].y * inv_n * rstd[i];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-                float2 o = fma2(make_float2(gr[k][j], gr[k][j + 1]), make_float2(rstd[i], rstd[i]),
+                float2 o = fma2(make_float2(gr[i][j], gr[i][j + 1]), make_float2(rstd[i], rstd[i]),
                                 make_float2(c1, c1));
-                o = fma2(make_float2(xh[k][j], xh[k][j + 1]), make_float2(c2, c2), o);
-                gr[k][j] = o.x, gr[k][j + 1] = o.y;
+                o = fma2(make_float2(xh[i][j], xh[i][j + 1]), make_float2(c2, c2), o);
+                gr[i][j] = o.x, gr[i][j + 1] = o.y;
             }
-            store_chunk<ANY>(static_cast<TX *>(a.out) + row * a.ld_out + c * 16, gr[k],
-                             row < a.rows ? cols - c * 16 : 0, a.w32, g.t, G);
+            store_chunk<ANY>(static_cast<TX *>(a.out) + row * a.ld_out + g.t * 16, gr[i],
+                             row < a.rows ? cols - g.t * 16 : 0, a.w32, g.t, G);
         }
     }
-    if constexpr (ACC) {
-        cp_async_wait<0>();
-        if (!a.part) return;
-        const int lanes = MULTI ? 32 : G;  // lanes that hold different columns
-        if (!MULTI)
-            for (int d = 16; d >= G; d >>= 1)
+    cp_async_wait<0>();
+    if (!a.part) return;
+    const int lanes = MULTI ? 32 : G;  // lanes that hold different columns
+    if (!MULTI)
+        for (int d = 16; d >= G; d >>= 1)
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    dw[j] = add2(dw[j], make_float2(__shfl_xor_sync(0xffffffffu, dw[j].x, d),
-                                                          __shfl_xor_sync(0xffffffffu, dw[j].y, d)));
-                    db[j] = add2(db[j], make_float2(__shfl_xor_sync(0xffffffffu, db[j].x, d),
-                                                          __shfl_xor_sync(0xffffffffu, db[j].y, d)));
-                }
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sums' blocks may start
-        // turns: the groups, or the warps of groups already added up in lanes
-        const int turns = MULTI ? groups : blockDim.x >> 5, mine = MULTI ? g.id : threadIdx.x >> 5;
-        float2 *sw = reinterpret_cast<float2 *>(shared), *sb = sw + chunks * 8;
-        for (int turn = 0; turn < turns; turn++) {
-            __syncthreads();
-            if (turn == mine && (threadIdx.x & 31) < lanes) {
-#pragma unroll
-                for (int j = 0; j < 8; j++) {  // pair j of every chunk together: no bank conflicts
-                    const int at = j * chunks + g.t;
-                    sw[at] = turn ? add2(sw[at], dw[j]) : dw[j];
-                    sb[at] = turn ? add2(sb[at], db[j]) : db[j];
-                }
+            for (int j = 0; j < 8; j++) {
+                dw[j] = add2(dw[j], make_float2(__shfl_xor_sync(0xffffffffu, dw[j].x, d),
+                                                __shfl_xor_sync(0xffffffffu, dw[j].y, d)));
+                db[j] = add2(db[j], make_float2(__shfl_xor_sync(0xffffffffu, db[j].x, d),
+                                                __shfl_xor_sync(0xffffffffu, db[j].y, d)));
             }
-        }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sums' blocks may start
+    // turns: the groups, or the warps of groups already added up in lanes
+    const int turns = MULTI ? groups : blockDim.x >> 5, mine = MULTI ? g.id : threadIdx.x >> 5;
+    float2 *sw = reinterpret_cast<float2 *>(shared), *sb = sw + G * 8;
+    for (int turn = 0; turn < turns; turn++) {
         __syncthreads();
-        for (int c = threadIdx.x; c < cols; c += blockDim.x) {
-            const int at = ((c >> 1 & 7) * chunks + (c >> 4)) * 2 + (c & 1);
-            a.part[((int64_t)blockIdx.x * 2) * cols + c] = shared[at];
-            a.part[((int64_t)blockIdx.x * 2 + 1) * cols + c] = shared[chunks * 16 + at];
-        }
-    }
-}
-
-// Column sums of rows too wide for the accumulators: a thread takes chunk i of
-// the rows of slice blockIdx.y.
-template <typename TX, typename TY, bool CKPT, bool ANY>
-__global__ void __launch_bounds__(NM_THREADS) norm_dw_wide_kernel(NormArgs a)
-{
-    const int cols = (int)a.cols, i = blockIdx.x * NM_THREADS + threadIdx.x;
-    const int n = max(0, min(16, cols - i * 16));
-    if (n == 0) return;
-    float2 dw[8] = {}, db[8] = {};
-    for (int64_t r = blockIdx.y; r < a.rows; r += a.splits) {
-        RawBackward<TX, TY, CKPT, ANY> raw;
-        load_backward(a, r, i, n, raw);
-        float d[16], xh[16];
-        dy16(raw, n, d);
-        xhat16(a, raw, n, CKPT || a.rms ? 0.0f : __ldg(a.mean + r), CKPT ? 1.0f : __ldg(a.rstd + r), xh);
+        if (turn == mine && lane < lanes) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            dw[j] = fma2(make_float2(d[2 * j], d[2 * j + 1]), make_float2(xh[2 * j], xh[2 * j + 1]), dw[j]);
-            db[j] = add2(db[j], make_float2(d[2 * j], d[2 * j + 1]));
-        }
-    }
-    float *pw = a.part + ((int64_t)blockIdx.y * 2) * cols + i * 16, *pb = pw + cols;
-#pragma unroll
-    for (int j = 0; j < 16; j++)
-        if (j < n) {
-            pw[j] = j & 1 ? dw[j / 2].y : dw[j / 2].x;
-            pb[j] = j & 1 ? db[j / 2].y : db[j / 2].x;
-        }
-}
-
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(NM_THREADS) norm_forward_kernel(NormArgs a)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float n = (float)a.cols;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const TX *x = static_cast<const TX *>(a.x) + r * a.ld_x;
-        TY *y = static_cast<TY *>(a.out) + r * a.ld_out;
-        float mean = 0.0f;
-        if (!a.rms) {
-            float t = 0.0f;
-            for (int64_t c = threadIdx.x; c < a.cols; c += NM_THREADS) t += to_f32(x[c]);
-            mean = block_sum(t, 0.0f).x / n;
-        }
-        float t = 0.0f;
-        for (int64_t c = threadIdx.x; c < a.cols; c += NM_THREADS) {
-            const float d = to_f32(x[c]) - mean;
-            t = fmaf(d, d, t);
-        }
-        const float rstd = 1.0f / sqrtf(block_sum(t, 0.0f).x / n + a.eps);
-        if (threadIdx.x == 0) {
-            if (a.mean_out) a.mean_out[r] = mean;
-            if (a.rstd_out) a.rstd_out[r] = rstd;
-        }
-        for (int64_t b = warp; b * 32 < a.cols; b += NM_WARPS) {
-            const int64_t c = b * 32 + lane;
-            float xh = 0.0f;
-            if (c < a.cols) {
-                xh = (to_f32(x[c]) - mean) * rstd;
-                y[c] = from_f32<TY>(
-                    fmaf(xh, param(a.weight, a.w_dtype, c, 1.0f), param(a.bias, a.w_dtype, c, 0.0f)));
+            for (int j = 0; j < 8; j++) {  // pair j of every chunk together: no bank conflicts
+                const int at = j * G + g.t;
+                sw[at] = turn ? add2(sw[at], dw[j]) : dw[j];
+                sb[at] = turn ? add2(sb[at], db[j]) : db[j];
             }
-            if (a.q) ckpt_store_lane(xh, a.fmt, a.q + r * a.ld_q + b * 32, a.s + r * a.ld_s + b, lane);
         }
     }
-}
-
-// xh of one element, from x or from the checkpoint.
-template <typename TX>
-__device__ __forceinline__ float norm_xhat(const NormArgs &a, int64_t r, int64_t c, float mean, float rstd)
-{
-    if (a.x) return (to_f32(static_cast<const TX *>(a.x)[r * a.ld_x + c]) - mean) * rstd;
-    return ckpt_load_one(a.q + r * a.ld_q, a.s + r * a.ld_s, c, a.fmt);
-}
-
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(NM_THREADS) norm_dx_kernel(NormArgs a)
-{
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const TY *dy = static_cast<const TY *>(a.dy) + r * a.ld_dy;
-        TX *dx = static_cast<TX *>(a.out) + r * a.ld_out;
-        const float rstd = a.rstd[r], mean = a.x && !a.rms ? a.mean[r] : 0.0f;
-        float s1 = 0.0f, s2 = 0.0f;
-        for (int64_t c = threadIdx.x; c < a.cols; c += NM_THREADS) {
-            const float g = to_f32(dy[c]) * param(a.weight, a.w_dtype, c, 1.0f);
-            s1 += g;
-            s2 = fmaf(g, norm_xhat<TX>(a, r, c, mean, rstd), s2);
-        }
-        const float2 t = block_sum(s1, s2);
-        const float c1 = a.rms ? 0.0f : t.x / (float)a.cols, c2 = t.y / (float)a.cols;
-        for (int64_t c = threadIdx.x; c < a.cols; c += NM_THREADS) {
-            const float g = to_f32(dy[c]) * param(a.weight, a.w_dtype, c, 1.0f);
-            dx[c] = from_f32<TX>(rstd * (g - c1 - norm_xhat<TX>(a, r, c, mean, rstd) * c2));
-        }
-    }
-}
-
-// Column sums over the rows of slice blockIdx.y (rows blockIdx.y, + splits, ...
-// in groups of NM_LANES).
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(NM_THREADS) norm_dw_kernel(NormArgs a)
-{
-    __shared__ float2 part[NM_LANES][NM_COLS];
-    const int tc = threadIdx.x % NM_COLS, tr = threadIdx.x / NM_COLS;
-    const int64_t c = (int64_t)blockIdx.x * NM_COLS + tc;
-    float dw = 0.0f, db = 0.0f;
-    if (c < a.cols)
-        for (int64_t r = (int64_t)blockIdx.y * NM_LANES + tr; r < a.rows; r += (int64_t)a.splits * NM_LANES) {
-            const float dy = to_f32(static_cast<const TY *>(a.dy)[r * a.ld_dy + c]);
-            const float mean = a.x && !a.rms ? a.mean[r] : 0.0f;
-            dw = fmaf(dy, norm_xhat<TX>(a, r, c, mean, a.x ? a.rstd[r] : 1.0f), dw);
-            db += dy;
-        }
-    part[tr][tc] = make_float2(dw, db);
     __syncthreads();
-    if (tr == 0 && c < a.cols) {
-        for (int i = 1; i < NM_LANES; i++) {
-            dw += part[i][tc].x;
-            db += part[i][tc].y;
-        }
-        a.part[((int64_t)blockIdx.y * 2) * a.cols + c] = dw;
-        a.part[((int64_t)blockIdx.y * 2 + 1) * a.cols + c] = db;
+    float *part = a.part + (int64_t)block * 2 * row_cols;
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+        const int at = ((c >> 1 & 7) * G + (c >> 4)) * 2 + (c & 1);
+        part[c] = shared[at];
+        part[row_cols + c] = shared[G * 16 + at];
     }
 }
 
@@ -868,8 +772,9 @@ __global__ void __launch_bounds__(NM_COLS * NM_SUM_LANES) norm_dw_sum_kernel(Nor
     }
 }
 
-static void launch_dw_sum(NormArgs a, cudaStream_t st)
+static void launch_dw_sum(NormArgs a, int slices, cudaStream_t st)
 {
+    a.splits = slices;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -882,90 +787,91 @@ static void launch_dw_sum(NormArgs a, cudaStream_t st)
     cudaLaunchKernelEx(&cfg, norm_dw_sum_kernel, a);
 }
 
-// Row slices of the narrow column sums: enough blocks for eight per SM, at
-// least NM_LANES rows each.
-static int narrow_splits(int64_t rows, int64_t cols)
-{
-    const int64_t tiles = (cols + NM_COLS - 1) / NM_COLS;
-    int64_t want = ((int64_t)num_sms() * 8 + tiles - 1) / tiles;
-    const int64_t most = (rows + NM_LANES - 1) / NM_LANES;
-    if (want > most) want = most;
-    return want < 1 ? 1 : (int)want;
-}
-
-// Row slices of the wide column sums: four blocks per SM, 16 rows a slice.
-static int wide_splits(int64_t rows, int64_t cols)
-{
-    const int64_t tiles = (cols + 16 * NM_THREADS - 1) / (16 * NM_THREADS);
-    int64_t want = ((int64_t)num_sms() * 4 + tiles - 1) / tiles;
-    if (want > rows / 16) want = rows / 16;
-    return want < 1 ? 1 : (int)want;
-}
-
-static unsigned row_grid(int64_t rows)
-{
-    const int64_t cap = (int64_t)num_sms() * 8;
-    return (unsigned)(rows < cap ? rows : cap);
-}
-
 static bool rows_aligned(const void *p, int64_t ld, int size, int al)
 {
     return !p || (aligned(p, al) && ld * size % al == 0);
 }
 
-// Row groups and blocks of a wide kernel.
-struct WidePlan {
-    bool multi;       // groups of several warps
-    int chunks, G;    // chunks a thread, threads a group
+// Row groups, blocks and clusters of a launch.
+struct Plan {
+    bool multi;      // groups of several warps
+    int chunks, G;   // chunks a thread, threads a group
+    int ranks;       // blocks that share a row
+    int part_cols;   // columns of a block
     unsigned threads, grid;
+    int slices;      // of the rows, one a block (or cluster): slices of the workspace too
 };
 
 // `chunks` chunks a thread where a warp's lanes do not cover the row (one where
-// they do), at most `most` threads a block.  Few rows are spread over the SMs
-// before a second group joins a block.
-static WidePlan wide_plan(int64_t rows, int64_t cols, int chunks, int most)
+// they do).  Few rows are spread over the SMs before a second group joins a
+// block.
+static Plan make_plan(int64_t rows, int64_t cols, int chunks)
 {
-    WidePlan p;
-    const int64_t need = (cols + 15) / 16;
+    Plan p;
+    p.ranks = 1;
+    while ((int64_t)NM_PART * chunks * p.ranks < cols) p.ranks *= 2;
+    // whole warps of columns, so that only the last block has fewer
+    const int64_t share = (cols + p.ranks - 1) / p.ranks, whole = 512 * chunks;
+    p.part_cols = (int)(p.ranks == 1 ? cols : (share + whole - 1) / whole * whole);
+    const int need = (p.part_cols + 15) / 16;
     p.chunks = need > 32 ? chunks : 1;
     p.multi = need > 32 * p.chunks;
     int groups;
     if (p.multi) {
-        p.G = (int)((need + 32 * p.chunks - 1) / (32 * p.chunks)) * 32;
-        groups = most / p.G;
+        p.G = (need + 32 * p.chunks - 1) / (32 * p.chunks) * 32;
+        groups = NM_BLOCK / p.G;
         if (groups > NM_MAX_GROUPS) groups = NM_MAX_GROUPS;
     } else {
         p.G = 2;  // at least two lanes: a checkpoint block's halves
         while (p.G * p.chunks < need) p.G *= 2;
-        groups = most / p.G;
+        groups = NM_BLOCK / p.G;
     }
     const int64_t per_sm = (rows + num_sms() - 1) / num_sms();
     if (groups > per_sm) groups = (int)per_sm;
     if (!p.multi) groups = (groups * p.G + 31) / 32 * 32 / p.G;  // whole warps
-    if (groups < 1) groups = 1;
+    if (groups < 1 || p.ranks > 1) groups = 1;
     p.threads = (unsigned)(groups * p.G);
-    const int64_t blocks = (rows + groups - 1) / groups;
-    p.grid = (unsigned)(blocks < num_sms() ? blocks : num_sms());
+    const int64_t most = num_sms() / p.ranks, blocks = (rows + groups - 1) / groups;
+    p.slices = (int)(blocks < most ? blocks : most < 1 ? 1 : most);
+    p.grid = (unsigned)(p.slices * p.ranks);
     return p;
 }
 
 template <typename K>
-static void launch_wide(K kernel, const WidePlan &p, int smem, const NormArgs &a, cudaStream_t st)
+static void launch(K kernel, const Plan &p, int smem, NormArgs a, cudaStream_t st)
 {
+    a.G = p.G;
+    a.ranks = p.ranks;
+    a.part_cols = p.part_cols;
     // 48 KB without asking, the kernel's own few KB among them
     if (smem > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    kernel<<<p.grid, p.threads, smem, st>>>(a);
+    if (p.ranks == 1) {
+        kernel<<<p.grid, p.threads, smem, st>>>(a);
+        return;
+    }
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)p.ranks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid);
+    cfg.blockDim = dim3(p.threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <typename TX, typename TY, bool ANY>
-static void launch_forward_wide(NormArgs a, cudaStream_t st)
+static void launch_forward_as(const NormArgs &a, cudaStream_t st)
 {
-    const WidePlan p = wide_plan(a.rows, a.cols, 2, NM_BLOCK);
-    a.G = p.G;
+    const Plan p = make_plan(a.rows, a.cols, 2);
     const int smem = p.chunks * p.G * 16 * (int)sizeof(float) * (a.bias ? 2 : 1);
-    if (p.chunks == 1) launch_wide(norm_forward_wide_kernel<TX, TY, 1, false, ANY>, p, smem, a, st);
-    else if (!p.multi) launch_wide(norm_forward_wide_kernel<TX, TY, 2, false, ANY>, p, smem, a, st);
-    else launch_wide(norm_forward_wide_kernel<TX, TY, 2, true, ANY>, p, smem, a, st);
+    if (p.ranks > 1) launch(norm_forward_kernel<TX, TY, 2, true, ANY, true>, p, smem, a, st);
+    else if (p.chunks == 1) launch(norm_forward_kernel<TX, TY, 1, false, ANY, false>, p, smem, a, st);
+    else if (!p.multi) launch(norm_forward_kernel<TX, TY, 2, false, ANY, false>, p, smem, a, st);
+    else launch(norm_forward_kernel<TX, TY, 2, true, ANY, false>, p, smem, a, st);
 }
 
 template <typename TX, typename TY>
@@ -975,57 +881,44 @@ static void launch_forward(NormArgs a, cudaStream_t st)
         return rows_aligned(a.x, a.ld_x, sizeof(TX), al) && rows_aligned(a.out, a.ld_out, sizeof(TY), al);
     };
     a.w32 = all_aligned(32);
-    if (a.cols > NM_MAX_WIDE) norm_forward_kernel<TX, TY><<<row_grid(a.rows), NM_THREADS, 0, st>>>(a);
-    else if (all_aligned(16)) launch_forward_wide<TX, TY, false>(a, st);
-    else launch_forward_wide<TX, TY, true>(a, st);
+    if (all_aligned(16)) launch_forward_as<TX, TY, false>(a, st);
+    else launch_forward_as<TX, TY, true>(a, st);
 }
 
 template <typename TX, typename TY, bool CKPT, bool ANY>
-static void launch_backward_wide(NormArgs a, cudaStream_t st)
+static void launch_backward_as(NormArgs a, cudaStream_t st)
 {
-    const bool grads = a.dweight || a.dbias, fused = a.cols <= NM_MAX_FUSED;
-    const WidePlan p = wide_plan(a.rows, a.cols, fused ? 1 : 2, NM_BLOCK);
-    const int vec = p.chunks * p.G * 16 * (int)sizeof(float);
-    a.G = p.G;
-    if (fused) {
-        a.splits = (int)p.grid;
-        if (!grads) a.part = nullptr;
-        using R = Ring<TX, TY, CKPT>;
-        const int ring = ANY ? 0 : R::stages * R::rows * R::slots * 16 * (int)p.threads, smem = 2 * vec + ring;
-        if (p.multi) launch_wide(norm_backward_wide_kernel<TX, TY, 1, true, CKPT, true, ANY>, p, smem, a, st);
-        else launch_wide(norm_backward_wide_kernel<TX, TY, 1, false, CKPT, true, ANY>, p, smem, a, st);
-    } else {
-        launch_wide(norm_backward_wide_kernel<TX, TY, 2, true, CKPT, false, ANY>, p, vec, a, st);
-        if (!grads) return;
-        a.splits = wide_splits(a.rows, a.cols);
-        const dim3 grid((unsigned)((a.cols + 16 * NM_THREADS - 1) / (16 * NM_THREADS)), (unsigned)a.splits);
-        norm_dw_wide_kernel<TX, TY, CKPT, ANY><<<grid, NM_THREADS, 0, st>>>(a);
-    }
-    if (grads) launch_dw_sum(a, st);
+    const Plan p = make_plan(a.rows, a.cols, 1);
+    using R = Ring<TX, TY, CKPT>;
+    const int ring = ANY ? 0 : R::stages * R::rows * R::slots * 16 * (int)p.threads;
+    const int smem = 2 * p.G * 16 * (int)sizeof(float) + ring;
+    const bool grads = a.dweight || a.dbias;
+    if (!grads) a.part = nullptr;
+    if (p.ranks > 1) launch(norm_backward_kernel<TX, TY, true, CKPT, ANY, true>, p, smem, a, st);
+    else if (p.multi) launch(norm_backward_kernel<TX, TY, true, CKPT, ANY, false>, p, smem, a, st);
+    else launch(norm_backward_kernel<TX, TY, false, CKPT, ANY, false>, p, smem, a, st);
+    if (grads) launch_dw_sum(a, p.slices, st);
 }
 
 template <typename TX, typename TY>
 static void launch_backward(NormArgs a, cudaStream_t st)
 {
+    if (a.rows == 0) {  // gradients of zero: no slices to add
+        if (a.dweight || a.dbias) launch_dw_sum(a, 0, st);
+        return;
+    }
     const auto all_aligned = [&](int al) {
         return rows_aligned(a.dy, a.ld_dy, sizeof(TY), al) && rows_aligned(a.out, a.ld_out, sizeof(TX), al) &&
                rows_aligned(a.x, a.ld_x, sizeof(TX), al);
     };
-    if (a.rows > 0 && a.cols <= NM_MAX_WIDE) {
-        a.w32 = all_aligned(32);
-        const bool any = !all_aligned(16);
-        if (a.x && any) launch_backward_wide<TX, TY, false, true>(a, st);
-        else if (a.x) launch_backward_wide<TX, TY, false, false>(a, st);
-        else if (any) launch_backward_wide<TX, TY, true, true>(a, st);
-        else launch_backward_wide<TX, TY, true, false>(a, st);
-        return;
-    }
-    if (a.rows > 0) norm_dx_kernel<TX, TY><<<row_grid(a.rows), NM_THREADS, 0, st>>>(a);
-    if (!a.dweight && !a.dbias) return;
-    a.splits = narrow_splits(a.rows, a.cols);
-    const dim3 grid((unsigned)((a.cols + NM_COLS - 1) / NM_COLS), (unsigned)a.splits);
-    norm_dw_kernel<TX, TY><<<grid, NM_THREADS, 0, st>>>(a);
-    launch_dw_sum(a, st);
+    a.w32 = all_aligned(32);
+    a.end_dy = rows_end(a.ld_dy, a.rows, a.cols);
+    a.end_x = rows_end(a.ld_x, a.rows, a.cols);
+    const bool any = !all_aligned(16);
+    if (a.x && any) launch_backward_as<TX, TY, false, true>(a, st);
+    else if (a.x) launch_backward_as<TX, TY, false, false>(a, st);
+    else if (any) launch_backward_as<TX, TY, true, true>(a, st);
+    else launch_backward_as<TX, TY, true, false>(a, st);
 }
 
 static bool good_dtype(int d) { return d >= FP8_DTYPE_BF16 && d <= FP8_DTYPE_F32; }
@@ -1048,7 +941,8 @@ static fp8_status_t check_codes(const void *q, int64_t ld_q, const void *s, int6
 static fp8_status_t check_common(int64_t rows, int64_t cols, int kind, int xt, int yt, int wt, const void *w,
                                  const void *b)
 {
-    if (rows < 0 || cols < 1 || rows > INT32_MAX || cols > INT32_MAX - FP8_MX_BLOCK) return FP8_ERR_INVALID_ARG;
+    if (rows < 0 || cols < 1 || rows > INT32_MAX) return FP8_ERR_INVALID_ARG;
+    if (cols > NM_MAX_COLS) return FP8_ERR_UNSUPPORTED;
     if (kind != FP8_NORM_LAYER && kind != FP8_NORM_RMS) return FP8_ERR_INVALID_ARG;
     if (!good_dtype(xt) || !good_dtype(yt) || !good_dtype(wt)) return FP8_ERR_INVALID_ARG;
     if (xt != yt && xt != FP8_DTYPE_F32) return FP8_ERR_UNSUPPORTED;
@@ -1115,13 +1009,8 @@ extern "C" fp8_status_t fp8_norm_forward(const void *x, int x_dtype, int64_t ld_
 
 extern "C" int64_t fp8_norm_workspace_bytes(int64_t rows, int64_t cols)
 {
-    if (rows < 0 || cols < 1 || rows > INT32_MAX || cols > INT32_MAX - FP8_MX_BLOCK) return -1;
-    // the most row slices that any form makes: the wide fused kernel's blocks,
-    // or the slices of either column kernel
-    int64_t most = num_sms();
-    if (narrow_splits(rows, cols) > most) most = narrow_splits(rows, cols);
-    if (wide_splits(rows, cols) > most) most = wide_splits(rows, cols);
-    if (most > rows) most = rows > 0 ? rows : 1;  // a slice has a row at least
+    if (rows < 0 || cols < 1 || rows > INT32_MAX || cols > NM_MAX_COLS) return -1;
+    const int64_t most = rows > 0 ? make_plan(rows, cols, 1).slices : 1;
     return most * 2 * cols * (int64_t)sizeof(float);
 }
 

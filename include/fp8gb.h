@@ -523,7 +523,8 @@ FP8GB_API fp8_status_t fp8_mx_grouped_gemm(int mode, const uint8_t *A, int fa, c
  * take bf16).  Tensors are row-major with a row stride (ld) in elements, of
  * any width and any element-aligned address and stride; wide accesses are
  * used where the addresses and strides allow them.  Outputs must not overlap
- * inputs.  rows, cols <= 2^31 - 33.
+ * inputs.  rows < 2^31; cols < 2^31 - 32 in all, and at most 65536 for the
+ * norms (FP8_ERR_UNSUPPORTED).
  *
  * Checkpoint format.  A row is cut into blocks of FP8_MX_BLOCK = 32 columns
  * (the last one may be short).  A block's scale is X = 2^e, e the smallest
@@ -557,17 +558,20 @@ FP8GB_API fp8_status_t fp8_checkpoint_restore(const uint8_t *q, int64_t ld_q, co
 
 /*
  * fp8_swiglu_checkpoint -- h = bf16(silu(gate) * up) of gate_up_bf16 [rows][ld]
- * (gate in columns [0, F), up in [F, 2F)), evaluated as in
- * fp8_mx_swiglu_quantize, and the 2-part checkpoint of gate_up, in one read.
+ * (gate in columns [0, F), up in [F, 2F)), and the 2-part checkpoint of
+ * gate_up, in one read.
  *
  * fp8_swiglu_backward -- with s = sigma(gate),
  *   d_gate = dh * up * s * (1 + gate * (1 - s)),  d_up = dh * gate * s,
  * written side by side into d_gate_up_bf16 [rows][ld_d].  gate and up come
  * from gate_up_bf16 (q, s NULL) or, with gate_up_bf16 NULL, from their
  * 2-part checkpoint.  h_bf16: optional, receives bf16(silu(gate) * up) of
- * the same gate and up (the down projection's input, recomputed).  fp32
- * arithmetic with the fast exponential, one rounding each; a gate below
- * about -87, -Inf included, gives zeros (2^-119 of |dh|, |dh up| or |up|).
+ * the same gate and up (the down projection's input, recomputed: from
+ * gate_up_bf16 the bits of fp8_swiglu_checkpoint's h).
+ *
+ * fp32 arithmetic with the fast exponential, one rounding each (h within one
+ * bf16 ulp); a gate below about -87, -Inf included, gives zeros (what that
+ * leaves out is under 2^-119 of |dh|, |dh up| or |up|).
  */
 FP8GB_API fp8_status_t fp8_swiglu_checkpoint(const void *gate_up_bf16, int64_t rows, int64_t F, int64_t ld, int fmt,
                                              void *h_bf16, int64_t ld_h, uint8_t *q, int64_t ld_q, uint8_t *s,

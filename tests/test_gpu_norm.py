@@ -114,6 +114,20 @@ def test_widths(cols, kind):
         check_backward(dy, x if fmt is None else f.checkpoint, f, w, kind, x if fmt is None else None, what=f"{cols}")
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("cols", [8200, 16385, 16392, 24000, 32768, 32769, 40001, 65536])
+def test_rows_shared_by_a_cluster(cols, kind):
+    """Widths that two, four and eight blocks share, aligned or not, in bf16
+    and with an fp32 x, with few and with several rows a cluster."""
+    for rows, tx, pad in ((3, BF16, 0), (170, F32, 0), (41, BF16, 24)):
+        x, dy = values(rows, cols, tx, cols, 1.3, 0.2, pad), values(rows, cols, BF16, cols + 1, 0.05, 0.0, pad)
+        w, b = params(cols, BF16, cols + 2)
+        b = b if kind == fp8.LAYER_NORM else None
+        f = check_forward(x, w, b, kind, 1e-5, BF16, 0, what=f"{rows} x {cols}")
+        check_backward(dy, x, f, w, kind, x, what=f"{rows} x {cols} from x")
+        check_backward(dy, f.checkpoint, f, w, kind, dx_dtype=tx, what=f"{rows} x {cols} from the checkpoint")
+
+
 @pytest.mark.parametrize("pair", PAIRS)
 @pytest.mark.parametrize("wt", [BF16, F16, F32])
 @pytest.mark.parametrize("shape", [(5, 96, 0, 0), (33, 1000, 8, 0), (9, 4096, 3, 1), (12, 7171, 5, 0)])
@@ -145,6 +159,18 @@ def test_row_counts(rows, cols):
     w, b = params(cols, F32, 2)
     f = check_forward(x, w, b, fp8.LAYER_NORM, 1e-5, None, what=f"{rows}")
     check_backward(dy, x, f, w, fp8.LAYER_NORM, x, what=f"{rows}")
+
+
+@pytest.mark.parametrize("cols", [8, 40, 272, 1000, 2056, 4616, 7168])
+def test_two_rows_a_step_with_short_last_blocks(cols):
+    """Enough rows for every step of the backward to hold two, at widths whose
+    last block of 32 columns has only its first lane's half."""
+    rows = 700
+    x, dy = values(rows, cols, BF16, cols, 1.3, 0.2), values(rows, cols, BF16, cols + 1, 0.05)
+    w, b = params(cols, F32, cols + 2)
+    f = check_forward(x, w, b, fp8.LAYER_NORM, 1e-5, None, 0, what=f"{cols}")
+    check_backward(dy, x, f, w, fp8.LAYER_NORM, x, what=f"{cols} from x")
+    check_backward(dy, f.checkpoint, f, w, fp8.LAYER_NORM, what=f"{cols} from the checkpoint")
 
 
 @pytest.mark.parametrize("cols", [100, 4096])
@@ -337,6 +363,9 @@ def test_refusals():
     refused(fp8.norm_forward, x, w, b, checkpoint_fmt=fp8.E4M3FNUZ)
     refused(fp8.norm_forward, x, w, b, out=torch.empty((8, 32), dtype=BF16, device=DEV))
     refused(fp8.norm_forward, x[:1].expand(8, 64), w, b)
+    wide = torch.zeros((1, 65537), dtype=BF16, device=DEV)
+    refused(fp8.norm_forward, wide)
+    refused(fp8.norm_backward, wide, wide, f.mean[:1], f.rstd[:1])
     dy = values(8, 64, BF16, 3)
     refused(fp8.norm_backward, dy, x, None, f.rstd, w)
     refused(fp8.norm_backward, dy, x[:4], f.mean, f.rstd, w)
