@@ -493,10 +493,17 @@ struct CopyPlace {
 };
 
 // Bytes 0 .. valid - 1 of the warp's part of a row at `src` (zeros after).
-template <int SLOTS>
+template <int SLOTS, bool MULTI>
 __device__ __forceinline__ void copy_ahead(uint32_t dst, const void *src, int valid, const CopyPlace &c,
                                            const void *anywhere)
 {
+    if (MULTI && valid >= SLOTS * 512) {  // all of the warp's columns: its units are 32 apart, the swizzle one
+        const char *p = static_cast<const char *>(src) + c.t * 16;
+        dst += (c.t ^ (c.t >> 3 & (SLOTS - 1))) * 16;
+#pragma unroll
+        for (int j = 0; j < SLOTS; j++) cp_async_16(dst + j * 512, p + j * 512, 16);
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < SLOTS; j++) {
         const int u = j * c.G + c.t, at = c.sub * SLOTS * c.G + u, bytes = max(0, min(16, valid - u * 16));
@@ -511,6 +518,13 @@ __device__ __forceinline__ uint4 copied(uint32_t src, int lane, int j)
 {
     const int at = SLOTS * lane + j;
     return ld_shared_16b(src + (at ^ (at >> 3 & (SLOTS - 1))) * 16);
+}
+
+__device__ __forceinline__ int lane_id()
+{
+    int v;
+    asm volatile("mov.u32 %0, %%laneid;" : "=r"(v));
+    return v;
 }
 
 template <int N>
@@ -540,11 +554,11 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
     const Group g = group_of<MULTI>(G, parts);
     const int groups = CLUSTER ? 1 : MULTI ? blockDim.x / G : blockDim.x >> (31 - __clz(G));
     const int block = CLUSTER ? blockIdx.x / a.ranks : blockIdx.x;  // of those that split the rows
-    const int64_t step = (int64_t)(CLUSTER ? gridDim.x / a.ranks : gridDim.x) * groups;
+    // rows are counted in 32 bits: fewer registers, and below 2^31 + a few steps
+    const uint32_t rows = (uint32_t)a.rows, step = (CLUSTER ? gridDim.x / a.ranks : gridDim.x) * groups;
     const int n = max(0, min(16, cols - g.t * 16));  // columns of the row in this thread's chunk
 
-    int64_t r = (int64_t)block * groups + g.id;
-    int64_t first = MULTI ? r : r - (threadIdx.x & 31) / G;
+    uint32_t r = block * groups + g.id;
     using R = Ring<TX, TY, CKPT>;
     constexpr int S = ANY ? 0 : R::stages;  // 0: one row ahead in registers
     constexpr int ROWS = S ? R::rows : 1, AHEAD = S ? S - 1 : 1;
@@ -555,28 +569,29 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
     constexpr bool LANES = MULTI && ROWS == 2;
     float mean_q[AHEAD][ROWS] = {}, rstd_q[AHEAD][ROWS] = {}, stat = 0.0f;
     uint32_t scale = 127;
-    const int lane = threadIdx.x & 31, col0 = MULTI ? (g.t >> 5) * 512 : 0;  // of the warp's part of the row
+    // %laneid: read where it is wanted, it costs no register over the loop
+    const int lane = lane_id(), col0 = MULTI ? (g.t >> 5) * 512 : 0;  // of the warp's part of the row
     const CopyPlace cp{MULTI ? lane : g.t, MULTI ? 32 : G, MULTI ? 0 : lane / G};
     constexpr int DY = R::dy_slots, X = R::x_slots;
     // a warp's part of a row: 32 lanes of DY units, then of X
     const uint32_t ring = smem_u32(shared + 2 * G * 16) + (threadIdx.x >> 5) * (R::slots * 512);
     const uint32_t row_bytes = blockDim.x * R::slots * 16;
-    const auto fetch = [&](int64_t row0, int stage) {
+    const auto fetch = [&](uint32_t row0, int stage) {
 #pragma unroll
         for (int i = 0; i < ROWS; i++) {
-            const int64_t row = row0 + i * step;
-            const bool live = row < a.rows;
+            const uint32_t row = row0 + i * step;
+            const bool live = row < rows;
             if constexpr (S == 0) {
                 load_backward(a, row, g.t, live ? n : 0, raw[0]);
             } else {
                 const uint32_t at = ring + (stage * ROWS + i) * row_bytes;
                 const int have = live ? cols - col0 : 0;
-                copy_ahead<DY>(at, static_cast<const TY *>(a.dy) + row * a.ld_dy + col0, have * (int)sizeof(TY), cp,
+                copy_ahead<DY, MULTI>(at, static_cast<const TY *>(a.dy) + row * a.ld_dy + col0, have * (int)sizeof(TY), cp,
                                a.dy);
                 if constexpr (CKPT)
-                    copy_ahead<X>(at + DY * 512, a.q + row * a.ld_q + col0, have > 0 ? have + 15 & ~15 : 0, cp, a.q);
+                    copy_ahead<X, MULTI>(at + DY * 512, a.q + row * a.ld_q + col0, have > 0 ? have + 15 & ~15 : 0, cp, a.q);
                 else
-                    copy_ahead<X>(at + DY * 512, static_cast<const TX *>(a.x) + row * a.ld_x + col0,
+                    copy_ahead<X, MULTI>(at + DY * 512, static_cast<const TX *>(a.x) + row * a.ld_x + col0,
                                   have * (int)sizeof(TX), cp, a.x);
             }
             if (live && !LANES) {
@@ -585,14 +600,14 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
             }
         }
         if (LANES) {
-            const int64_t row = row0 + (lane >> 1 & 1) * step;
-            if (row < a.rows) stat = __ldg((lane & 1 && !CKPT && !a.rms ? a.mean : a.rstd) + row);
+            const uint32_t row = row0 + (lane >> 1 & 1) * step;
+            if (row < rows) stat = __ldg((lane & 1 && !CKPT && !a.rms ? a.mean : a.rstd) + row);
         }
         if (CKPT && S > 0) {
             // the scale byte of a block's two lanes: the even lane's of row 0, the odd lane's of row 1
             // (also where the odd lane's own columns are past the row)
-            const int64_t row = row0 + (lane & 1) * step;
-            if (row < a.rows && (g.t & ~1) * 16 < cols) scale = __ldg(a.s + row * a.ld_s + (g.t >> 1));
+            const uint32_t row = row0 + (lane & 1) * step;
+            if (row < rows && (g.t & ~1) * 16 < cols) scale = __ldg(a.s + row * a.ld_s + (g.t >> 1));
         }
         if constexpr (S > 0) asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -618,7 +633,8 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
 
     float2 dw[8] = {}, db[8] = {};  // ACC: one chunk a thread
     int slot = 0, stage = 0;
-    for (; first < a.rows; first += ROWS * step, r += ROWS * step) {
+    // the groups of a warp go on until the first of them is done
+    for (; (MULTI ? r : r - cp.sub) < rows; r += ROWS * step) {
         float gr[ROWS][16], xh[ROWS][16], rstd[ROWS];
         if constexpr (S > 0) {
             cp_async_wait<(S > 0 ? S - 2 : 0)>();
@@ -631,7 +647,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
                 if constexpr (CKPT) {
                     raw[i].q = copied<X>(at + DY * 512, lane, 0);
                     const uint32_t s = __shfl_sync(0xffffffffu, scale, lane & ~1 | i);
-                    raw[i].s = r + i * step < a.rows ? s : 127u;
+                    raw[i].s = r + i * step < rows ? s : 127u;
                 } else {
 #pragma unroll
                     for (int j = 0; j < X; j++) raw[i].x.v[j] = copied<X>(at + DY * 512, lane, j);
@@ -651,7 +667,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
             xhat16(a, raw[i], n, mean, rstd[i], xh[i]);
         }
         advance();
-        if (S > 0 || first + step < a.rows) {
+        if (S > 0 || (MULTI ? r : r - cp.sub) + step < rows) {
             // into the place of the step before this one
             fetch(r + AHEAD * ROWS * step, stage == 0 ? S - 1 : stage - 1);
             if (S > 0) stage = stage + 1 == S ? 0 : stage + 1;
@@ -689,7 +705,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
         slot ^= 1;
 #pragma unroll
         for (int i = 0; i < ROWS; i++) {
-            const int64_t row = r + i * step;
+            const uint32_t row = r + i * step;
             const float c1 = a.rms ? 0.0f : -sum[i].x * inv_n * rstd[i], c2 = -sum[i].y * inv_n * rstd[i];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -699,7 +715,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
                 gr[i][j] = o.x, gr[i][j + 1] = o.y;
             }
             store_chunk<ANY>(static_cast<TX *>(a.out) + row * a.ld_out + g.t * 16, gr[i],
-                             row < a.rows ? cols - g.t * 16 : 0, a.w32, g.t, G);
+                             row < rows ? cols - g.t * 16 : 0, a.w32, g.t, G);
         }
     }
     cp_async_wait<0>();
