@@ -6,7 +6,8 @@
 //
 // A thread works on 16 consecutive columns, half a block: the bf16 side is one
 // 32-byte access, the codes one of 16, and the block maximum one shuffle with the
-// neighbour.  It issues the loads of UNROLL rows before it works on the first.
+// neighbour.  Checkpoint and restore issue the loads of four rows before they work
+// on the first.
 // The threads of a block cover 2^lg chunks of CK_THREADS >> lg rows, so no thread
 // divides.  Rows that are no multiple of 16 bytes apart (ANY) are read and
 // written in the aligned words that cover them, shifted into place.
@@ -74,7 +75,7 @@ __device__ __forceinline__ WidePlace wide_place(const WideGeometry &g)
 __device__ __forceinline__ int chunk_rest(int64_t cols, int64_t c) { return (int)(cols - c); }
 __device__ __forceinline__ int chunk_columns(int64_t cols, int64_t c) { return max(0, min(16, chunk_rest(cols, c))); }
 
-constexpr int STORE_UNROLL = 4, RESTORE_UNROLL = 4, SWIGLU_UNROLL = 2, BACKWARD_UNROLL = 2;
+constexpr int STORE_UNROLL = 4, RESTORE_UNROLL = 4;  // rows whose loads a thread issues first
 
 template <typename T, int FMT, bool ANY>
 __global__ void __launch_bounds__(CK_THREADS) checkpoint_kernel(CkArgs a)
@@ -137,118 +138,96 @@ __global__ void __launch_bounds__(CK_THREADS) restore_kernel(CkArgs a)
     }
 }
 
+// The SwiGLU kernels take one row a thread and four blocks an SM (64 registers):
+// two rows and two blocks took 149 and 153 us where these take 140 and 142 (forward
+// and backward of [8192, 14336]).
 template <int FMT, bool ANY>
-__global__ void __launch_bounds__(CK_THREADS) swiglu_checkpoint_kernel(SwArgs a)
+__global__ void __launch_bounds__(CK_THREADS, ANY ? 3 : 4) swiglu_checkpoint_kernel(SwArgs a)
 {
     using T = __nv_bfloat16;
-    const WidePlace p = wide_place<SWIGLU_UNROLL>(a.geo);
-    const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16;
-    const bool in = p.chunk < cpp;
+    const WidePlace p = wide_place<1>(a.geo);
+    const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16, r = p.row;
+    const bool in = p.chunk < cpp && r < a.rows;
     const int n = in ? chunk_columns(a.F, c) : 0, rest = in ? chunk_rest(a.F, c) : 0;
     const int lanes = 1 << a.geo.lg, t = threadIdx.x & (lanes - 1);
-    const int64_t end = rows_end(a.ld, a.rows, 2 * a.F);
-    Raw<T, ANY> gr[SWIGLU_UNROLL], ur[SWIGLU_UNROLL];
-#pragma unroll
-    for (int k = 0; k < SWIGLU_UNROLL; k++) {
-        const int64_t r = p.row + (int64_t)k * p.ty;
-        const int64_t at = r * a.ld + c;
-        load_chunk<ANY>(a.gate_up + at, r < a.rows ? n : 0, a.w32, at, end, gr[k]);
-        load_chunk<ANY>(a.gate_up + at + a.F, r < a.rows ? n : 0, a.w32, at + a.F, end, ur[k]);
+    const int64_t at = r * a.ld + c, end = rows_end(a.ld, a.rows, 2 * a.F);
+    Raw<T, ANY> gr, ur;
+    load_chunk<ANY>(a.gate_up + at, n, a.w32, at, end, gr);
+    load_chunk<ANY>(a.gate_up + at + a.F, n, a.w32, at + a.F, end, ur);
+    float g[16], u[16], h[16];
+    unpack16(gr, g);
+    unpack16(ur, u);
+    if (ANY) {
+        fill_from(g, n, 0.0f);
+        fill_from(u, n, 0.0f);
     }
+    const uint32_t cg = ckpt_code(block_amax16(g), FMT), cu = ckpt_code(block_amax16(u), FMT);
 #pragma unroll
-    for (int k = 0; k < SWIGLU_UNROLL; k++) {
-        const int64_t r = p.row + (int64_t)k * p.ty;
-        float g[16], u[16], h[16];
-        unpack16(gr[k], g);
-        unpack16(ur[k], u);
-        if (ANY) {
-            fill_from(g, n, 0.0f);
-            fill_from(u, n, 0.0f);
-        }
-        const uint32_t cg = ckpt_code(block_amax16(g), FMT), cu = ckpt_code(block_amax16(u), FMT);
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            float2 e, sigma, silu;
-            silu2(make_float2(g[j], g[j + 1]), e, sigma, silu);
-            const float2 v = mul2(silu, make_float2(u[j], u[j + 1]));
-            h[j] = v.x, h[j + 1] = v.y;
-        }
-        store_chunk<ANY>(a.h + r * a.ld_h + c, h, r < a.rows ? rest : 0, a.w32, t, lanes);
-        if (!in || r >= a.rows) continue;
-        uint8_t *q = a.q + r * a.ld_q + c;
-        *reinterpret_cast<uint4 *>(q) = encode16<FMT>(g, ckpt_inv_scale(cg));
-        *reinterpret_cast<uint4 *>(q + cpp * 16) = encode16<FMT>(u, ckpt_inv_scale(cu));
-        if (!(p.chunk & 1)) {
-            uint8_t *s = a.s + r * a.ld_s + (p.chunk >> 1);
-            s[0] = (uint8_t)cg;
-            s[cpp >> 1] = (uint8_t)cu;
-        }
+    for (int j = 0; j < 16; j += 2) {
+        float2 e, sigma, silu;
+        silu2(make_float2(g[j], g[j + 1]), e, sigma, silu);
+        const float2 v = mul2(silu, make_float2(u[j], u[j + 1]));
+        h[j] = v.x, h[j + 1] = v.y;
+    }
+    store_chunk<ANY>(a.h + r * a.ld_h + c, h, rest, a.w32, t, lanes);
+    if (!in) return;
+    uint8_t *q = a.q + r * a.ld_q + c;
+    *reinterpret_cast<uint4 *>(q) = encode16<FMT>(g, ckpt_inv_scale(cg));
+    *reinterpret_cast<uint4 *>(q + cpp * 16) = encode16<FMT>(u, ckpt_inv_scale(cu));
+    if (!(p.chunk & 1)) {
+        uint8_t *s = a.s + r * a.ld_s + (p.chunk >> 1);
+        s[0] = (uint8_t)cg;
+        s[cpp >> 1] = (uint8_t)cu;
     }
 }
 
 // CKPT: gate and up from the checkpoint, else from bf16.
 template <int FMT, bool CKPT, bool ANY>
-__global__ void __launch_bounds__(CK_THREADS) swiglu_backward_kernel(SwArgs a)
+__global__ void __launch_bounds__(CK_THREADS, 4) swiglu_backward_kernel(SwArgs a)
 {
     using T = __nv_bfloat16;
-    const WidePlace p = wide_place<BACKWARD_UNROLL>(a.geo);
-    const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16;
-    const int n = chunk_columns(a.F, c), rest = chunk_rest(a.F, c);  // nothing past the row
+    const WidePlace p = wide_place<1>(a.geo);
+    const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16, r = p.row;
+    const int n = r < a.rows ? chunk_columns(a.F, c) : 0, rest = r < a.rows ? chunk_rest(a.F, c) : 0;
     const int lanes = 1 << a.geo.lg, t = threadIdx.x & (lanes - 1);
-    const int64_t end = rows_end(a.ld, a.rows, 2 * a.F), end_dh = rows_end(a.ld_dh, a.rows, a.F);
-    Raw<T, ANY> gr[BACKWARD_UNROLL], ur[BACKWARD_UNROLL], dr[BACKWARD_UNROLL];
-    uint4 gq[BACKWARD_UNROLL], uq[BACKWARD_UNROLL];
-    uint32_t gs[BACKWARD_UNROLL], us[BACKWARD_UNROLL];
-#pragma unroll
-    for (int k = 0; k < BACKWARD_UNROLL; k++) {
-        const int64_t r = p.row + (int64_t)k * p.ty;
-        const int have = r < a.rows ? n : 0;
-        if constexpr (CKPT) {
-            gq[k] = uq[k] = make_uint4(0, 0, 0, 0);
-            gs[k] = us[k] = 0;
-            if (have > 0) {
-                const uint8_t *q = a.q + r * a.ld_q + c, *s = a.s + r * a.ld_s + (p.chunk >> 1);
-                gq[k] = ld_stream_16b(q);
-                uq[k] = ld_stream_16b(q + cpp * 16);
-                gs[k] = __ldg(s);
-                us[k] = __ldg(s + (cpp >> 1));
-            }
-        } else {
-            const int64_t at = r * a.ld + c;
-            load_chunk<ANY>(a.gate_up + at, have, a.w32, at, end, gr[k]);
-            load_chunk<ANY>(a.gate_up + at + a.F, have, a.w32, at + a.F, end, ur[k]);
+    float g[16], u[16], d[16];
+    Raw<T, ANY> dr;
+    const int64_t at_dh = r * a.ld_dh + c;
+    load_chunk<ANY>(a.dh + at_dh, n, a.w32, at_dh, rows_end(a.ld_dh, a.rows, a.F), dr);
+    if constexpr (CKPT) {
+        uint4 gq = make_uint4(0, 0, 0, 0), uq = gq;
+        uint32_t gs = 0, us = 0;
+        if (n > 0) {
+            const uint8_t *q = a.q + r * a.ld_q + c, *s = a.s + r * a.ld_s + (p.chunk >> 1);
+            gq = ld_stream_16b(q);
+            uq = ld_stream_16b(q + cpp * 16);
+            gs = __ldg(s);
+            us = __ldg(s + (cpp >> 1));
         }
-        const int64_t at = r * a.ld_dh + c;
-        load_chunk<ANY>(a.dh + at, have, a.w32, at, end_dh, dr[k]);
+        decode16<FMT>(gq, ckpt_scale(gs), g);
+        decode16<FMT>(uq, ckpt_scale(us), u);
+    } else {
+        Raw<T, ANY> gr, ur;
+        const int64_t at = r * a.ld + c, end = rows_end(a.ld, a.rows, 2 * a.F);
+        load_chunk<ANY>(a.gate_up + at, n, a.w32, at, end, gr);
+        load_chunk<ANY>(a.gate_up + at + a.F, n, a.w32, at + a.F, end, ur);
+        unpack16(gr, g);
+        unpack16(ur, u);
     }
+    unpack16(dr, d);
+    // the gradients take the places of g and u, h that of dh
 #pragma unroll
-    for (int k = 0; k < BACKWARD_UNROLL; k++) {
-        const int64_t r = p.row + (int64_t)k * p.ty;
-        float g[16], u[16], d[16];
-        if constexpr (CKPT) {
-            decode16<FMT>(gq[k], ckpt_scale(gs[k]), g);
-            decode16<FMT>(uq[k], ckpt_scale(us[k]), u);
-        } else {
-            unpack16(gr[k], g);
-            unpack16(ur[k], u);
-        }
-        unpack16(dr[k], d);
-        // the gradients take the places of g and u, h that of dh
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            float2 dg, du, h;
-            swiglu_grad2(make_float2(g[j], g[j + 1]), make_float2(u[j], u[j + 1]), make_float2(d[j], d[j + 1]), dg,
-                         du, h);
-            g[j] = dg.x, g[j + 1] = dg.y;
-            u[j] = du.x, u[j + 1] = du.y;
-            d[j] = h.x, d[j + 1] = h.y;
-        }
-        const int have = r < a.rows ? rest : 0;
-        T *out = a.d + r * a.ld_d + c;
-        if (a.h) store_chunk<ANY>(a.h + r * a.ld_h + c, d, have, a.w32, t, lanes);
-        store_chunk<ANY>(out, g, have, a.w32, t, lanes);
-        store_chunk<ANY>(out + a.F, u, have, a.w32, t, lanes);
+    for (int j = 0; j < 16; j += 2) {
+        float2 dg, du, h;
+        swiglu_grad2(make_float2(g[j], g[j + 1]), make_float2(u[j], u[j + 1]), make_float2(d[j], d[j + 1]), dg, du, h);
+        g[j] = dg.x, g[j + 1] = dg.y;
+        u[j] = du.x, u[j + 1] = du.y;
+        d[j] = h.x, d[j + 1] = h.y;
     }
+    T *out = a.d + r * a.ld_d + c;
+    if (a.h) store_chunk<ANY>(a.h + r * a.ld_h + c, d, rest, a.w32, t, lanes);
+    store_chunk<ANY>(out, g, rest, a.w32, t, lanes);
+    store_chunk<ANY>(out + a.F, u, rest, a.w32, t, lanes);
 }
 
 // The widest block whose tiles cover a row of `chunks` with at most 1/16 of
@@ -341,7 +320,7 @@ static void launch_swiglu_checkpoint(SwArgs a, cudaStream_t st)
     const auto all_aligned = [&](int al) {
         return rows_aligned(a.gate_up, a.ld, a.F, 2, al) && rows_aligned(a.h, a.ld_h, 0, 2, al);
     };
-    a.geo = wide_geometry(a.rows, ckpt_width(a.F) / 16, SWIGLU_UNROLL);
+    a.geo = wide_geometry(a.rows, ckpt_width(a.F) / 16, 1);
     a.w32 = all_aligned(32);
     if (all_aligned(16)) swiglu_checkpoint_kernel<FMT, false><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
     else swiglu_checkpoint_kernel<FMT, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
@@ -354,7 +333,7 @@ static void launch_swiglu_backward(SwArgs a, cudaStream_t st)
         return rows_aligned(a.dh, a.ld_dh, 0, 2, al) && rows_aligned(a.d, a.ld_d, a.F, 2, al) &&
                rows_aligned(a.h, a.h ? a.ld_h : 0, 0, 2, al) && (CKPT || rows_aligned(a.gate_up, a.ld, a.F, 2, al));
     };
-    a.geo = wide_geometry(a.rows, ckpt_width(a.F) / 16, BACKWARD_UNROLL);
+    a.geo = wide_geometry(a.rows, ckpt_width(a.F) / 16, 1);
     a.w32 = all_aligned(32);
     if (all_aligned(16)) swiglu_backward_kernel<FMT, CKPT, false><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
     else swiglu_backward_kernel<FMT, CKPT, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
