@@ -23,8 +23,8 @@ namespace fp8gb {
 
 constexpr int CK_THREADS = 256;
 
-// How the blocks of the wide kernels cover rows x chunks of 16 columns.
-struct WideGeometry {
+// How the blocks of a launch cover rows x chunks of 16 columns.
+struct Geometry {
     int lg;             // a block is 2^lg chunks wide and CK_THREADS / 2^lg rows high, times UNROLL
     uint32_t n_tiles;   // blocks across a row
     uint32_t grid;
@@ -37,7 +37,7 @@ struct CkArgs {
     int64_t ld_q, ld_s;
     int64_t rows, cols;
     int parts, fmt;
-    WideGeometry geo;
+    Geometry geo;
     int w32;  // x's rows and parts start on 32-byte boundaries
 };
 
@@ -50,21 +50,21 @@ struct SwArgs {
     int fmt;
     __nv_bfloat16 *h, *d;
     int64_t ld_h, ld_d;
-    WideGeometry geo;
+    Geometry geo;
     int w32;
 };
 
 // A thread's chunk and first row; its later rows are `ty` further each.
-struct WidePlace {
+struct Place {
     int64_t chunk, row;
     int ty;
 };
 
 template <int UNROLL>
-__device__ __forceinline__ WidePlace wide_place(const WideGeometry &g)
+__device__ __forceinline__ Place place_of(const Geometry &g)
 {
     const uint32_t rt = blockIdx.x / g.n_tiles, ct = blockIdx.x - rt * g.n_tiles;
-    WidePlace p;
+    Place p;
     p.ty = CK_THREADS >> g.lg;
     p.chunk = ((int64_t)ct << g.lg) + (threadIdx.x & ((1 << g.lg) - 1));
     p.row = (int64_t)rt * p.ty * UNROLL + (threadIdx.x >> g.lg);
@@ -80,7 +80,7 @@ constexpr int STORE_UNROLL = 4, RESTORE_UNROLL = 4;  // rows whose loads a threa
 template <typename T, int FMT, bool ANY>
 __global__ void __launch_bounds__(CK_THREADS) checkpoint_kernel(CkArgs a)
 {
-    const WidePlace p = wide_place<STORE_UNROLL>(a.geo);
+    const Place p = place_of<STORE_UNROLL>(a.geo);
     const int64_t cpp = ckpt_width(a.cols) / 16;  // chunks of a part
     const bool in = p.chunk < a.parts * cpp;
     const int64_t part = a.parts == 1 ? 0 : p.chunk / cpp, c = (p.chunk - part * cpp) * 16;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(CK_THREADS) checkpoint_kernel(CkArgs a)
 template <typename T, int FMT, bool ANY>
 __global__ void __launch_bounds__(CK_THREADS) restore_kernel(CkArgs a)
 {
-    const WidePlace p = wide_place<RESTORE_UNROLL>(a.geo);
+    const Place p = place_of<RESTORE_UNROLL>(a.geo);
     const int64_t cpp = ckpt_width(a.cols) / 16;
     const bool in = p.chunk < a.parts * cpp;
     const int64_t part = a.parts == 1 ? 0 : p.chunk / cpp, c = (p.chunk - part * cpp) * 16;
@@ -145,7 +145,7 @@ template <int FMT, bool ANY>
 __global__ void __launch_bounds__(CK_THREADS, ANY ? 3 : 4) swiglu_checkpoint_kernel(SwArgs a)
 {
     using T = __nv_bfloat16;
-    const WidePlace p = wide_place<1>(a.geo);
+    const Place p = place_of<1>(a.geo);
     const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16, r = p.row;
     const bool in = p.chunk < cpp && r < a.rows;
     const int n = in ? chunk_columns(a.F, c) : 0, rest = in ? chunk_rest(a.F, c) : 0;
@@ -186,7 +186,7 @@ template <int FMT, bool CKPT, bool ANY>
 __global__ void __launch_bounds__(CK_THREADS, 4) swiglu_backward_kernel(SwArgs a)
 {
     using T = __nv_bfloat16;
-    const WidePlace p = wide_place<1>(a.geo);
+    const Place p = place_of<1>(a.geo);
     const int64_t cpp = ckpt_width(a.F) / 16, c = p.chunk * 16, r = p.row;
     const int n = r < a.rows ? chunk_columns(a.F, c) : 0, rest = r < a.rows ? chunk_rest(a.F, c) : 0;
     const int lanes = 1 << a.geo.lg, t = threadIdx.x & (lanes - 1);
@@ -232,9 +232,9 @@ __global__ void __launch_bounds__(CK_THREADS, 4) swiglu_backward_kernel(SwArgs a
 
 // The widest block whose tiles cover a row of `chunks` with at most 1/16 of
 // their threads idle (two chunks at least: a block's halves are neighbours).
-static WideGeometry wide_geometry(int64_t rows, int64_t chunks, int unroll)
+static Geometry geometry(int64_t rows, int64_t chunks, int unroll)
 {
-    WideGeometry g;
+    Geometry g;
     g.lg = 8;
     while (g.lg > 1) {
         const int64_t covered = ((chunks + (1LL << g.lg) - 1) >> g.lg) << g.lg;
@@ -291,28 +291,38 @@ template <typename T>
 static bool plan(CkArgs &a, int unroll)
 {
     const int64_t off = a.parts > 1 ? a.cols : 0;
-    a.geo = wide_geometry(a.rows, a.parts * (ckpt_width(a.cols) / 16), unroll);
+    a.geo = geometry(a.rows, a.parts * (ckpt_width(a.cols) / 16), unroll);
     a.w32 = rows_aligned(a.x, a.ld_x, off, sizeof(T), 32);
     return rows_aligned(a.x, a.ld_x, off, sizeof(T), 16);
 }
 
-template <typename T>
+template <typename T, int FMT>
 static void launch_checkpoint(CkArgs a, cudaStream_t st)
 {
-    const bool wide = plan<T>(a, STORE_UNROLL);
-    const auto run = [&](auto kernel) { kernel<<<a.geo.grid, CK_THREADS, 0, st>>>(a); };
-    if (a.fmt == FP8_E5M2) wide ? run(checkpoint_kernel<T, FP8_E5M2, false>) : run(checkpoint_kernel<T, FP8_E5M2, true>);
-    else wide ? run(checkpoint_kernel<T, FP8_E4M3FN, false>) : run(checkpoint_kernel<T, FP8_E4M3FN, true>);
+    if (plan<T>(a, STORE_UNROLL)) checkpoint_kernel<T, FMT, false><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    else checkpoint_kernel<T, FMT, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
 }
 
-template <typename T>
+template <typename T, int FMT>
 static void launch_restore(CkArgs a, cudaStream_t st)
 {
-    const bool wide = plan<T>(a, RESTORE_UNROLL);
-    const auto run = [&](auto kernel) { kernel<<<a.geo.grid, CK_THREADS, 0, st>>>(a); };
-    if (a.fmt == FP8_E5M2) wide ? run(restore_kernel<T, FP8_E5M2, false>) : run(restore_kernel<T, FP8_E5M2, true>);
-    else wide ? run(restore_kernel<T, FP8_E4M3FN, false>) : run(restore_kernel<T, FP8_E4M3FN, true>);
+    if (plan<T>(a, RESTORE_UNROLL)) restore_kernel<T, FMT, false><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
+    else restore_kernel<T, FMT, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
 }
+
+// The element type and format of a call as template parameters.
+#define CK_DISPATCH(FN, dtype, a, st)                                                                       \
+    do {                                                                                                    \
+        if (a.fmt == FP8_E5M2) {                                                                            \
+            if (dtype == FP8_DTYPE_BF16) FN<__nv_bfloat16, FP8_E5M2>(a, st);                                \
+            else if (dtype == FP8_DTYPE_F16) FN<__half, FP8_E5M2>(a, st);                                   \
+            else FN<float, FP8_E5M2>(a, st);                                                                \
+        } else {                                                                                            \
+            if (dtype == FP8_DTYPE_BF16) FN<__nv_bfloat16, FP8_E4M3FN>(a, st);                              \
+            else if (dtype == FP8_DTYPE_F16) FN<__half, FP8_E4M3FN>(a, st);                                 \
+            else FN<float, FP8_E4M3FN>(a, st);                                                              \
+        }                                                                                                   \
+    } while (0)
 
 template <int FMT>
 static void launch_swiglu_checkpoint(SwArgs a, cudaStream_t st)
@@ -320,7 +330,7 @@ static void launch_swiglu_checkpoint(SwArgs a, cudaStream_t st)
     const auto all_aligned = [&](int al) {
         return rows_aligned(a.gate_up, a.ld, a.F, 2, al) && rows_aligned(a.h, a.ld_h, 0, 2, al);
     };
-    a.geo = wide_geometry(a.rows, ckpt_width(a.F) / 16, 1);
+    a.geo = geometry(a.rows, ckpt_width(a.F) / 16, 1);
     a.w32 = all_aligned(32);
     if (all_aligned(16)) swiglu_checkpoint_kernel<FMT, false><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
     else swiglu_checkpoint_kernel<FMT, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
@@ -333,7 +343,7 @@ static void launch_swiglu_backward(SwArgs a, cudaStream_t st)
         return rows_aligned(a.dh, a.ld_dh, 0, 2, al) && rows_aligned(a.d, a.ld_d, a.F, 2, al) &&
                rows_aligned(a.h, a.h ? a.ld_h : 0, 0, 2, al) && (CKPT || rows_aligned(a.gate_up, a.ld, a.F, 2, al));
     };
-    a.geo = wide_geometry(a.rows, ckpt_width(a.F) / 16, 1);
+    a.geo = geometry(a.rows, ckpt_width(a.F) / 16, 1);
     a.w32 = all_aligned(32);
     if (all_aligned(16)) swiglu_backward_kernel<FMT, CKPT, false><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
     else swiglu_backward_kernel<FMT, CKPT, true><<<a.geo.grid, CK_THREADS, 0, st>>>(a);
@@ -350,9 +360,7 @@ extern "C" fp8_status_t fp8_checkpoint(const void *x, int dtype, int64_t rows, i
     const fp8_status_t rc = check_ck(a, dtype);
     if (rc != FP8_OK || rows == 0) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == FP8_DTYPE_BF16) launch_checkpoint<__nv_bfloat16>(a, st);
-    else if (dtype == FP8_DTYPE_F16) launch_checkpoint<__half>(a, st);
-    else launch_checkpoint<float>(a, st);
+    CK_DISPATCH(launch_checkpoint, dtype, a, st);
     return check_launch();
 }
 
@@ -364,9 +372,7 @@ extern "C" fp8_status_t fp8_checkpoint_restore(const uint8_t *q, int64_t ld_q, c
     const fp8_status_t rc = check_ck(a, dtype);
     if (rc != FP8_OK || rows == 0) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == FP8_DTYPE_BF16) launch_restore<__nv_bfloat16>(a, st);
-    else if (dtype == FP8_DTYPE_F16) launch_restore<__half>(a, st);
-    else launch_restore<float>(a, st);
+    CK_DISPATCH(launch_restore, dtype, a, st);
     return check_launch();
 }
 

@@ -88,21 +88,6 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 // carries them.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// One element per lane, a block per warp: store code and scale byte.
-__device__ __forceinline__ void ckpt_store_lane(float v, int fmt, uint8_t *q, uint8_t *s, int lane)
-{
-    const uint32_t code = ckpt_code(__reduce_max_sync(0xffffffffu, abs_bits(v)), fmt);
-    const float t = v * ckpt_inv_scale(code);
-    q[lane] = (uint8_t)(fmt == FP8_E5M2 ? cvt2<FP8_E5M2>(t, 0.0f) : cvt2<FP8_E4M3FN>(t, 0.0f));
-    if (lane == 0) *s = (uint8_t)code;
-}
-
-__device__ __forceinline__ float ckpt_load_one(const uint8_t *q, const uint8_t *s, int64_t col, int fmt)
-{
-    const float v = fmt == FP8_E5M2 ? fp8x2_to_float2<FP8_E5M2>(q[col]).x : fp8x2_to_float2<FP8_E4M3FN>(q[col]).x;
-    return v * ckpt_scale(s[col / FP8_MX_BLOCK]);
-}
-
 // ---------------------------------------------------------------------------
 // Sixteen consecutive elements per thread, half a block: 32 bytes of a 16-bit
 // type (one 32-byte access when everything is 32-byte aligned, `w32`, else

@@ -65,7 +65,7 @@ struct NormArgs {
     int G;          // threads of a row group
     int ranks;      // blocks that share a row
     int part_cols;  // columns of each of them but the last
-    int w32;  // every row of the tensors starts on a 32-byte boundary
+    int w32;        // every row of the tensors starts on a 32-byte boundary
     int64_t end_x, end_dy;  // elements from their start to the end of their last row
 };
 
@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_forward_kernel(NormArgs a)
 #pragma unroll
             for (int q = 0; q < 4; q++) {
                 const float4 w = param4(shared, chunks, i, q);
-                float2 lo = make_float2(f[k][4 * q], f[k][4 * q + 1]), hi = make_float2(f[k][4 * q + 2], f[k][4 * q + 3]);
+                float2 lo = make_float2(f[k][4 * q], f[k][4 * q + 1]);
+                float2 hi = make_float2(f[k][4 * q + 2], f[k][4 * q + 3]);
                 if (a.bias) {
                     const float4 b = param4(shared + chunks * 16, chunks, i, q);
                     lo = fma2(lo, make_float2(w.x, w.y), make_float2(b.x, b.y));
@@ -466,7 +467,7 @@ __device__ __forceinline__ void xhat16(const NormArgs &a, const RawBackward<TX, 
     }
 }
 
-// Rows ahead of the fused backward, in shared memory: each warp copies its own
+// Rows ahead of the backward, in shared memory: each warp copies its own
 // columns of dy and of x (or the codes) with cp.async into a ring, so the loads
 // in flight cost no registers and no block barrier, and the registers hold two
 // rows at a time, whose sums share one barrier and each other's latencies.
@@ -588,13 +589,14 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
             } else {
                 const uint32_t at = ring + (stage * ROWS + i) * row_bytes;
                 const int have = live ? cols - col0 : 0;
-                copy_ahead<DY, MULTI>(at, static_cast<const TY *>(a.dy) + row * a.ld_dy + col0, have * (int)sizeof(TY), cp,
-                               a.dy);
-                if constexpr (CKPT)
-                    copy_ahead<X, MULTI>(at + DY * 512, a.q + row * a.ld_q + col0, have > 0 ? have + 15 & ~15 : 0, cp, a.q);
+                copy_ahead<DY, MULTI>(at, static_cast<const TY *>(a.dy) + row * a.ld_dy + col0,
+                                      have * (int)sizeof(TY), cp, a.dy);
+                if constexpr (CKPT)  // whole chunks of codes: a checkpoint's rows end on one
+                    copy_ahead<X, MULTI>(at + DY * 512, a.q + row * a.ld_q + col0,
+                                         have > 0 ? (have + 15) & ~15 : 0, cp, a.q);
                 else
                     copy_ahead<X, MULTI>(at + DY * 512, static_cast<const TX *>(a.x) + row * a.ld_x + col0,
-                                  have * (int)sizeof(TX), cp, a.x);
+                                         have * (int)sizeof(TX), cp, a.x);
             }
             if (live && !LANES) {
                 rstd_q[AHEAD - 1][i] = __ldg(a.rstd + row);
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
             parts[i] = make_float2(0.0f, 0.0f);
     __syncthreads();
 
-    float2 dw[8] = {}, db[8] = {};  // ACC: one chunk a thread
+    float2 dw[8] = {}, db[8] = {};  // of this thread's columns, over all its rows
     int slot = 0, stage = 0;
     // the groups of a warp go on until the first of them is done
     for (; (MULTI ? r : r - cp.sub) < rows; r += ROWS * step) {
@@ -648,7 +650,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
                 for (int j = 0; j < DY; j++) raw[i].dy.v[j] = copied<DY>(at, lane, j);
                 if constexpr (CKPT) {
                     raw[i].q = copied<X>(at + DY * 512, lane, 0);
-                    const uint32_t s = __shfl_sync(0xffffffffu, scale, lane & ~1 | i);
+                    const uint32_t s = __shfl_sync(0xffffffffu, scale, (lane & ~1) | i);
                     raw[i].s = r + i * step < rows ? s : 127u;
                 } else {
 #pragma unroll
