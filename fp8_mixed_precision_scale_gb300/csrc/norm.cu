@@ -293,7 +293,7 @@ __device__ __forceinline__ float sum16(const float (&f)[16])
 // instructions an element ([32768, 4096] 89.7 us, 6.0 TB/s; with the checkpoint
 // [32768, 7168] 197 us, 6.0 TB/s).
 template <typename TX, typename TY, int CH, bool MULTI, bool ANY, bool CLUSTER>
-__global__ void __launch_bounds__(NM_BLOCK) norm_forward_kernel(NormArgs a)
+__global__ void __launch_bounds__(NM_BLOCK, CH == 1 && !ANY ? 2 : 1) norm_forward_kernel(NormArgs a)
 {
     extern __shared__ __align__(16) float shared[];  // weight, bias
     __shared__ __align__(16) float2 parts[MULTI ? NM_MAX_GROUPS * 4 * NM_GROUP_WARPS : 1];
@@ -869,8 +869,9 @@ static int clusters_at_once(int ranks)
 
 // `chunks` chunks a thread where a warp's lanes do not cover the row (one where
 // they do).  Few rows are spread over the SMs before a second group joins a
-// block.
-static Plan make_plan(int64_t rows, int64_t cols, int chunks)
+// block.  `small`: a kernel of one chunk and part-warp groups takes 64 registers,
+// two blocks an SM.
+static Plan make_plan(int64_t rows, int64_t cols, int chunks, bool small = false)
 {
     Plan p;
     p.ranks = 1;
@@ -896,7 +897,8 @@ static Plan make_plan(int64_t rows, int64_t cols, int chunks)
     if (!p.multi) groups = (groups * p.G + 31) / 32 * 32 / p.G;  // whole warps
     if (groups < 1 || p.ranks > 1) groups = 1;
     p.threads = (unsigned)(groups * p.G);
-    const int64_t most = clusters_at_once(p.ranks), blocks = (rows + groups - 1) / groups;
+    const int64_t most = (int64_t)clusters_at_once(p.ranks) * (small && p.chunks == 1 && !p.multi ? 2 : 1);
+    const int64_t blocks = (rows + groups - 1) / groups;
     p.slices = (int)(blocks < most ? blocks : most);
     p.grid = (unsigned)(p.slices * p.ranks);
     return p;
@@ -931,7 +933,7 @@ static void launch(K kernel, const Plan &p, int smem, NormArgs a, cudaStream_t s
 template <typename TX, typename TY, bool ANY>
 static void launch_forward_as(const NormArgs &a, cudaStream_t st)
 {
-    const Plan p = make_plan(a.rows, a.cols, 2);
+    const Plan p = make_plan(a.rows, a.cols, 2, !ANY);
     const int smem = p.chunks * p.G * 16 * (int)sizeof(float) * (a.bias ? 2 : 1);
     if (p.ranks > 1) launch(norm_forward_kernel<TX, TY, 2, true, ANY, true>, p, smem, a, st);
     else if (p.chunks == 1) launch(norm_forward_kernel<TX, TY, 1, false, ANY, false>, p, smem, a, st);

@@ -591,7 +591,7 @@ FP8GB_API fp8_status_t fp8_swiglu_backward(const void *dh_bf16, int64_t ld_dh, c
  *   weight, bias   [cols] of w_dtype; NULL: 1 and 0.
  *   mean, rstd     fp32 [rows], each optional.
  *   q, s           optional (both or neither): the checkpoint of xh.
- *   eps >= 0; a row holding a NaN or Inf gives NaN in that row alone.
+ *   eps >= 0.  A NaN or Inf stays in its row, as the formulas carry it.
  *
  * fp8_norm_backward -- with g = dy w, c1 = sum g / n (0 for RMS),
  *   c2 = sum g xh / n:  dx = r (g - c1 - xh c2),  dweight = sum over rows of

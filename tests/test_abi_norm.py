@@ -141,3 +141,16 @@ def test_norm_validation(lib):
     assert c(ws=FAKE + 4) == ALIGN
     assert c(yt=1) == UNSUPPORTED
     assert c(dw=FAKE + 1) == ALIGN
+
+
+def test_wrappers_refuse_host_tensors():
+    """The Python wrappers check where a tensor lies before anything else."""
+    import torch
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    c = fp8.Checkpoint(torch.zeros((4, 64), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8), 0, 64)
+    for call in (lambda: fp8.norm_forward(x), lambda: fp8.norm_backward(x, x, None, x[:, 0].float()),
+                 lambda: fp8.checkpoint(x), lambda: fp8.checkpoint_restore(c), lambda: fp8.swiglu_checkpoint(x),
+                 lambda: fp8.swiglu_backward(x, x)):
+        with pytest.raises(fp8.Fp8Error) as e:
+            call()
+        assert e.value.status == INVALID
