@@ -257,7 +257,9 @@ __device__ __forceinline__ int take_part(NormArgs &a, int rank)
 // Sums of N values over the blocks of a cluster, in rank order; every thread
 // gets the same bits.  Called by all threads of every block equally often,
 // with alternating slots: a slot is written again only after every block has
-// passed the barrier in between, and so has read it.
+// passed the barrier in between, and so has read it.  A kernel passes a cluster
+// barrier before its first call, since a block that has not started has no shared
+// memory to write to.
 template <int N>
 __device__ __forceinline__ void cluster_sum(float (&v)[N], float (*trade)[NM_MAX_RANKS][4], int slot, int rank,
                                             int ranks)
@@ -328,6 +330,7 @@ __global__ void __launch_bounds__(NM_BLOCK, CH == 1 && !ANY ? 2 : 1) norm_forwar
         for (int i = threadIdx.x; i < NM_MAX_GROUPS * 4 * NM_GROUP_WARPS; i += blockDim.x)
             parts[i] = make_float2(0.0f, 0.0f);
     __syncthreads();
+    if constexpr (CLUSTER) cluster_sync();  // all its blocks run: cluster_sum may write to them
 
     int slot = 0;
     for (; first < a.rows; first += step, r += step) {
@@ -643,6 +646,7 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
         for (int i = threadIdx.x; i < NM_MAX_GROUPS * 4 * NM_GROUP_WARPS; i += blockDim.x)
             parts[i] = make_float2(0.0f, 0.0f);
     __syncthreads();
+    if constexpr (CLUSTER) cluster_sync();  // all its blocks run: cluster_sum may write to them
 
     float2 dw[8] = {}, db[8] = {};  // of this thread's columns, over all its rows
     int slot = 0, stage = 0;
