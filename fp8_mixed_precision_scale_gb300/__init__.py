@@ -666,7 +666,9 @@ def _on(stream):
     """Context that makes `stream` current: torch then allocates for it, and
     what is dropped at return (a workspace) is reused in that stream's order."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        handle = int(stream)
+        # ExternalStream takes 0, the default stream's handle, as none given and makes a stream of its own
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
 
 
