@@ -580,7 +580,9 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
     RawBackward<TX, TY, CKPT, ANY> raw[ROWS];
     // statistics of the steps ahead, the next one first.  Two rows in whole
     // warps: one register, lanes 4 i to 4 i + 3 holding rstd and mean of row 0
-    // and of row 1 (a value that is spilled on arrival is waited for)
+    // and of row 1 (a value that is spilled on arrival is waited for).  0 for rows
+    // past the last: their dy is 0, but times what another row's statistics make
+    // of x = 0 it would be NaN where mean * rstd overflows
     constexpr bool LANES = MULTI && ROWS == 2;
     float mean_q[AHEAD][ROWS] = {}, rstd_q[AHEAD][ROWS] = {}, stat = 0.0f;
     uint32_t scale = 127;
@@ -610,13 +612,17 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
                     copy_ahead<X, MULTI>(at + DY * 512, static_cast<const TX *>(a.x) + row * a.ld_x + col0,
                                          have * (int)sizeof(TX), cp, a.x);
             }
-            if (live && !LANES) {
-                rstd_q[AHEAD - 1][i] = __ldg(a.rstd + row);
-                if (!CKPT && !a.rms) mean_q[AHEAD - 1][i] = __ldg(a.mean + row);
+            if (!LANES) {
+                rstd_q[AHEAD - 1][i] = mean_q[AHEAD - 1][i] = 0.0f;
+                if (live) {
+                    rstd_q[AHEAD - 1][i] = __ldg(a.rstd + row);
+                    if (!CKPT && !a.rms) mean_q[AHEAD - 1][i] = __ldg(a.mean + row);
+                }
             }
         }
         if (LANES) {
             const uint32_t row = row0 + (lane >> 1 & 1) * step;
+            stat = 0.0f;
             if (row < rows) stat = __ldg((lane & 1 && !CKPT && !a.rms ? a.mean : a.rstd) + row);
         }
         if (CKPT && S > 0) {

@@ -1,5 +1,5 @@
 """GPU tests of the norm, SwiGLU and checkpoint operators where callers and
-values leave the usual: the default stream by its handle."""
+values leave the usual: the default stream by its handle, rows past the last one."""
 import pytest
 import torch
 
@@ -42,3 +42,22 @@ def test_default_stream_by_its_handle():
         assert torch.equal(f.y, want.y) and torch.equal(b.dx, back.dx) and torch.equal(b.dweight, back.dweight)
         assert torch.equal(c.q, gate_up.q) and torch.equal(h2, h) and torch.equal(d, grad)
         assert torch.equal(r, fp8.checkpoint_restore(gate_up))
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (F16, F16), (F32, BF16), (F32, F32)])
+@pytest.mark.parametrize("cols", [64, 100, 1024, 1111, 8200])
+@pytest.mark.parametrize("rows", [37, 700, 4500])
+def test_rows_past_the_end_add_nothing(rows, cols, types):
+    """Constant rows with mean * rstd above fp32's range: xhat is 0 in every row,
+    so dweight is exactly 0, also where a group's last step reaches past the
+    rows (the row before's mean * rstd, times a dy of 0, would be NaN)."""
+    tx, ty = types
+    value = 2.0 ** 15 if tx == F16 else 2.0 ** 120
+    x = torch.full((rows, cols), value, dtype=tx, device=DEV)
+    dy = torch.ones((rows, cols), dtype=ty, device=DEV)
+    mean = torch.full((rows,), value, dtype=F32, device=DEV)
+    rstd = torch.full((rows,), 2.0 ** 128 / value * (1 - 2.0 ** -24), dtype=F32, device=DEV) * 2
+    b = fp8.norm_backward(dy, x, mean, rstd, torch.ones(cols, dtype=F32, device=DEV))
+    assert not b.dx.isnan().any()
+    assert int((b.dweight != 0).sum()) == 0
+    assert bool((b.dbias == rows).all())   # sums of ones below 2^24 are exact
