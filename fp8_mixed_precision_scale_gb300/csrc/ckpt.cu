@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(CK_THREADS) restore_kernel(CkArgs a)
         const int64_t r = p.row + (int64_t)k * p.ty;
         float f[16];
         decode16<FMT>(q[k], ckpt_scale(s[k]), f);
+        if constexpr (__is_same(T, __half)) hold_65536(f);
         store_chunk<ANY>(x + r * a.ld_x, f, r < a.rows ? rest : 0, a.w32, c == 0 ? 0 : t, rest <= 16 ? t + 1 : lanes);
     }
 }

@@ -9,8 +9,12 @@
 // MX rule clips to fp8_max: a checkpoint has no tensor core to please, so
 // nothing is clipped and every normal element is within 2^-4 (E4M3) or 2^-3
 // (E5M2) of itself.  The scales are powers of two, so scaling by them is
-// exact both ways and the conversion to 8 bits is the only rounding.  An all-zero block
-// has byte 0; a block with a NaN or Inf has byte 255 and restores as NaN.
+// exact both ways and the conversion to 8 bits is the only rounding.  That one
+// can go up to the next power of two, which at the top of a type's range lies
+// outside: fp16 takes it back (hold_65536), while bf16 and fp32 values from 1.9375 *
+// 2^127 (E4M3) or 1.875 * 2^127 (E5M2) on restore as Inf, for 2^128 is what
+// their code and scale stand for.  An all-zero block has byte 0; a block with a
+// NaN or Inf has byte 255 and restores as NaN.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -436,6 +440,15 @@ __device__ __forceinline__ void decode16(const uint4 &q, float scale, float (&f)
         mul2_rn(f[4 * j], f[4 * j + 1], scale, scale);
         mul2_rn(f[4 * j + 2], f[4 * j + 3], scale, scale);
     }
+}
+
+// Restored fp16 values: +-65536 as +-65504.  The largest finite fp16 values
+// (from 63488 on in E4M3, 61440 in E5M2) are kept as 65536, which fp16 would round
+// to Inf; 65504 is nearer to them.  Anything larger was no finite fp16 value.
+__device__ __forceinline__ void hold_65536(float (&f)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 16; j++) f[j] = fabsf(f[j]) == 65536.0f ? copysignf(65504.0f, f[j]) : f[j];
 }
 
 // Packed pairs of fp32, each operation rounded to nearest.

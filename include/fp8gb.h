@@ -532,7 +532,9 @@ FP8GB_API fp8_status_t fp8_mx_grouped_gemm(int mode, const uint8_t *A, int fa, c
  * byte e + 127 (0 for an all-zero block); a block with a NaN or Inf has byte
  * 255 and restores as NaN.  Each element is rne_fp8(v / X): nothing finite
  * saturates, and an element of at least 2^-13 (E4M3; 2^-28 for E5M2) of its
- * block's largest restores within 2^-4 (2^-3) of itself.  Several `parts` of the
+ * block's largest restores within 2^-4 (2^-3) of itself, except that bf16 and
+ * fp32 values of 1.9375 * 2^127 (E5M2: 1.875 * 2^127) and more round up to
+ * 2^128 and so restore as Inf.  Several `parts` of the
  * same width side by side (gate | up) each start a block: with W = roundup(
  * cols, 32), part p's codes are at [row * ld_q + p * W] and its scale bytes
  * at [row * ld_s + p * W / 32]; codes between cols and W are 0.  q is
@@ -546,7 +548,9 @@ enum { FP8_NORM_LAYER = 0, FP8_NORM_RMS = 1 };
  * fp8_checkpoint -- store x [rows][ld_x] (parts tensors of cols columns side
  * by side: part p at column p * cols) as codes and scale bytes.
  * fp8_checkpoint_restore -- the inverse: x = code * X, rounded to the type
- * (exact in bf16 and fp32 unless it falls below their range).
+ * (exact in bf16 and fp32 unless it falls outside their range).  In fp16
+ * +-65536, which stands for the largest finite values of that type, restores
+ * as +-65504: every finite fp16 tensor restores finite.
  * rows == 0 returns FP8_OK without touching any buffer.
  */
 FP8GB_API fp8_status_t fp8_checkpoint(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ld_x, int parts,

@@ -1,5 +1,6 @@
 """GPU tests of the norm, SwiGLU and checkpoint operators where callers and
-values leave the usual: the default stream by its handle, rows past the last one."""
+values leave the usual: the default stream by its handle, rows past the last one,
+the largest values of a type."""
 import pytest
 import torch
 
@@ -61,3 +62,20 @@ def test_rows_past_the_end_add_nothing(rows, cols, types):
     assert not b.dx.isnan().any()
     assert int((b.dweight != 0).sum()) == 0
     assert bool((b.dbias == rows).all())   # sums of ones below 2^24 are exact
+
+
+@pytest.mark.parametrize("fmt", [fp8.E4M3FN, fp8.E5M2])
+@pytest.mark.parametrize("cols,pad", [(64, 0), (100, 0), (77, 3)])
+def test_finite_fp16_restores_finite(cols, pad, fmt):
+    """Every finite fp16 magnitude of the top binade, both signs: back within
+    2^-4 (E4M3) or 2^-3 (E5M2) of itself, half a step of a 3 or 2 bit mantissa."""
+    top = torch.arange(0x7800, 0x7C00, dtype=torch.int16, device=DEV).view(F16)   # 32768 .. 65504
+    x = torch.ones((32, cols + pad), dtype=F16, device=DEV)[:, :cols]
+    x[:16, :64] = top.view(16, 64)
+    x[16:, :64] = -top.view(16, 64)
+    back = fp8.checkpoint_restore(fp8.checkpoint(x, fmt), F16, out=torch.empty_like(x))
+    assert torch.isfinite(back).all()
+    off = (back.double() - x.double()).abs()[:, :64]
+    assert bool((off <= 2.0 ** (-4 if fmt == fp8.E4M3FN else -3) * x.double().abs()[:, :64]).all())
+    back = fp8.checkpoint_restore(fp8.checkpoint(x.float() * 4, fmt), F16)        # beyond fp16: Inf, as any conversion
+    assert torch.isinf(back[:, :64]).all() and torch.equal(back[:, :64] > 0, x[:, :64] > 0)
