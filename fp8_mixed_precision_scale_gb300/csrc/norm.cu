@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(NM_COLS * NM_SUM_LANES) norm_dw_sum_kernel(Nor
     }
 }
 
-static void launch_dw_sum(NormArgs a, int slices, cudaStream_t st)
+static fp8_status_t launch_dw_sum(NormArgs a, int slices, cudaStream_t st)
 {
     a.splits = slices;
     cudaLaunchAttribute attr;
@@ -824,6 +824,7 @@ static void launch_dw_sum(NormArgs a, int slices, cudaStream_t st)
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     cudaLaunchKernelEx(&cfg, norm_dw_sum_kernel, a);
+    return check_launch();
 }
 
 static bool rows_aligned(const void *p, int64_t ld, int size, int al)
@@ -841,6 +842,49 @@ struct Plan {
     int slices;      // of the rows, one a block (or cluster): slices of the workspace too
 };
 
+// Dynamic shared memory of a launch, and the most that any launch of the kernel
+// takes: NM_BLOCK threads, of which a row of up to 32 threads' chunks needs the
+// parameters of no more than these.
+static constexpr int forward_shared(int chunks, int G, bool bias)
+{
+    return chunks * G * 16 * (int)sizeof(float) * (bias ? 2 : 1);
+}
+
+static constexpr int forward_shared_most(bool multi) { return forward_shared(2, multi ? NM_BLOCK : 32, true); }
+
+template <typename TX, typename TY, bool CKPT, bool ANY>
+static constexpr int backward_shared(int G, int threads)
+{
+    using R = Ring<TX, TY, CKPT>;
+    return 2 * G * 16 * (int)sizeof(float) + (ANY ? 0 : R::stages * R::rows * R::slots * 16 * threads);
+}
+
+template <typename TX, typename TY, bool CKPT, bool ANY>
+static constexpr int backward_shared_most(bool multi)
+{
+    return backward_shared<TX, TY, CKPT, ANY>(multi ? NM_BLOCK : 32, NM_BLOCK);
+}
+
+// 48 KB without asking, the kernel's own few KB among them.
+constexpr int NM_SHARED_FREE = 40 * 1024;
+
+// Lets a kernel's launches take more than that.  The limit belongs to the kernel
+// and device, not to a launch, and other host threads may be about to launch with
+// it: it is set once, to the most that any launch takes, and never lowered.
+template <auto KERNEL, int MOST>
+static bool allow_shared()
+{
+    constexpr int MAX_DEVICES = 64;
+    static std::atomic<bool> allowed[MAX_DEVICES];
+    static_assert(MOST + 8 * 1024 <= 227 * 1024, "more than a block can have");
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < MAX_DEVICES && allowed[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST) != cudaSuccess) return false;
+    if (dev < MAX_DEVICES) allowed[dev].store(true, std::memory_order_release);
+    return true;
+}
+
 // Blocks (of one to an SM) that run at once in clusters of `ranks`, in
 // clusters.  The SMs of a GPC are no multiple of 4 or 8, so it is fewer than the
 // SMs would give: a grid for all SMs leaves clusters for a second wave ([2048,
@@ -855,8 +899,8 @@ static int clusters_at_once(int ranks)
     if (ranks == 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return most;
     int n = known[dev][ranks].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    using R = Ring<__nv_bfloat16, __nv_bfloat16, false>;
-    const auto kernel = norm_backward_kernel<__nv_bfloat16, __nv_bfloat16, true, false, false, true>;
+    constexpr auto kernel = norm_backward_kernel<__nv_bfloat16, __nv_bfloat16, true, false, false, true>;
+    constexpr int shared = backward_shared_most<__nv_bfloat16, __nv_bfloat16, false, false>(true);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)ranks;
@@ -864,12 +908,11 @@ static int clusters_at_once(int ranks)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(most * ranks));
     cfg.blockDim = dim3(NM_BLOCK);
-    cfg.dynamicSmemBytes = 2 * NM_PART * (int)sizeof(float) + R::stages * R::rows * R::slots * 16 * NM_BLOCK;
+    cfg.dynamicSmemBytes = shared;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1 || n > most) {
+    if (!allow_shared<kernel, shared>() || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1 ||
+        n > most) {
         cudaGetLastError();
         n = most;
     }
@@ -914,18 +957,13 @@ static Plan make_plan(int64_t rows, int64_t cols, int chunks, bool small = false
     return p;
 }
 
-template <typename K>
-static void launch(K kernel, const Plan &p, int smem, NormArgs a, cudaStream_t st)
+template <auto KERNEL, int MOST>
+static fp8_status_t launch(const Plan &p, int smem, NormArgs a, cudaStream_t st)
 {
     a.G = p.G;
     a.ranks = p.ranks;
     a.part_cols = p.part_cols;
-    // 48 KB without asking, the kernel's own few KB among them
-    if (smem > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (p.ranks == 1) {
-        kernel<<<p.grid, p.threads, smem, st>>>(a);
-        return;
-    }
+    if (smem > NM_SHARED_FREE && !allow_shared<KERNEL, MOST>()) return cuda_fail();
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)p.ranks;
@@ -936,54 +974,54 @@ static void launch(K kernel, const Plan &p, int smem, NormArgs a, cudaStream_t s
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, kernel, a);
+    cfg.numAttrs = p.ranks > 1;
+    cudaLaunchKernelEx(&cfg, KERNEL, a);
+    return check_launch();
 }
 
 template <typename TX, typename TY, bool ANY>
-static void launch_forward_as(const NormArgs &a, cudaStream_t st)
+static fp8_status_t launch_forward_as(const NormArgs &a, cudaStream_t st)
 {
     const Plan p = make_plan(a.rows, a.cols, 2, !ANY);
-    const int smem = p.chunks * p.G * 16 * (int)sizeof(float) * (a.bias ? 2 : 1);
-    if (p.ranks > 1) launch(norm_forward_kernel<TX, TY, 2, true, ANY, true>, p, smem, a, st);
-    else if (p.chunks == 1) launch(norm_forward_kernel<TX, TY, 1, false, ANY, false>, p, smem, a, st);
-    else if (!p.multi) launch(norm_forward_kernel<TX, TY, 2, false, ANY, false>, p, smem, a, st);
-    else launch(norm_forward_kernel<TX, TY, 2, true, ANY, false>, p, smem, a, st);
+    const int smem = forward_shared(p.chunks, p.G, a.bias != nullptr);
+    constexpr int narrow = forward_shared_most(false), wide = forward_shared_most(true);
+    if (p.ranks > 1) return launch<norm_forward_kernel<TX, TY, 2, true, ANY, true>, wide>(p, smem, a, st);
+    if (p.chunks == 1) return launch<norm_forward_kernel<TX, TY, 1, false, ANY, false>, narrow>(p, smem, a, st);
+    if (!p.multi) return launch<norm_forward_kernel<TX, TY, 2, false, ANY, false>, narrow>(p, smem, a, st);
+    return launch<norm_forward_kernel<TX, TY, 2, true, ANY, false>, wide>(p, smem, a, st);
 }
 
 template <typename TX, typename TY>
-static void launch_forward(NormArgs a, cudaStream_t st)
+static fp8_status_t launch_forward(NormArgs a, cudaStream_t st)
 {
     const auto all_aligned = [&](int al) {
         return rows_aligned(a.x, a.ld_x, sizeof(TX), al) && rows_aligned(a.out, a.ld_out, sizeof(TY), al);
     };
     a.w32 = all_aligned(32);
-    if (all_aligned(16)) launch_forward_as<TX, TY, false>(a, st);
-    else launch_forward_as<TX, TY, true>(a, st);
+    return all_aligned(16) ? launch_forward_as<TX, TY, false>(a, st) : launch_forward_as<TX, TY, true>(a, st);
 }
 
 template <typename TX, typename TY, bool CKPT, bool ANY>
-static void launch_backward_as(NormArgs a, cudaStream_t st)
+static fp8_status_t launch_backward_as(NormArgs a, cudaStream_t st)
 {
     const Plan p = make_plan(a.rows, a.cols, 1);
-    using R = Ring<TX, TY, CKPT>;
-    const int ring = ANY ? 0 : R::stages * R::rows * R::slots * 16 * (int)p.threads;
-    const int smem = 2 * p.G * 16 * (int)sizeof(float) + ring;
+    const int smem = backward_shared<TX, TY, CKPT, ANY>(p.G, (int)p.threads);
+    constexpr int narrow = backward_shared_most<TX, TY, CKPT, ANY>(false);
+    constexpr int wide = backward_shared_most<TX, TY, CKPT, ANY>(true);
     const bool grads = a.dweight || a.dbias;
     if (!grads) a.part = nullptr;
-    if (p.ranks > 1) launch(norm_backward_kernel<TX, TY, true, CKPT, ANY, true>, p, smem, a, st);
-    else if (p.multi) launch(norm_backward_kernel<TX, TY, true, CKPT, ANY, false>, p, smem, a, st);
-    else launch(norm_backward_kernel<TX, TY, false, CKPT, ANY, false>, p, smem, a, st);
-    if (grads) launch_dw_sum(a, p.slices, st);
+    fp8_status_t rc;
+    if (p.ranks > 1) rc = launch<norm_backward_kernel<TX, TY, true, CKPT, ANY, true>, wide>(p, smem, a, st);
+    else if (p.multi) rc = launch<norm_backward_kernel<TX, TY, true, CKPT, ANY, false>, wide>(p, smem, a, st);
+    else rc = launch<norm_backward_kernel<TX, TY, false, CKPT, ANY, false>, narrow>(p, smem, a, st);
+    return rc == FP8_OK && grads ? launch_dw_sum(a, p.slices, st) : rc;  // no sums of slices never written
 }
 
 template <typename TX, typename TY>
-static void launch_backward(NormArgs a, cudaStream_t st)
+static fp8_status_t launch_backward(NormArgs a, cudaStream_t st)
 {
-    if (a.rows == 0) {  // gradients of zero: no slices to add
-        if (a.dweight || a.dbias) launch_dw_sum(a, 0, st);
-        return;
-    }
+    if (a.rows == 0)  // gradients of zero: no slices to add
+        return a.dweight || a.dbias ? launch_dw_sum(a, 0, st) : FP8_OK;
     const auto all_aligned = [&](int al) {
         return rows_aligned(a.dy, a.ld_dy, sizeof(TY), al) && rows_aligned(a.out, a.ld_out, sizeof(TX), al) &&
                rows_aligned(a.x, a.ld_x, sizeof(TX), al);
@@ -992,10 +1030,10 @@ static void launch_backward(NormArgs a, cudaStream_t st)
     a.end_dy = rows_end(a.ld_dy, a.rows, a.cols);
     a.end_x = rows_end(a.ld_x, a.rows, a.cols);
     const bool any = !all_aligned(16);
-    if (a.x && any) launch_backward_as<TX, TY, false, true>(a, st);
-    else if (a.x) launch_backward_as<TX, TY, false, false>(a, st);
-    else if (any) launch_backward_as<TX, TY, true, true>(a, st);
-    else launch_backward_as<TX, TY, true, false>(a, st);
+    if (a.x && any) return launch_backward_as<TX, TY, false, true>(a, st);
+    if (a.x) return launch_backward_as<TX, TY, false, false>(a, st);
+    if (any) return launch_backward_as<TX, TY, true, true>(a, st);
+    return launch_backward_as<TX, TY, true, false>(a, st);
 }
 
 static bool good_dtype(int d) { return d >= FP8_DTYPE_BF16 && d <= FP8_DTYPE_F32; }
@@ -1035,13 +1073,11 @@ static fp8_status_t check_fmt(int fmt)
 
 // The five pairs of types: equal ones, and an fp32 x with 16-bit y.
 #define NORM_TYPES(FN, xt, yt, ...)                                                        \
-    do {                                                                                   \
-        if (xt == FP8_DTYPE_BF16) FN<__nv_bfloat16, __nv_bfloat16>(__VA_ARGS__);           \
-        else if (xt == FP8_DTYPE_F16) FN<__half, __half>(__VA_ARGS__);                     \
-        else if (yt == FP8_DTYPE_BF16) FN<float, __nv_bfloat16>(__VA_ARGS__);              \
-        else if (yt == FP8_DTYPE_F16) FN<float, __half>(__VA_ARGS__);                      \
-        else FN<float, float>(__VA_ARGS__);                                                \
-    } while (0)
+    (xt == FP8_DTYPE_BF16   ? FN<__nv_bfloat16, __nv_bfloat16>(__VA_ARGS__)                \
+     : xt == FP8_DTYPE_F16  ? FN<__half, __half>(__VA_ARGS__)                              \
+     : yt == FP8_DTYPE_BF16 ? FN<float, __nv_bfloat16>(__VA_ARGS__)                        \
+     : yt == FP8_DTYPE_F16  ? FN<float, __half>(__VA_ARGS__)                               \
+                            : FN<float, float>(__VA_ARGS__))
 
 }  // namespace fp8gb
 
@@ -1080,8 +1116,7 @@ extern "C" fp8_status_t fp8_norm_forward(const void *x, int x_dtype, int64_t ld_
     a.w_dtype = w_dtype;
     a.mean_out = mean;
     a.rstd_out = rstd;
-    NORM_TYPES(launch_forward, x_dtype, y_dtype, a, static_cast<cudaStream_t>(stream));
-    return check_launch();
+    return NORM_TYPES(launch_forward, x_dtype, y_dtype, a, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int64_t fp8_norm_workspace_bytes(int64_t rows, int64_t cols)
@@ -1138,6 +1173,5 @@ extern "C" fp8_status_t fp8_norm_backward(const void *dy, int y_dtype, int64_t l
     a.dweight = dweight;
     a.dbias = dbias;
     a.part = static_cast<float *>(workspace);
-    NORM_TYPES(launch_backward, x_dtype, y_dtype, a, static_cast<cudaStream_t>(stream));
-    return check_launch();
+    return NORM_TYPES(launch_backward, x_dtype, y_dtype, a, static_cast<cudaStream_t>(stream));
 }

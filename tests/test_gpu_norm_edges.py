@@ -1,6 +1,8 @@
 """GPU tests of the norm, SwiGLU and checkpoint operators where callers and
 values leave the usual: the default stream by its handle, rows past the last one,
-the largest values of a type."""
+the largest values of a type, host threads side by side."""
+import threading
+
 import pytest
 import torch
 
@@ -79,3 +81,44 @@ def test_finite_fp16_restores_finite(cols, pad, fmt):
     assert bool((off <= 2.0 ** (-4 if fmt == fp8.E4M3FN else -3) * x.double().abs()[:, :64]).all())
     back = fp8.checkpoint_restore(fp8.checkpoint(x.float() * 4, fmt), F16)        # beyond fp16: Inf, as any conversion
     assert torch.isinf(back[:, :64]).all() and torch.equal(back[:, :64] > 0, x[:, :64] > 0)
+
+
+def test_host_threads_at_different_widths():
+    """Calls of one kernel at different widths from several host threads, on
+    streams of their own: none is refused for the shared memory another asked for."""
+    calls, rows = 20000, 4
+    lib = fp8.load_library()
+    refused, wrong = {}, []
+
+    def caller(cols, backward):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            g = torch.Generator(device=DEV).manual_seed(cols)
+            x, dy = (torch.randn((rows, cols), generator=g, device=DEV).to(BF16) for _ in range(2))
+            w = torch.ones(cols, dtype=F32, device=DEV)
+            f = fp8.norm_forward(x, w, w)
+            want = fp8.norm_backward(dy, x, f.mean, f.rstd, w)
+            y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+            n = fp8.fp8_norm_workspace_bytes(rows, cols)
+            ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+            P = lambda t: t.data_ptr()  # noqa: E731
+            if backward:
+                fn, args = lib.fp8_norm_backward, (P(dy), 0, cols, P(x), cols, None, 0, None, 0, 0, rows, cols, 0,
+                                                   P(f.mean), P(f.rstd), P(w), 2, P(dx), 0, cols, P(dw), None, P(ws),
+                                                   n, side.cuda_stream)
+            else:
+                fn, args = lib.fp8_norm_forward, (P(x), 0, cols, rows, cols, 0, 1e-5, P(w), P(w), 2, P(y), 0, cols,
+                                                  None, None, 0, None, 0, None, 0, side.cuda_stream)
+            refused[cols, backward] = sum(fn(*args) != 0 for _ in range(calls))
+            side.synchronize()
+            if not (torch.equal(dx, want.dx) and torch.equal(dw, want.dweight) if backward else torch.equal(y, f.y)):
+                wrong.append((cols, backward))
+
+    threads = [threading.Thread(target=caller, args=a)
+               for a in ((8192, True), (4096, True), (6144, True), (16384, False), (8192, False))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(refused) == len(threads) and not any(refused.values()), refused
+    assert not wrong
