@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(CK_THREADS) restore_kernel(CkArgs a)
     const bool in = p.chunk < a.parts * cpp;
     const int64_t part = a.parts == 1 ? 0 : p.chunk / cpp, c = (p.chunk - part * cpp) * 16;
     const int rest = in ? chunk_rest(a.cols, c) : 0;
-    // a part's first and last chunk have no neighbours, whatever the lanes beside them hold
+    // a part's first chunk has no neighbour before it, whatever the lane there holds
     const int lanes = 1 << a.geo.lg, t = threadIdx.x & (lanes - 1);
     T *x = static_cast<T *>(a.x) + part * a.cols + c;
     uint4 q[RESTORE_UNROLL];
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(CK_THREADS) restore_kernel(CkArgs a)
         float f[16];
         decode16<FMT>(q[k], ckpt_scale(s[k]), f);
         if constexpr (__is_same(T, __half)) hold_65536(f);
-        store_chunk<ANY>(x + r * a.ld_x, f, r < a.rows ? rest : 0, a.w32, c == 0 ? 0 : t, rest <= 16 ? t + 1 : lanes);
+        store_chunk<ANY>(x + r * a.ld_x, f, r < a.rows ? rest : 0, a.w32, c == 0 ? 0 : t, lanes);
     }
 }
 

@@ -38,7 +38,7 @@ namespace fp8gb {
 
 constexpr int NM_COLS = 32;            // columns of a block of the last sums
 constexpr int NM_BLOCK = 512;          // threads of a block at most: 128 registers each
-constexpr int NM_MAX_GROUPS = 15;      // row groups with a named barrier each
+constexpr int NM_MAX_GROUPS = NM_BLOCK / 64;  // row groups of two warps or more, a named barrier each
 constexpr int NM_GROUP_WARPS = 16;     // warps of a row group at most
 constexpr int NM_MAX_RANKS = 8;        // blocks of a cluster at most
 constexpr int NM_PART = 16 * 32 * NM_GROUP_WARPS;  // columns one chunk a thread covers in a block
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(NM_BLOCK, CH == 1 && !ANY ? 2 : 1) norm_forwar
     const float inv_n = 1.0f / (float)a.cols;
     const int rank = CLUSTER ? (int)cluster_ctarank() : 0;
     const int64_t end = rows_end(a.ld_x, a.rows, a.cols) - (CLUSTER ? rank * a.part_cols : 0);
-    if (CLUSTER && a.out) a.out = static_cast<TY *>(a.out) + rank * a.part_cols;
+    if (CLUSTER) a.out = static_cast<TY *>(a.out) + rank * a.part_cols;
     const int cols = CLUSTER ? take_part<TX, TY>(a, rank) : (int)a.cols, G = a.G, chunks = CH * G;
     const Group g = group_of<MULTI>(G, parts);
     // one group of a block where the row has several
@@ -939,7 +939,6 @@ static Plan make_plan(int64_t rows, int64_t cols, int chunks, bool small = false
     if (p.multi) {
         p.G = (need + 32 * p.chunks - 1) / (32 * p.chunks) * 32;
         groups = NM_BLOCK / p.G;
-        if (groups > NM_MAX_GROUPS) groups = NM_MAX_GROUPS;
     } else {
         p.G = 2;  // at least two lanes: a checkpoint block's halves
         while (p.G * p.chunks < need) p.G *= 2;
