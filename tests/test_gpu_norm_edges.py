@@ -122,3 +122,32 @@ def test_host_threads_at_different_widths():
         t.join()
     assert len(refused) == len(threads) and not any(refused.values()), refused
     assert not wrong
+
+
+def test_mirrors_of_the_entry_points():
+    """The one-to-one mirrors of the C entry points give what the wrappers give."""
+    rows, cols = 9, 100
+    x, dy = torch.randn((rows, cols), device=DEV).to(BF16), torch.randn((rows, cols), device=DEV).to(BF16)
+    w = torch.ones(cols, dtype=BF16, device=DEV)
+    codes = lambda parts, n: (torch.empty((rows, parts * n), dtype=torch.uint8, device=DEV),  # noqa: E731
+                              torch.empty((rows, parts * n // 32), dtype=torch.uint8, device=DEV))
+    f = fp8.norm_forward(x, w, checkpoint_fmt=0)
+    (q, s), y, rstd = codes(1, 128), torch.empty_like(x), torch.empty_like(f.rstd)
+    fp8.fp8_norm_forward(x, 0, cols, rows, cols, fp8.LAYER_NORM, 1e-5, w, None, 0, y, 0, cols, None, rstd, 0, q, 128,
+                         s, 4)
+    assert torch.equal(y, f.y) and torch.equal(rstd, f.rstd)
+    assert torch.equal(q, f.checkpoint.q) and torch.equal(s, f.checkpoint.s)
+    c = fp8.checkpoint(x, parts=2)
+    q, s = codes(2, 64)
+    fp8.fp8_checkpoint(x, 0, rows, 50, cols, 2, 0, q, 128, s, 4)
+    assert torch.equal(q, c.q) and torch.equal(s, c.s)
+    back = torch.empty_like(x)
+    fp8.fp8_checkpoint_restore(q, 128, s, 4, 0, rows, 50, 2, back, 0, cols)
+    assert torch.equal(back, fp8.checkpoint_restore(c))
+    h, c = fp8.swiglu_checkpoint(x)
+    h2, d = torch.empty_like(h), torch.empty_like(x)
+    fp8.fp8_swiglu_checkpoint(x, rows, 50, cols, 0, h2, 50, q, 128, s, 4)
+    assert torch.equal(h2, h) and torch.equal(q, c.q) and torch.equal(s, c.s)
+    fp8.fp8_swiglu_backward(h, 50, None, 0, q, 128, s, 4, 0, rows, 50, d, cols)
+    assert torch.equal(d, fp8.swiglu_backward(h, c))
+    assert fp8.fp8_checkpoint(x, 0, rows, 0, cols, 2, 0, q, 128, s, 4, check=False) == 1   # FP8_ERR_INVALID_ARG
