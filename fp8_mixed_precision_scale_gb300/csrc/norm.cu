@@ -899,8 +899,14 @@ static int clusters_at_once(int ranks)
     if (ranks == 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return most;
     int n = known[dev][ranks].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    constexpr auto kernel = norm_backward_kernel<__nv_bfloat16, __nv_bfloat16, true, false, false, true>;
-    constexpr int shared = backward_shared_most<__nv_bfloat16, __nv_bfloat16, false, false>(true);
+    constexpr auto kernel = norm_backward_kernel<float, __nv_bfloat16, true, false, false, true>;
+    constexpr int shared = backward_shared_most<float, __nv_bfloat16, false, false>(true);
+    static_assert(shared >= backward_shared_most<float, float, false, false>(true) &&
+                      shared >= backward_shared_most<__nv_bfloat16, __nv_bfloat16, false, false>(true) &&
+                      shared >= backward_shared_most<float, __nv_bfloat16, true, false>(true) &&
+                      shared >= backward_shared_most<float, float, true, false>(true) &&
+                      shared >= forward_shared_most(true),
+                  "the largest launch");
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)ranks;
