@@ -575,7 +575,9 @@ FP8GB_API fp8_status_t fp8_checkpoint_restore(const uint8_t *q, int64_t ld_q, co
  *
  * fp32 arithmetic with the fast exponential, one rounding each (h within one
  * bf16 ulp); a gate below about -87, -Inf included, gives zeros (what that
- * leaves out is under 2^-119 of |dh|, |dh up| or |up|).
+ * leaves out is under 2^-119 of |dh|, |dh up| or |up|).  The h inside
+ * fp8_swiglu_quantize and fp8_mx_swiglu_quantize does without that exception
+ * and need not have the same bits.
  */
 FP8GB_API fp8_status_t fp8_swiglu_checkpoint(const void *gate_up_bf16, int64_t rows, int64_t F, int64_t ld, int fmt,
                                              void *h_bf16, int64_t ld_h, uint8_t *q, int64_t ld_q, uint8_t *s,

@@ -1,12 +1,13 @@
 """GPU tests of the norm, SwiGLU and checkpoint operators where callers and
 values leave the usual: the default stream by its handle, rows past the last one,
-the largest values of a type, host threads side by side."""
+the largest values of a type, gates far below zero, host threads side by side."""
 import threading
 
 import pytest
 import torch
 
 import fp8_mixed_precision_scale_gb300 as fp8
+import norm_ref as ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -151,3 +152,36 @@ def test_mirrors_of_the_entry_points():
     fp8.fp8_swiglu_backward(h, 50, None, 0, q, 128, s, 4, 0, rows, 50, d, cols)
     assert torch.equal(d, fp8.swiglu_backward(h, c))
     assert fp8.fp8_checkpoint(x, 0, rows, 0, cols, 2, 0, q, 128, s, 4, check=False) == 1   # FP8_ERR_INVALID_ARG
+
+
+def test_swiglu_far_gates():
+    """h and the gradients of gates from -150 to 150, relative to themselves.
+
+    Bound: __expf is documented to 2 + 1.173 |x| ulp, 105 of them (2^-16.3) where
+    the gate is held at -88; with the reciprocal and the products' roundings sigma
+    and silu are within 2^-16, and the slope sigma (1 + gate (1 - sigma)), whose two
+    terms keep more than 86 / 88 of their sum's size there, within 2^-15.  bf16
+    outputs add half an ulp (2^-8).  The slope crosses zero at -1.28, where both
+    terms are about 0.22 and off by under 2^-20 of that each: gates within 8 of zero
+    are allowed 2^-20 |dh up| besides.  What gates under -87 leave out is under
+    2^-119 of |up|, |dh| or |dh up| (and fp32's own subnormals)."""
+    g = torch.cat([torch.linspace(-150, 150, 2047), torch.tensor([-float("inf")])]).to(BF16)
+    n = g.numel()
+    gu = torch.stack([torch.cat([g, torch.full_like(g, v)]) for v in (1.0, -3.0, 1e4)]).to(DEV)
+    dh = torch.full((3, n), 0.5, dtype=BF16, device=DEV)
+    h, _ = fp8.swiglu_checkpoint(gu)
+    d, again = fp8.swiglu_backward(dh, gu, return_h=True)
+    assert torch.equal(h, again)
+    x, dd = ref.f64(gu), ref.f64(dh)
+    gate, up = x[:, :n].clip(-1e4), x[:, n:]   # e^-1e4 is 0 in float64 too: what the formulas tend to at -Inf
+    dg, du = ref.swiglu_backward(gate, up, dd)
+    want = ref.swiglu(gate, up)
+    lost = lambda scale: 2.0 ** -119 * abs(scale) + 2.0 ** -133  # noqa: E731
+    rel = 2.0 ** -8 + 2.0 ** -15
+    ref.assert_within(ref.f64(h), want, rel * abs(want) + lost(up), "h")
+    ref.assert_within(ref.f64(d)[:, n:], du, rel * abs(du) + lost(dd), "d up")
+    ref.assert_within(ref.f64(d)[:, :n], dg,
+                      rel * abs(dg) + lost(dd * up) + (abs(gate) < 8) * 2.0 ** -20 * abs(dd * up),
+                      "d gate")
+    for out in (h, d[:, :n], d[:, n:]):
+        assert int(out[:, g < -88].count_nonzero()) == 0
