@@ -673,18 +673,18 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
-def _here(t: torch.Tensor, where: str, name: str):
-    """Refuse a tensor of another device than the current one, on which the call
+def _elsewhere(t: torch.Tensor, where: str, name: str):
+    """A tensor of another device than the current one, on which the call
     launches: a kernel cannot count on reaching its memory."""
-    if t.get_device() != torch._C._cuda_getDevice():
-        _refuse(where, f"{name} is on cuda:{t.get_device()}, the current device is {torch._C._cuda_getDevice()}")
+    _refuse(where, f"{name} is on cuda:{t.get_device()}, the current device is {torch._C._cuda_getDevice()}")
 
 
 def _matrix(t: torch.Tensor, where: str, name: str, rows=None, cols=None, dtype=None) -> int:
     """Check a CUDA matrix; returns its row stride."""
     if not t.is_cuda or t.dim() != 2:
         _refuse(where, f"{name} must be a CUDA matrix")
-    _here(t, where, name)
+    if t.get_device() != torch._C._cuda_getDevice():
+        _elsewhere(t, where, name)
     if t.dtype not in DTYPES if dtype is None else t.dtype != dtype:
         _refuse(where, f"{name} has type {t.dtype}")
     n, c = t.shape
@@ -699,7 +699,8 @@ def _matrix(t: torch.Tensor, where: str, name: str, rows=None, cols=None, dtype=
 def _vector(t, where: str, name: str, n: int, dtype=None):
     if not t.is_cuda or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         _refuse(where, f"{name} must be a contiguous CUDA vector of {n} elements")
-    _here(t, where, name)
+    if t.get_device() != torch._C._cuda_getDevice():
+        _elsewhere(t, where, name)
     if t.dtype not in DTYPES if dtype is None else t.dtype != dtype:
         _refuse(where, f"{name} has type {t.dtype}")
 
