@@ -3,7 +3,7 @@
 // SwiGLU backward that reads it.  The block rule is ckpt.cuh's.
 //
 // All four are one pass over their tensors and bounded by HBM: at [8192, 14336]
-// store 51.6, restore 52.8, SwiGLU forward with checkpoint 140 and backward from
+// store 51.7, restore 53.0, SwiGLU forward with checkpoint 139 and backward from
 // it 143 us, 6.6 to 6.9 TB/s.
 //
 // A thread works on 16 consecutive columns, half a block: the bf16 side is one

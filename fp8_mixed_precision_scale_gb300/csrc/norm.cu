@@ -291,9 +291,11 @@ __device__ __forceinline__ float sum16(const float (&f)[16])
 // A row in the registers of its group: thread t of G holds columns (k G + t) 16
 // .. + 15 for k < CH.  Two chunks a thread halve what a row sum costs per element
 // and leave room for the next row.  Bound by HBM for large fp32 rows ([32768,
-// 7168] fp32 to bf16 203 us, 6.95 TB/s); bf16 rows are close to issue bound, 12
-// instructions an element ([32768, 4096] 89.7 us, 6.0 TB/s; with the checkpoint
-// [32768, 7168] 197 us, 6.0 TB/s).
+// 7168] fp32 to bf16 203 us, 6.95 TB/s).  bf16 rows are bound by latency: with 14 to
+// 16 warps an SM, half of the issue slots are used (12 instructions an element, 16
+// with the checkpoint) and the rest goes to waits for dependent instructions,
+// shuffles and the group's barrier ([32768, 4096] 88.6 us, 6.1 TB/s; with the
+// checkpoint [32768, 7168] 196 us, 6.0 TB/s).
 template <typename TX, typename TY, int CH, bool MULTI, bool ANY, bool CLUSTER>
 __global__ void __launch_bounds__(NM_BLOCK, CH == 1 && !ANY ? 2 : 1) norm_forward_kernel(NormArgs a)
 {
@@ -547,10 +549,13 @@ __device__ __forceinline__ void cp_async_wait()
 // added over the block's groups in shared memory (in group order) into the
 // block's slice of the workspace.  One chunk a thread, since the accumulators
 // and two rows fill its 128 registers: whatever spills is waited for, and each
-// spill that went was worth 3 to 10 %.  From x bound by HBM ([32768, 4096] 124
-// us, 6.5 TB/s; [32768, 7168], one group an SM, 224 us, 6.3 TB/s); from the
-// checkpoint by issue, about 18 instructions an element ([32768, 7168] 216 us,
-// 5.5 TB/s).
+// spill that went was worth 3 to 10 %.  Aligned bf16 rows have none (8 bytes in a
+// cluster, from the checkpoint).  Forms with an fp16 dy spill up to 56 bytes, and
+// fp16 rows take 1.2 to 1.5 times as long ([32768, 7168] 302 us from x, 322 from the
+// checkpoint).  From x bound by HBM ([32768, 4096] 124 us, 6.5 TB/s; [32768, 7168],
+// one group an SM, 222 us, 6.4 TB/s).  From the checkpoint bound by latency, as the
+// forward is: 18 instructions an element in half of the issue slots ([32768, 7168]
+// 215 us, 5.5 TB/s).
 template <typename TX, typename TY, bool MULTI, bool CKPT, bool ANY, bool CLUSTER>
 __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
 {
@@ -888,7 +893,7 @@ static bool allow_shared()
 // Blocks (of one to an SM) that run at once in clusters of `ranks`, in
 // clusters.  The SMs of a GPC are no multiple of 4 or 8, so it is fewer than the
 // SMs would give: a grid for all SMs leaves clusters for a second wave ([2048,
-// 20480] backward: 137 us with 38 clusters, 80 with those that fit).  Asked once
+// 20480] backward: 137 us with 38 clusters, 82 with those that fit).  Asked once
 // per device, with the largest launch a cluster makes.
 static int clusters_at_once(int ranks)
 {
