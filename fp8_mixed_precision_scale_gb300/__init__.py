@@ -19,6 +19,10 @@ The C ABI (include/fp8gb.h) is mirrored one to one:
   fp8_swiglu_checkpoint    SwiGLU that stores gate|up in 8 bits
   fp8_swiglu_backward      its backward, from gate|up or from the checkpoint
   fp8_checkpoint[_restore] any activation to 8 bits and back
+  fp8[_mx]_norm_quantize   residual add, norm and quantize in one read
+  fp8_residual_norm_backward  fp8_norm_backward plus the gradient past the norm
+  fp8[_mx]_swiglu_gemm     gate|up product with the SwiGLU in its epilogue
+  fp8[_mx]_swiglu_gemm_backward  dh product with its backward in the epilogue
 
 `quantize`, `scaled_gemm`, `grouped_gemm` are convenience wrappers that
 allocate the outputs with torch and call the entry points above.
@@ -51,7 +55,9 @@ EXPORTED = ("fp8_quantize", "fp8_update_amax_history", "fp8_scaled_gemm", "fp8_g
             "fp8_mx_grouped_gemm", "fp8_mx_permute_quantize", "fp8_mx_swiglu_quantize", "fp8_blockwise_quantize",
             "fp8_quantize_rowwise_resident", "fp8_permute_quantize", "fp8_swiglu_quantize", "fp8_checkpoint",
             "fp8_checkpoint_restore", "fp8_swiglu_checkpoint", "fp8_swiglu_backward", "fp8_norm_forward",
-            "fp8_norm_workspace_bytes", "fp8_norm_backward")
+            "fp8_norm_workspace_bytes", "fp8_norm_backward", "fp8_norm_quantize", "fp8_mx_norm_quantize",
+            "fp8_residual_norm_backward", "fp8_swiglu_gemm", "fp8_mx_swiglu_gemm", "fp8_swiglu_gemm_backward",
+            "fp8_mx_swiglu_gemm_backward")
 MX_BLOCK = 32
 MX_GROUP_ALIGN = 128
 
@@ -162,6 +168,27 @@ def load_library():
             lib.fp8_norm_backward.restype = i32
             lib.fp8_norm_backward.argtypes = [P, i32, i64, P, i64, P, i64, P, i64, i32, i64, i64, i32, P, P, P, i32, P,
                                               i32, i64, P, P, P, i64, P]
+            lib.fp8_norm_quantize.restype = i32
+            lib.fp8_norm_quantize.argtypes = [P, i32, i64, P, i32, i64, i64, i64, i32, f32, P, P, i32, P, i64, P, P,
+                                              i32, ctypes.POINTER(fp8_recipe_t), i32, P, P, P, P, P, i64, P, P]
+            lib.fp8_mx_norm_quantize.restype = i32
+            lib.fp8_mx_norm_quantize.argtypes = [P, i32, i64, P, i32, i64, i64, i64, i32, f32, P, P, i32, P, i64, P,
+                                                 P, i32, i32, P, P, P, i64, P, P]
+            lib.fp8_residual_norm_backward.restype = i32
+            lib.fp8_residual_norm_backward.argtypes = [P, i32, i64, P, i64, P, i64, P, i64, i32, P, i64, i64, i64,
+                                                       i32, P, P, P, i32, P, i32, i64, P, P, P, i64, P]
+            lib.fp8_swiglu_gemm.restype = i32
+            lib.fp8_swiglu_gemm.argtypes = [P, i32, i64, P, i32, i64, i64, i64, i64, P, i32, P, i32, i32, i32, P, P,
+                                            P, P, i64, P, P, i64, P, i64, i32, P, i64, P, i64, P]
+            lib.fp8_mx_swiglu_gemm.restype = i32
+            lib.fp8_mx_swiglu_gemm.argtypes = [P, i32, i64, P, P, i32, i64, P, i64, i64, i64, i32, i32, P, P, P, i64,
+                                               P, P, i64, P, i64, i32, P, i64, P, i64, P]
+            lib.fp8_swiglu_gemm_backward.restype = i32
+            lib.fp8_swiglu_gemm_backward.argtypes = [P, i32, i64, P, i32, i64, i64, i64, i64, P, i32, P, i32, P, i64,
+                                                     P, i64, P, i64, i32, i32, i32, P, P, P, P, i64, P, P, i64, P]
+            lib.fp8_mx_swiglu_gemm_backward.restype = i32
+            lib.fp8_mx_swiglu_gemm_backward.argtypes = [P, i32, i64, P, P, i32, i64, P, i64, i64, i64, P, i64, P,
+                                                        i64, P, i64, i32, i32, i32, P, P, P, i64, P, P, i64, P]
             lib.fp8_mx_gemm.restype = i32
             lib.fp8_mx_gemm.argtypes = [P, i32, i64, P, P, i32, i64, P, i64, i64, i64, P, i64, P]
             lib.fp8_mx_grouped_gemm.restype = i32
@@ -385,6 +412,90 @@ def fp8_norm_backward(dy, y_dtype, ld_dy, x, ld_x, q, ld_q, s, ld_s, fmt, rows, 
                                           _p(dweight), _p(dbias), _p(workspace), workspace_bytes, _stream(stream))
     if check:
         _check(rc, "fp8_norm_backward")
+    return rc
+
+
+def fp8_norm_quantize(x, x_dtype, ld_x, residual, r_dtype, ld_r, rows, cols, kind, eps, weight, bias, w_dtype, sum,
+                      ld_sum, mean, rstd, fmt, recipe: Recipe, layouts, scale_in, amax_out, q_row, scale_inv_row,
+                      q_colT, ld_colT, scale_inv_col, stream=None, check=True):
+    rc = load_library().fp8_norm_quantize(_p(x), x_dtype, ld_x, _p(residual), r_dtype, ld_r, rows, cols, kind, eps,
+                                          _p(weight), _p(bias), w_dtype, _p(sum), ld_sum, _p(mean), _p(rstd), fmt,
+                                          ctypes.byref(recipe.c()), layouts, _p(scale_in), _p(amax_out), _p(q_row),
+                                          _p(scale_inv_row), _p(q_colT), ld_colT, _p(scale_inv_col), _stream(stream))
+    if check:
+        _check(rc, "fp8_norm_quantize")
+    return rc
+
+
+def fp8_mx_norm_quantize(x, x_dtype, ld_x, residual, r_dtype, ld_r, rows, cols, kind, eps, weight, bias, w_dtype, sum,
+                         ld_sum, mean, rstd, fmt, layouts, q_row, s_row, q_colT, ld_colT, s_col, stream=None,
+                         check=True):
+    rc = load_library().fp8_mx_norm_quantize(_p(x), x_dtype, ld_x, _p(residual), r_dtype, ld_r, rows, cols, kind, eps,
+                                             _p(weight), _p(bias), w_dtype, _p(sum), ld_sum, _p(mean), _p(rstd), fmt,
+                                             layouts, _p(q_row), _p(s_row), _p(q_colT), ld_colT, _p(s_col),
+                                             _stream(stream))
+    if check:
+        _check(rc, "fp8_mx_norm_quantize")
+    return rc
+
+
+def fp8_residual_norm_backward(dy, y_dtype, ld_dy, x, ld_x, q, ld_q, s, ld_s, fmt, dsum, ld_dsum, rows, cols, kind,
+                               mean, rstd, weight, w_dtype, dx, x_dtype, ld_dx, dweight, dbias, workspace,
+                               workspace_bytes, stream=None, check=True):
+    rc = load_library().fp8_residual_norm_backward(_p(dy), y_dtype, ld_dy, _p(x), ld_x, _p(q), ld_q, _p(s), ld_s, fmt,
+                                                   _p(dsum), ld_dsum, rows, cols, kind, _p(mean), _p(rstd),
+                                                   _p(weight), w_dtype, _p(dx), x_dtype, ld_dx, _p(dweight),
+                                                   _p(dbias), _p(workspace), workspace_bytes, _stream(stream))
+    if check:
+        _check(rc, "fp8_residual_norm_backward")
+    return rc
+
+
+def fp8_swiglu_gemm(A, fa, lda, W, fw, ldw, M, F, K, sa, sa_mode, sw, sw_mode, fmt=0, layouts=0, scale_in=None,
+                    amax_out=None, q_row=None, q_colT=None, ld_colT=0, scale_inv=None, h=None, ld_h=0, gate_up=None,
+                    ld_gu=0, ckpt_fmt=0, q=None, ld_q=0, s=None, ld_s=0, stream=None, check=True):
+    rc = load_library().fp8_swiglu_gemm(_p(A), fa, lda, _p(W), fw, ldw, M, F, K, _p(sa), sa_mode, _p(sw), sw_mode,
+                                        fmt, layouts, _p(scale_in), _p(amax_out), _p(q_row), _p(q_colT), ld_colT,
+                                        _p(scale_inv), _p(h), ld_h, _p(gate_up), ld_gu, ckpt_fmt, _p(q), ld_q, _p(s),
+                                        ld_s, _stream(stream))
+    if check:
+        _check(rc, "fp8_swiglu_gemm")
+    return rc
+
+
+def fp8_mx_swiglu_gemm(A, fa, lda, sA, W, fw, ldw, sW, M, F, K, fmt=0, layouts=0, q_row=None, s_row=None, q_colT=None,
+                       ld_colT=0, s_col=None, h=None, ld_h=0, gate_up=None, ld_gu=0, ckpt_fmt=0, q=None, ld_q=0,
+                       s=None, ld_s=0, stream=None, check=True):
+    rc = load_library().fp8_mx_swiglu_gemm(_p(A), fa, lda, _p(sA), _p(W), fw, ldw, _p(sW), M, F, K, fmt, layouts,
+                                           _p(q_row), _p(s_row), _p(q_colT), ld_colT, _p(s_col), _p(h), ld_h,
+                                           _p(gate_up), ld_gu, ckpt_fmt, _p(q), ld_q, _p(s), ld_s, _stream(stream))
+    if check:
+        _check(rc, "fp8_mx_swiglu_gemm")
+    return rc
+
+
+def fp8_swiglu_gemm_backward(A, fa, lda, B, fb, ldb, M, F, K, sa, sa_mode, sb, sb_mode, gate_up=None, ld_gu=0, q=None,
+                             ld_q=0, s=None, ld_s=0, ckpt_fmt=0, fmt=0, layouts=0, scale_in=None, amax_out=None,
+                             q_row=None, q_colT=None, ld_colT=0, scale_inv=None, d_gate_up=None, ld_d=0, stream=None,
+                             check=True):
+    rc = load_library().fp8_swiglu_gemm_backward(_p(A), fa, lda, _p(B), fb, ldb, M, F, K, _p(sa), sa_mode, _p(sb),
+                                                 sb_mode, _p(gate_up), ld_gu, _p(q), ld_q, _p(s), ld_s, ckpt_fmt, fmt,
+                                                 layouts, _p(scale_in), _p(amax_out), _p(q_row), _p(q_colT), ld_colT,
+                                                 _p(scale_inv), _p(d_gate_up), ld_d, _stream(stream))
+    if check:
+        _check(rc, "fp8_swiglu_gemm_backward")
+    return rc
+
+
+def fp8_mx_swiglu_gemm_backward(A, fa, lda, sA, B, fb, ldb, sB, M, F, K, gate_up=None, ld_gu=0, q=None, ld_q=0,
+                                s=None, ld_s=0, ckpt_fmt=0, fmt=0, layouts=0, q_row=None, s_row=None, q_colT=None,
+                                ld_colT=0, s_col=None, d_gate_up=None, ld_d=0, stream=None, check=True):
+    rc = load_library().fp8_mx_swiglu_gemm_backward(_p(A), fa, lda, _p(sA), _p(B), fb, ldb, _p(sB), M, F, K,
+                                                    _p(gate_up), ld_gu, _p(q), ld_q, _p(s), ld_s, ckpt_fmt, fmt,
+                                                    layouts, _p(q_row), _p(s_row), _p(q_colT), ld_colT, _p(s_col),
+                                                    _p(d_gate_up), ld_d, _stream(stream))
+    if check:
+        _check(rc, "fp8_mx_swiglu_gemm_backward")
     return rc
 
 
@@ -888,15 +999,16 @@ def norm_forward(x: torch.Tensor, weight=None, bias=None, kind: int = LAYER_NORM
 
 
 def norm_backward(dy: torch.Tensor, src, mean, rstd: torch.Tensor, weight=None, kind: int = LAYER_NORM, dx_dtype=None,
-                  weight_grad: bool = True, bias_grad=None, out=None, stream=None) -> NormBackward:
-    """Backward of norm_forward from src: the forward's x, or the checkpoint
+                  weight_grad: bool = True, bias_grad=None, out=None, stream=None, dsum=None) -> NormBackward:
+    """Backward of norm_forward and the norm of norm_quantize from src: the forward's x, or the checkpoint
     it made (mean is then not read and may be None).  dweight and dbias have
     the weight's type (fp32 without a weight); bias_grad defaults to whether
     the norm is a layer norm.  dx has x's type; from a checkpoint, dx_dtype,
-    by default dy's type."""
+    by default dy's type.  dsum (of dx's type) is the gradient that reaches x
+    past the norm and is added to dx before its rounding."""
     if stream is not None:
         with _on(stream):
-            return norm_backward(dy, src, mean, rstd, weight, kind, dx_dtype, weight_grad, bias_grad, out)
+            return norm_backward(dy, src, mean, rstd, weight, kind, dx_dtype, weight_grad, bias_grad, out, dsum=dsum)
     where = "norm_backward"
     ld_dy = _matrix(dy, where, "dy")
     rows, cols = dy.shape
@@ -935,8 +1047,302 @@ def norm_backward(dy: torch.Tensor, src, mean, rstd: torch.Tensor, weight=None, 
         n = load_library().fp8_norm_workspace_bytes(rows, cols)
         if n > 0:  # -1: a shape that the call refuses
             ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    _check(load_library().fp8_norm_backward(dy.data_ptr(), DTYPES[dy.dtype], ld_dy, _ptr(x), ld_x, _ptr(q), ld_q,
-                                            _ptr(s), ld_s, fmt, rows, cols, kind, _ptr(mean), rstd.data_ptr(),
-                                            _ptr(weight), DTYPES[w_dtype], out.data_ptr(), DTYPES[dx_dtype], ld_dx,
-                                            _ptr(dw), _ptr(db), _ptr(ws), n, _stream(None)), where)
+    if dsum is None:
+        _check(load_library().fp8_norm_backward(dy.data_ptr(), DTYPES[dy.dtype], ld_dy, _ptr(x), ld_x, _ptr(q), ld_q,
+                                                _ptr(s), ld_s, fmt, rows, cols, kind, _ptr(mean), rstd.data_ptr(),
+                                                _ptr(weight), DTYPES[w_dtype], out.data_ptr(), DTYPES[dx_dtype],
+                                                ld_dx, _ptr(dw), _ptr(db), _ptr(ws), n, _stream(None)), where)
+    else:
+        ld_dsum = _matrix(dsum, where, "dsum", rows, cols, dx_dtype)
+        _check(load_library().fp8_residual_norm_backward(
+            dy.data_ptr(), DTYPES[dy.dtype], ld_dy, _ptr(x), ld_x, _ptr(q), ld_q, _ptr(s), ld_s, fmt, dsum.data_ptr(),
+            ld_dsum, rows, cols, kind, _ptr(mean), rstd.data_ptr(), _ptr(weight), DTYPES[w_dtype], out.data_ptr(),
+            DTYPES[dx_dtype], ld_dx, _ptr(dw), _ptr(db), _ptr(ws), n, _stream(None)), where)
     return NormBackward(out, dw, db)
+
+
+# --- joined with the quantizes and products around them -------------------------
+
+@dataclass
+class NormQuantize:
+    q: Quantized | MxQuantized       # the norm's result in 8 bits
+    sum: torch.Tensor                # x + residual as stored (x without a residual): norm_backward's src
+    mean: torch.Tensor | None        # fp32 [rows]; None for RMS_NORM
+    rstd: torch.Tensor               # fp32 [rows]
+
+
+def _u8(rows, cols, dev):
+    """u8 [rows, cols], never a zero-byte (null) allocation."""
+    return torch.empty(max(16, rows * cols), dtype=torch.uint8, device=dev)[:rows * cols].view(rows, cols)
+
+
+def _scaled_outputs(rows, cols, dev, layouts, per_row) -> Quantized:
+    ld_colT = max(16, (rows + 15) // 16 * 16)
+    q = Quantized(None, None, None, None, ld_colT)
+    scale = torch.empty(max(rows, 1) if per_row else 1, dtype=torch.float32, device=dev)
+    if layouts & LAYOUT_ROW:
+        q.q_row, q.scale_inv_row = _u8(rows, cols, dev), scale[:rows] if per_row else scale
+    if layouts & LAYOUT_COLT:
+        q.q_colT, q.scale_inv_col = _u8(cols, ld_colT, dev), scale
+    return q
+
+
+def _mx_split_outputs(rows, row_cols, col_rows, dev, layouts) -> MxQuantized:
+    """MX outputs whose row layout may be wider than the transposed one is tall."""
+    ld_colT = max(16, (rows + 15) // 16 * 16)
+    q = MxQuantized(None, None, None, None, ld_colT, rows)
+    if layouts & LAYOUT_ROW:
+        q.q_row = _u8(rows, row_cols, dev)
+        q.s_row = torch.empty(max(16, fp8_mx_scale_bytes(rows, row_cols // MX_BLOCK)), dtype=torch.uint8, device=dev)
+    if layouts & LAYOUT_COLT:
+        q.q_colT = _u8(col_rows, ld_colT, dev)
+        q.s_col = torch.empty(max(16, fp8_mx_scale_bytes(col_rows, rows // MX_BLOCK)), dtype=torch.uint8, device=dev)
+    return q
+
+
+def _norm_inputs(x, residual, weight, bias, kind, out, where):
+    """Checks of norm_quantize and mx_norm_quantize: what the C call wants of
+    them, and the tensors it writes besides the 8 bits."""
+    ld_x = _matrix(x, where, "x")
+    rows, cols = x.shape
+    dev = x.device
+    w_dtype = 0
+    if weight is not None:
+        _vector(weight, where, "weight", cols)
+        w_dtype = DTYPES[weight.dtype]
+    if bias is not None:
+        _vector(bias, where, "bias", cols, None if weight is None else weight.dtype)
+        w_dtype = DTYPES[bias.dtype]
+    ld_r = ld_sum = r_dtype = 0
+    if residual is not None:
+        ld_r = _matrix(residual, where, "residual", rows, cols)
+        r_dtype = DTYPES[residual.dtype]
+        if out is None:
+            out, ld_sum = torch.empty((rows, cols), dtype=residual.dtype, device=dev), cols
+        else:
+            ld_sum = _matrix(out, where, "out", rows, cols, residual.dtype)
+    elif out is not None:
+        _refuse(where, "out receives x + residual: there is no residual")
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if kind == LAYER_NORM else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    front = (x.data_ptr(), DTYPES[x.dtype], ld_x, _ptr(residual), r_dtype, ld_r, rows, cols)
+    params = (_ptr(weight), _ptr(bias), w_dtype, _ptr(out), ld_sum, _ptr(mean), rstd.data_ptr())
+    return front, params, out, mean, rstd
+
+
+def norm_quantize(x: torch.Tensor, residual=None, weight=None, bias=None, kind: int = LAYER_NORM, eps: float = 1e-5,
+                  fmt: int = E4M3FN, recipe: Recipe | None = None, layouts: int = LAYOUT_ROW, scale_in=None,
+                  amax_out=None, out=None, stream=None) -> NormQuantize:
+    """sum = x + residual (stored, in the residual's type: x's or fp32), its layer
+    or RMS norm, and that in 8 bits, in one read.  recipe: ROWWISE (the default;
+    one scale per row, row layout) or DELAYED (scale_in, amax_out; either layout)."""
+    if stream is not None:
+        with _on(stream):
+            return norm_quantize(x, residual, weight, bias, kind, eps, fmt, recipe, layouts, scale_in, amax_out, out)
+    where = "norm_quantize"
+    recipe = recipe or Recipe(kind=ROWWISE)
+    front, params, total, mean, rstd = _norm_inputs(x, residual, weight, bias, kind, out, where)
+    for t, name in ((scale_in, "scale_in"), (amax_out, "amax_out")):
+        if t is not None:
+            _vector(t, where, name, 1, torch.float32)
+    rows, cols = x.shape
+    q = _scaled_outputs(rows, cols, x.device, layouts, recipe.kind == ROWWISE)
+    _check(load_library().fp8_norm_quantize(*front, kind, eps, *params, fmt, ctypes.byref(recipe.c()), layouts,
+                                            _ptr(scale_in), _ptr(amax_out), _ptr(q.q_row), _ptr(q.scale_inv_row),
+                                            _ptr(q.q_colT), q.ld_colT, _ptr(q.scale_inv_col), _stream(None)), where)
+    return NormQuantize(q, x if residual is None else total, mean, rstd)
+
+
+def mx_norm_quantize(x: torch.Tensor, residual=None, weight=None, bias=None, kind: int = LAYER_NORM,
+                     eps: float = 1e-5, fmt: int = E4M3FN, layouts: int = LAYOUT_ROW | LAYOUT_COLT, out=None,
+                     stream=None) -> NormQuantize:
+    """norm_quantize with MX block scales (mx_quantize's layouts and limits)."""
+    if stream is not None:
+        with _on(stream):
+            return mx_norm_quantize(x, residual, weight, bias, kind, eps, fmt, layouts, out)
+    where = "mx_norm_quantize"
+    front, params, total, mean, rstd = _norm_inputs(x, residual, weight, bias, kind, out, where)
+    rows, cols = x.shape
+    q = _mx_split_outputs(rows, cols, cols, x.device, layouts)
+    _check(load_library().fp8_mx_norm_quantize(*front, kind, eps, *params, fmt, layouts, _ptr(q.q_row), _ptr(q.s_row),
+                                               _ptr(q.q_colT), q.ld_colT, _ptr(q.s_col), _stream(None)), where)
+    return NormQuantize(q, x if residual is None else total, mean, rstd)
+
+
+@dataclass
+class SwigluGemm:
+    q: Quantized | MxQuantized | None  # h in 8 bits
+    h: torch.Tensor | None             # bf16 [M, F]
+    gate_up: torch.Tensor | None       # bf16 [M, 2F]
+    checkpoint: Checkpoint | None      # of gate|up
+
+
+@dataclass
+class SwigluGemmBackward:
+    q: Quantized | MxQuantized | None  # d_gate | d_up in 8 bits
+    d_gate_up: torch.Tensor | None     # bf16 [M, 2F]
+
+
+def _codes(t: torch.Tensor, where: str, name: str, K: int) -> int:
+    """Check an FP8 operand of at least K columns; returns its row stride."""
+    ld = _matrix(t, where, name, dtype=torch.uint8)
+    if t.shape[1] < K:
+        _refuse(where, f"{name} has {t.shape[1]} columns, not {K}")
+    return ld if ld % 16 == 0 or t.shape[0] > 1 else (ld + 15) // 16 * 16
+
+
+def _scale(t: torch.Tensor, where: str, name: str, n: int) -> int:
+    _vector(t, where, name, n if t.numel() > 1 else 1, torch.float32)
+    return SCALE_PER_ROW if t.numel() > 1 else SCALE_TENSOR
+
+
+def _mx_scales(t: torch.Tensor, where: str, name: str, rows: int, K: int):
+    """MX scales must be as many as the operand's products read."""
+    _vector(t, where, name, t.numel(), torch.uint8)
+    need = fp8_mx_scale_bytes(rows, (K + MX_BLOCK - 1) // MX_BLOCK)
+    if t.numel() < need:
+        _refuse(where, f"{name} holds {t.numel()} bytes, {need} are needed")
+
+
+def _groups_of(F: int) -> int:
+    """Rows of a half in the MX layouts of gate|up: padded to whole groups."""
+    return (F + MX_GROUP_ALIGN - 1) // MX_GROUP_ALIGN * MX_GROUP_ALIGN
+
+
+def _kept(src, M, F, where):
+    """gate|up for the backward as the C call takes it."""
+    if isinstance(src, Checkpoint):
+        ld_q, ld_s = _checkpoint_strides(src, where, M, F, 2)
+        return None, 0, src.q.data_ptr(), ld_q, src.s.data_ptr(), ld_s, src.fmt
+    return src.data_ptr(), _matrix(src, where, "gate_up", M, 2 * F, torch.bfloat16), None, 0, None, 0, 0
+
+
+def _swiglu_gemm_outputs(M, F, dev, h, gate_up, checkpoint_fmt):
+    h = torch.empty((M, F), dtype=torch.bfloat16, device=dev) if h else None
+    gate_up = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev) if gate_up else None
+    c = None if checkpoint_fmt is None else _new_checkpoint(M, F, 2, dev, checkpoint_fmt)
+    nb = 2 * _blocks(F)
+    return h, gate_up, c, (_ptr(h), F, _ptr(gate_up), 2 * F, checkpoint_fmt or 0, _ptr(c and c.q), nb * MX_BLOCK,
+                           _ptr(c and c.s), nb)
+
+
+def swiglu_gemm(A: torch.Tensor, fa: int, W: torch.Tensor, fw: int, sa: torch.Tensor, sw: torch.Tensor, K=None,
+                fmt=None, layouts: int = LAYOUT_ROW | LAYOUT_COLT, scale_in=None, amax_out=None, h: bool = False,
+                gate_up: bool = False, checkpoint_fmt=None, stream=None) -> SwigluGemm:
+    """h = silu(gate) * up with gate | up = A[:, :K] . W[:, :K]^T, W u8 [2F, K]
+    the gate's rows, then the up's; sa / sw of size 1 are per-tensor, else per
+    row.  Leaves what is asked for: h in 8 bits (fmt given: the delayed recipe,
+    scale_in and amax_out), h in bf16, gate|up in bf16 or as a checkpoint."""
+    if stream is not None:
+        with _on(stream):
+            return swiglu_gemm(A, fa, W, fw, sa, sw, K, fmt, layouts, scale_in, amax_out, h, gate_up, checkpoint_fmt)
+    where = "swiglu_gemm"
+    M, K = A.shape[0], A.shape[1] if K is None else K
+    lda, ldw = _codes(A, where, "A", K), _codes(W, where, "W", K)
+    if W.shape[0] % 2:
+        _refuse(where, "W must have an even number of rows")
+    F, dev = W.shape[0] // 2, A.device
+    modes = _scale(sa, where, "sa", M), _scale(sw, where, "sw", 2 * F)
+    q, quant = _delayed_outputs(M, F, F, dev, fmt, layouts, scale_in, amax_out, where)
+    h, gate_up, c, rest = _swiglu_gemm_outputs(M, F, dev, h, gate_up, checkpoint_fmt)
+    _check(load_library().fp8_swiglu_gemm(A.data_ptr(), fa, lda, W.data_ptr(), fw, ldw, M, F, K, sa.data_ptr(),
+                                          modes[0], sw.data_ptr(), modes[1], *quant, *rest, _stream(None)), where)
+    return SwigluGemm(q, h, gate_up, c)
+
+
+def _delayed_outputs(M, row_cols, col_rows, dev, fmt, layouts, scale_in, amax_out, where):
+    """The delayed recipe's 8-bit outputs, and the C call's arguments for them."""
+    if fmt is None:
+        return None, (0, 0, None, None, None, None, 0, None)
+    for t, name in ((scale_in, "scale_in"), (amax_out, "amax_out")):
+        if t is None:
+            _refuse(where, f"8-bit results need {name}")
+        _vector(t, where, name, 1, torch.float32)
+    q = Quantized(None, None, None, None, max(16, (M + 15) // 16 * 16))
+    scale = torch.empty(1, dtype=torch.float32, device=dev)
+    if layouts & LAYOUT_ROW:
+        q.q_row, q.scale_inv_row = _u8(M, row_cols, dev), scale
+    if layouts & LAYOUT_COLT:
+        q.q_colT, q.scale_inv_col = _u8(col_rows, q.ld_colT, dev), scale
+    return q, (fmt, layouts, scale_in.data_ptr(), amax_out.data_ptr(), _ptr(q.q_row), _ptr(q.q_colT), q.ld_colT,
+               scale.data_ptr())
+
+
+def mx_swiglu_gemm(A: torch.Tensor, fa: int, sA: torch.Tensor, W: torch.Tensor, fw: int, sW: torch.Tensor, K=None,
+                   fmt=None, layouts: int = LAYOUT_ROW | LAYOUT_COLT, h: bool = False, gate_up: bool = False,
+                   checkpoint_fmt=None, stream=None) -> SwigluGemm:
+    """swiglu_gemm on MX operands; fmt: h in 8 bits with MX scales.  W quantized
+    as two groups of F rows (host_offsets [0, F, 2 F]), which for F % 128 == 0 is
+    what a plain mx_quantize gives."""
+    if stream is not None:
+        with _on(stream):
+            return mx_swiglu_gemm(A, fa, sA, W, fw, sW, K, fmt, layouts, h, gate_up, checkpoint_fmt)
+    where = "mx_swiglu_gemm"
+    M, K = A.shape[0], A.shape[1] if K is None else K
+    lda, ldw = _codes(A, where, "A", K), _codes(W, where, "W", K)
+    if W.shape[0] % 2:
+        _refuse(where, "W must have an even number of rows")
+    F, dev = W.shape[0] // 2, A.device
+    _mx_scales(sA, where, "sA", M, K)
+    _mx_scales(sW, where, "sW", 2 * _groups_of(F), K)
+    q, quant = _mx_gemm_outputs(M, F, F, dev, fmt, layouts)
+    h, gate_up, c, rest = _swiglu_gemm_outputs(M, F, dev, h, gate_up, checkpoint_fmt)
+    _check(load_library().fp8_mx_swiglu_gemm(A.data_ptr(), fa, lda, sA.data_ptr(), W.data_ptr(), fw, ldw,
+                                             sW.data_ptr(), M, F, K, *quant, *rest, _stream(None)), where)
+    return SwigluGemm(q, h, gate_up, c)
+
+
+def _mx_gemm_outputs(M, row_cols, col_rows, dev, fmt, layouts):
+    if fmt is None:
+        return None, (0, 0, None, None, None, 0, None)
+    q = _mx_split_outputs(M, row_cols, col_rows, dev, layouts)
+    return q, (fmt, layouts, _ptr(q.q_row), _ptr(q.s_row), _ptr(q.q_colT), q.ld_colT, _ptr(q.s_col))
+
+
+def swiglu_gemm_backward(A: torch.Tensor, fa: int, B: torch.Tensor, fb: int, sa: torch.Tensor, sb: torch.Tensor, src,
+                         K=None, fmt=None, layouts: int = LAYOUT_ROW | LAYOUT_COLT, scale_in=None, amax_out=None,
+                         d_gate_up: bool = False, stream=None) -> SwigluGemmBackward:
+    """Gradient of gate|up from dh = A[:, :K] . B[:, :K]^T (A the output gradient's
+    row layout, B u8 [F, K] the down weight's transposed layout) and src: bf16
+    gate|up or its checkpoint.  Leaves it in 8 bits (fmt given: the delayed
+    recipe) and / or in bf16."""
+    if stream is not None:
+        with _on(stream):
+            return swiglu_gemm_backward(A, fa, B, fb, sa, sb, src, K, fmt, layouts, scale_in, amax_out, d_gate_up)
+    where = "swiglu_gemm_backward"
+    M, K = A.shape[0], A.shape[1] if K is None else K
+    lda, ldb = _codes(A, where, "A", K), _codes(B, where, "B", K)
+    F, dev = B.shape[0], A.device
+    modes = _scale(sa, where, "sa", M), _scale(sb, where, "sb", F)
+    kept = _kept(src, M, F, where)
+    q, quant = _delayed_outputs(M, 2 * F, 2 * F, dev, fmt, layouts, scale_in, amax_out, where)
+    d = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev) if d_gate_up else None
+    _check(load_library().fp8_swiglu_gemm_backward(A.data_ptr(), fa, lda, B.data_ptr(), fb, ldb, M, F, K,
+                                                   sa.data_ptr(), modes[0], sb.data_ptr(), modes[1], *kept, *quant,
+                                                   _ptr(d), 2 * F, _stream(None)), where)
+    return SwigluGemmBackward(q, d)
+
+
+def mx_swiglu_gemm_backward(A: torch.Tensor, fa: int, sA: torch.Tensor, B: torch.Tensor, fb: int, sB: torch.Tensor,
+                            src, K=None, fmt=None, layouts: int = LAYOUT_ROW | LAYOUT_COLT, d_gate_up: bool = False,
+                            stream=None) -> SwigluGemmBackward:
+    """swiglu_gemm_backward on MX operands.  The row layout's halves are padded to
+    whole groups of 128 columns, as the columns of W quantized in two groups are
+    (its transposed layout is the other operand of the input's gradient); the
+    transposed layout's rows are the 2 F of W."""
+    if stream is not None:
+        with _on(stream):
+            return mx_swiglu_gemm_backward(A, fa, sA, B, fb, sB, src, K, fmt, layouts, d_gate_up)
+    where = "mx_swiglu_gemm_backward"
+    M, K = A.shape[0], A.shape[1] if K is None else K
+    lda, ldb = _codes(A, where, "A", K), _codes(B, where, "B", K)
+    F, dev = B.shape[0], A.device
+    _mx_scales(sA, where, "sA", M, K)
+    _mx_scales(sB, where, "sB", F, K)
+    kept = _kept(src, M, F, where)
+    q, quant = _mx_gemm_outputs(M, 2 * _groups_of(F), 2 * F, dev, fmt, layouts)
+    d = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev) if d_gate_up else None
+    _check(load_library().fp8_mx_swiglu_gemm_backward(A.data_ptr(), fa, lda, sA.data_ptr(), B.data_ptr(), fb, ldb,
+                                                      sB.data_ptr(), M, F, K, *kept, *quant, _ptr(d), 2 * F,
+                                                      _stream(None)), where)
+    return SwigluGemmBackward(q, d)

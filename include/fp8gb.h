@@ -22,7 +22,12 @@
  * layers: layer / RMS norm forward and backward (fp8_norm_forward,
  * fp8_norm_backward), the SwiGLU forward and backward
  * (fp8_swiglu_checkpoint, fp8_swiglu_backward) and 8-bit checkpoints of what
- * their backward needs (fp8_checkpoint, fp8_checkpoint_restore).
+ * their backward needs (fp8_checkpoint, fp8_checkpoint_restore).  Joined with
+ * the quantizes and products around them: the residual's addition with the norm
+ * and its quantize (fp8_norm_quantize, fp8_mx_norm_quantize; backward
+ * fp8_residual_norm_backward), and the gate|up product with the SwiGLU in its
+ * epilogue (fp8_swiglu_gemm, fp8_mx_swiglu_gemm; backward
+ * fp8_swiglu_gemm_backward, fp8_mx_swiglu_gemm_backward).
  *
  * Method sources (page title, section):
  *   - "FP8 training for Flux models" (AMD Primus guide), Configuration >
@@ -628,6 +633,147 @@ FP8GB_API fp8_status_t fp8_norm_backward(const void *dy, int y_dtype, int64_t ld
                                          const void *weight, int w_dtype, void *dx, int x_dtype, int64_t ld_dx,
                                          void *dweight, void *dbias, void *workspace, int64_t workspace_bytes,
                                          void *stream);
+
+/* ------------------------------------------------------------------------
+ * The same layers joined with the quantizes and products around them, so that
+ * neither the normalized rows, nor gate|up, nor the gradient of h is written in
+ * 16 bits only to be read back and quantized.  These entry points are this
+ * library's own too.  Results in 8 bits are rounded once, from fp32.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * fp8_norm_quantize, fp8_mx_norm_quantize -- sum = x + residual, rounded to the
+ * residual's type and stored; the norm of fp8_norm_forward of that stored sum
+ * (of x without a residual), y = xh w + b in fp32; y in 8 bits.
+ *   x              bf16, f16 or f32 [rows][ld_x], any alignment and stride.
+ *   residual       NULL, or [rows][ld_r] of x's type or f32
+ *                  (FP8_ERR_UNSUPPORTED otherwise); sum [rows][ld_sum] of the
+ *                  residual's type, required with it and NULL without.
+ *   weight, bias, w_dtype, kind, eps   as for fp8_norm_forward.
+ *   mean, rstd     fp32 [rows], each optional; FP8_LAYOUT_COLT requires rstd,
+ *                  and for FP8_NORM_LAYER mean.
+ *   fmt            FP8_E4M3FN or FP8_E5M2 (FP8_ERR_UNSUPPORTED for fnuz).
+ *   layouts        FP8_LAYOUT_ROW | FP8_LAYOUT_COLT (at least one); the other
+ *                  layout's pointers are not looked at.
+ *   rows == 0 returns FP8_OK without touching any buffer.
+ *
+ * fp8_norm_quantize: cols % 16 == 0; q_row [rows][cols] and q_colT
+ *   [cols][ld_colT] (ld_colT >= rows, % 16 == 0; bytes past rows untouched),
+ *   16-byte aligned.  Recipe kinds:
+ *   FP8_RECIPE_ROWWISE  row layout only (FP8_ERR_UNSUPPORTED with COLT: column
+ *                  scales need all rows of y first), scale_inv_row [rows];
+ *                  margin, scales and a non-finite amax as in fp8_quantize;
+ *                  scale_in and amax_out NULL.
+ *   FP8_RECIPE_DELAYED  scale_in [1] for both layouts, amax_out [1] receives
+ *                  max(amax_out, amax(y)); scale_inv_row / _col [1] = 1 /
+ *                  scale_in.
+ *   FP8_RECIPE_TENSORWISE is FP8_ERR_UNSUPPORTED.
+ * fp8_mx_norm_quantize: cols % 32 == 0, for COLT rows % 32 == 0; q_row, s_row,
+ *   q_colT, s_col as fp8_mx_quantize writes them (ungrouped).
+ */
+FP8GB_API fp8_status_t fp8_norm_quantize(const void *x, int x_dtype, int64_t ld_x, const void *residual, int r_dtype,
+                                         int64_t ld_r, int64_t rows, int64_t cols, int kind, float eps,
+                                         const void *weight, const void *bias, int w_dtype, void *sum,
+                                         int64_t ld_sum, float *mean, float *rstd, int fmt,
+                                         const fp8_recipe_t *recipe, int layouts, const float *scale_in,
+                                         float *amax_out, uint8_t *q_row, float *scale_inv_row, uint8_t *q_colT,
+                                         int64_t ld_colT, float *scale_inv_col, void *stream);
+
+FP8GB_API fp8_status_t fp8_mx_norm_quantize(const void *x, int x_dtype, int64_t ld_x, const void *residual,
+                                            int r_dtype, int64_t ld_r, int64_t rows, int64_t cols, int kind,
+                                            float eps, const void *weight, const void *bias, int w_dtype, void *sum,
+                                            int64_t ld_sum, float *mean, float *rstd, int fmt, int layouts,
+                                            uint8_t *q_row, uint8_t *s_row, uint8_t *q_colT, int64_t ld_colT,
+                                            uint8_t *s_col, void *stream);
+
+/*
+ * fp8_residual_norm_backward -- fp8_norm_backward with dx = the norm's own
+ * gradient + dsum, one rounding for both.  dsum [rows][ld_dsum] of x_dtype is the
+ * gradient that reaches the norm's input past the norm (of the stored sum, for a
+ * block whose residual goes on from it); everything else as there.  The quantize's
+ * rounding passes gradients through as they are.
+ */
+FP8GB_API fp8_status_t fp8_residual_norm_backward(const void *dy, int y_dtype, int64_t ld_dy, const void *x,
+                                                  int64_t ld_x, const uint8_t *q, int64_t ld_q, const uint8_t *s,
+                                                  int64_t ld_s, int fmt, const void *dsum, int64_t ld_dsum,
+                                                  int64_t rows, int64_t cols, int kind, const float *mean,
+                                                  const float *rstd, const void *weight, int w_dtype, void *dx,
+                                                  int x_dtype, int64_t ld_dx, void *dweight, void *dbias,
+                                                  void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * fp8_swiglu_gemm, fp8_mx_swiglu_gemm -- gate = A W_gate^T, up = A W_up^T,
+ * h = silu(gate) up from the fp32 accumulators, in one kernel.
+ *   A          u8 [M][lda], format fa, row layout of the block's input.
+ *   W          u8 [2F][ldw], format fw: the gate's F rows, then the up's.
+ *   Operands, scales, alignments and formats as fp8_scaled_gemm (sw: [1] or
+ *   [2F]; F % 16 == 0, K % 16 == 0) and fp8_mx_gemm (F % 32 == 0, K % 32 == 0).
+ *   MX: sW has the scale rows of W quantized as two groups of F rows (padded to
+ *   FP8_MX_GROUP_ALIGN: up's first is roundup(F, 128)); with F % 128 == 0 those
+ *   of a plain fp8_mx_quantize.
+ *   M >= 0; M == 0 returns FP8_OK without touching any buffer.
+ *   Outputs, at least one:
+ *   layouts    0, or FP8_LAYOUT_ROW | FP8_LAYOUT_COLT: h in 8 bits of format fmt,
+ *              q_row [M][F], q_colT [F][ld_colT] (ld_colT >= M, % 16 == 0; bytes
+ *              past M untouched), 16-byte aligned; pointers of a layout that is
+ *              not asked for are not looked at.  MX: s_row, s_col as
+ *              fp8_mx_quantize writes them, M % 32 == 0 for COLT.  Else the
+ *              delayed recipe: scale_in [1], amax_out [1] receives max(amax_out,
+ *              amax(h)), scale_inv [1] = 1 / scale_in.
+ *   h_bf16     NULL or [M][ld_h]: bf16(h).  16-byte aligned, ld_h % 8 == 0.
+ *   gate_up_bf16  NULL or [M][ld_gu]: gate, then up from column F on (ld_gu >=
+ *              2F, % 8 == 0, 16-byte aligned).
+ *   q, s       NULL, or the 2-part checkpoint of gate|up of format ckpt_fmt, as
+ *              fp8_checkpoint writes it (of the fp32 values).
+ *
+ * fp8_swiglu_gemm_backward, fp8_mx_swiglu_gemm_backward -- dh = A B^T, and
+ * d_gate, d_up of fp8_swiglu_backward from the fp32 dh, in one kernel.
+ *   A          u8 [M][lda]: row layout of the block's output gradient.
+ *   B          u8 [F][ldb]: transposed layout of the down projection's weight.
+ *   sb: [1] or [F].  gate|up: gate_up_bf16, or with that NULL the checkpoint q, s
+ *   of format ckpt_fmt.
+ *   layouts    d_gate | d_up in 8 bits.  q_row: [M][2F], up from column F on;
+ *              MX: [M][2 roundup(F, 128)], up from column roundup(F, 128) on and
+ *              zeros between, which is the order of the columns of W quantized in
+ *              two groups (s_row: KB = 2 roundup(F, 128) / 32).  q_colT
+ *              [2F][ld_colT], s_col R = 2F.
+ *   d_gate_up_bf16  NULL or [M][ld_d], up from column F on.
+ *
+ * SwiGLU's fp32 arithmetic is that of fp8_swiglu_checkpoint and
+ * fp8_swiglu_backward (a gate below about -87 gives zeros), with one rounding of
+ * each result.  NaN and Inf follow IEEE arithmetic and the quantizes' rules.
+ */
+FP8GB_API fp8_status_t fp8_swiglu_gemm(const uint8_t *A, int fa, int64_t lda, const uint8_t *W, int fw, int64_t ldw,
+                                       int64_t M, int64_t F, int64_t K, const float *sa, int sa_mode,
+                                       const float *sw, int sw_mode, int fmt, int layouts, const float *scale_in,
+                                       float *amax_out, uint8_t *q_row, uint8_t *q_colT, int64_t ld_colT,
+                                       float *scale_inv, void *h_bf16, int64_t ld_h, void *gate_up_bf16,
+                                       int64_t ld_gu, int ckpt_fmt, uint8_t *q, int64_t ld_q, uint8_t *s,
+                                       int64_t ld_s, void *stream);
+
+FP8GB_API fp8_status_t fp8_mx_swiglu_gemm(const uint8_t *A, int fa, int64_t lda, const uint8_t *sA, const uint8_t *W,
+                                          int fw, int64_t ldw, const uint8_t *sW, int64_t M, int64_t F, int64_t K,
+                                          int fmt, int layouts, uint8_t *q_row, uint8_t *s_row, uint8_t *q_colT,
+                                          int64_t ld_colT, uint8_t *s_col, void *h_bf16, int64_t ld_h,
+                                          void *gate_up_bf16, int64_t ld_gu, int ckpt_fmt, uint8_t *q, int64_t ld_q,
+                                          uint8_t *s, int64_t ld_s, void *stream);
+
+FP8GB_API fp8_status_t fp8_swiglu_gemm_backward(const uint8_t *A, int fa, int64_t lda, const uint8_t *B, int fb,
+                                                int64_t ldb, int64_t M, int64_t F, int64_t K, const float *sa,
+                                                int sa_mode, const float *sb, int sb_mode, const void *gate_up_bf16,
+                                                int64_t ld_gu, const uint8_t *q, int64_t ld_q, const uint8_t *s,
+                                                int64_t ld_s, int ckpt_fmt, int fmt, int layouts,
+                                                const float *scale_in, float *amax_out, uint8_t *q_row,
+                                                uint8_t *q_colT, int64_t ld_colT, float *scale_inv,
+                                                void *d_gate_up_bf16, int64_t ld_d, void *stream);
+
+FP8GB_API fp8_status_t fp8_mx_swiglu_gemm_backward(const uint8_t *A, int fa, int64_t lda, const uint8_t *sA,
+                                                   const uint8_t *B, int fb, int64_t ldb, const uint8_t *sB,
+                                                   int64_t M, int64_t F, int64_t K, const void *gate_up_bf16,
+                                                   int64_t ld_gu, const uint8_t *q, int64_t ld_q, const uint8_t *s,
+                                                   int64_t ld_s, int ckpt_fmt, int fmt, int layouts, uint8_t *q_row,
+                                                   uint8_t *s_row, uint8_t *q_colT, int64_t ld_colT, uint8_t *s_col,
+                                                   void *d_gate_up_bf16, int64_t ld_d, void *stream);
 
 /* Synchronise `stream`, then report and clear a device-side timeout word:
  * FP8_OK, FP8_ERR_TIMEOUT, or FP8_ERR_CUDA. */
