@@ -1073,7 +1073,15 @@ class NormQuantize:
 
 def _u8(rows, cols, dev):
     """u8 [rows, cols], never a zero-byte (null) allocation."""
-    return torch.empty(max(16, rows * cols), dtype=torch.uint8, device=dev)[:rows * cols].view(rows, cols)
+    if rows:
+        return torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+    return torch.empty(16, dtype=torch.uint8, device=dev)[:0].view(0, cols)
+
+
+def _mx_scale_buffer(rows, blocks, dev):
+    """Buffer of fp8_mx_scale_bytes(rows, blocks) bytes (computed here: a call into the library costs microseconds)."""
+    n = (blocks + 3) // 4 * 4 * ((rows + 127) // 128 * 128)
+    return torch.empty(n or 16, dtype=torch.uint8, device=dev)
 
 
 def _scaled_outputs(rows, cols, dev, layouts, per_row) -> Quantized:
@@ -1093,10 +1101,10 @@ def _mx_split_outputs(rows, row_cols, col_rows, dev, layouts) -> MxQuantized:
     q = MxQuantized(None, None, None, None, ld_colT, rows)
     if layouts & LAYOUT_ROW:
         q.q_row = _u8(rows, row_cols, dev)
-        q.s_row = torch.empty(max(16, fp8_mx_scale_bytes(rows, row_cols // MX_BLOCK)), dtype=torch.uint8, device=dev)
+        q.s_row = _mx_scale_buffer(rows, row_cols // MX_BLOCK, dev)
     if layouts & LAYOUT_COLT:
         q.q_colT = _u8(col_rows, ld_colT, dev)
-        q.s_col = torch.empty(max(16, fp8_mx_scale_bytes(col_rows, rows // MX_BLOCK)), dtype=torch.uint8, device=dev)
+        q.s_col = _mx_scale_buffer(col_rows, rows // MX_BLOCK, dev)
     return q
 
 
@@ -1199,7 +1207,7 @@ def _scale(t: torch.Tensor, where: str, name: str, n: int) -> int:
 def _mx_scales(t: torch.Tensor, where: str, name: str, rows: int, K: int):
     """MX scales must be as many as the operand's products read."""
     _vector(t, where, name, t.numel(), torch.uint8)
-    need = fp8_mx_scale_bytes(rows, (K + MX_BLOCK - 1) // MX_BLOCK)
+    need = (K + 127) // 128 * 4 * ((rows + 127) // 128 * 128)
     if t.numel() < need:
         _refuse(where, f"{name} holds {t.numel()} bytes, {need} are needed")
 

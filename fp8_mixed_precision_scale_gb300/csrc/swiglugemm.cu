@@ -48,11 +48,10 @@
 namespace fp8gb {
 namespace sg {
 
-constexpr int BM = 128;
-constexpr int BB = 128;  // rows of one of a stage's two B tiles
+constexpr int BM = 128;  // rows of A a CTA stages, and of the result that it holds
+constexpr int BB = 128;  // rows of one box of B
 constexpr int BK = 128;
 constexpr int UMMA_K = 32;
-constexpr int STAGES = 4;
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_FIRST = 4;  // their first warp: a warpgroup of its own for the registers
 constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
@@ -60,12 +59,10 @@ constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
 constexpr int REGS = 168, REGS_OTHER = 56, REGS_EPI = 224;
 static_assert(128 * REGS_OTHER + 32 * EPI_WARPS * REGS_EPI <= THREADS * REGS, "registers");
 constexpr int A_BYTES = BM * BK;
-constexpr int B_BYTES = 2 * BB * BK;
 constexpr int SF_BLOCK = 512;  // scale words of 128 rows in one K tile
 constexpr uint32_t TMEM_COLS = 512;
 // MX: one accumulator at column 0, per stage 4 columns of A's scales and 8 of B's
 constexpr uint32_t SFA_COL = 256, SFB_COL = 288;
-static_assert(SFA_COL + 4 * STAGES <= SFB_COL && SFB_COL + 8 * STAGES <= TMEM_COLS, "scale columns");
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 
 // Staging of a warp: 32 rows x 16 columns of fp32, rows 20 words apart and the
@@ -74,29 +71,33 @@ constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr int STAGE_WORDS = 31 * 20 + 16 + 16;
 __device__ __forceinline__ int stage_word(int row) { return row * 20 + (row & 16); }
 
+template <bool PAIR>
 struct Smem {
+    static constexpr int stages = PAIR ? 6 : 4;
+    static constexpr int boxes = PAIR ? 1 : 2;  // of B a CTA stages
+    static constexpr int b_bytes = boxes * BB * BK;
     static constexpr int a_off = 0;
-    static constexpr int b_off = STAGES * A_BYTES;
-    static constexpr int sfa_off = b_off + STAGES * B_BYTES;
-    static constexpr int sfb_off = sfa_off + STAGES * SF_BLOCK;
-    static constexpr int bar_off = sfb_off + STAGES * 2 * SF_BLOCK;
-    static constexpr int n_bars = 3 * STAGES + 2 + 2 + 2;
+    static constexpr int b_off = stages * A_BYTES;
+    static constexpr int sfa_off = b_off + stages * b_bytes;
+    static constexpr int sfb_off = sfa_off + stages * SF_BLOCK;
+    static constexpr int bar_off = sfb_off + stages * 2 * SF_BLOCK;
+    static constexpr int n_bars = 3 * stages + 2 + 2 + 2;
     static constexpr int slot_off = bar_off + n_bars * 8;
     static constexpr int stage_off = (slot_off + 16 + 127) / 128 * 128;
-    static constexpr int total = stage_off + EPI_WARPS * STAGE_WORDS * 4;
+    static constexpr int bytes = 1024 + stage_off + EPI_WARPS * STAGE_WORDS * 4;
+    static_assert(SFA_COL + 4 * stages <= SFB_COL && SFB_COL + 8 * stages <= TMEM_COLS, "scale columns");
+    static_assert(bytes + 1024 <= 227 * 1024, "smem");
 };
-constexpr int SMEM_BYTES = 1024 + Smem::total;
-static_assert(SMEM_BYTES + 1024 <= 227 * 1024, "smem");
+
+enum { FORWARD = 0, BACKWARD_CKPT = 1, BACKWARD_BF16 = 2 };  // KIND: the backward's gate|up in 8 bits or bf16
 
 struct Params {
     int64_t M, F;       // rows; columns of h
     int64_t K;          // contraction
     const float *sa, *sb;
     int sa_row, sb_row;  // per row, else one of the tensor
-    const uint8_t *sA, *sB;
-    int64_t rsA, rsB;    // scale rows of A's and B's layouts
     int32_t b1_row;      // forward: row of B where up starts
-    int64_t b1_srow;     // ... and its scale row
+    int32_t b1_srow;     // ... and its scale row
     int num_m, num_n, num_k, m_fastest;
     int64_t tiles;
     // bf16: h (forward) or d_gate | d_up (backward), up at column F
@@ -135,7 +136,8 @@ __device__ __forceinline__ uint32_t mx_code_of(uint32_t amax_bits, int fmt)
 __device__ __forceinline__ float amax16(const float (&v)[16], float m)  // NaN if any is
 {
 #pragma unroll
-    for (int j = 0; j < 16; j++) m = max_nan(m, fabsf(v[j]));
+    for (int j = 0; j < 16; j += 2)
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(fabsf(v[j])), "f"(fabsf(v[j + 1])));
     return m;
 }
 
@@ -170,131 +172,175 @@ __device__ __forceinline__ void put_bf16(uint16_t *p, const float (&v)[2][16], i
     }
 }
 
-// 32 columns of an 8-bit result.  A thread has row `row` (of a warp's 32 from
-// row0 on; `live`: inside the matrix; values outside the data are 0).
-//   oc, n_row   first column in q_row and how many of the 32 it has (0, 16, 32)
-//   cc, n_col   first row in q_col, likewise
-// The scale bytes of rows and columns behind the data are the zeros that a
-// zero block's code is, and lie inside the 128-row blocks of the scale layout.
-// PAD: they are written for all 32 columns (where the layouts' padding is this
-// tile's alone).
-template <bool MX, bool PAD>
-__device__ __forceinline__ void put_8bit(const Params &p, const float (&v)[2][16], int64_t row, bool live,
-                                         int64_t row0, int64_t oc, int n_row, int64_t cc, int n_col, float scale,
-                                         float *stage, int lane, float &amax)
+// Where a thread of the epilogue stands in its tile.
+struct Place {
+    int64_t row, row0;  // its row, and its warp's first
+    bool live;          // the row is inside the matrix
+    int lane;
+    float *stage;       // its warp's
+};
+
+// 32 columns of a result into the row layout; values outside the data are 0.
+// oc, n: the first column in q_row, and how many of the 32 it has (0, 16, 32).
+// MX: returns the block's scale code.
+template <bool MX>
+__device__ __forceinline__ uint32_t put_row(const Params &p, const float (&v)[2][16], const Place &t, int64_t oc,
+                                            int n, float scale)
 {
-    if (!MX) amax = amax16(v[1], amax16(v[0], amax));
-    if (p.q_row && (PAD || n_row > 0)) {
-        float inv = scale;
-        if (MX) {
-            const uint32_t code = mx_code_of(__float_as_uint(amax16(v[1], amax16(v[0], 0.0f))), p.fmt);
-            p.s_row[4 * mx_scale_word(oc >> 7, row, p.rs_row) + (oc >> 5 & 3)] = (uint8_t)code;
-            inv = mx_inv_scale(code);
-        }
-        if (live)
-            put_codes(p.q_row + row * p.ld_row + oc, encode(v[0], inv, p.fmt), encode(v[1], inv, p.fmt), n_row, p.q32);
+    uint32_t code = 0;
+    float inv = scale;
+    if (MX) {
+        code = mx_code_of(__float_as_uint(amax16(v[1], amax16(v[0], 0.0f))), p.fmt);
+        inv = mx_inv_scale(code);
     }
-    if (p.q_col && (PAD || n_col > 0)) {
-        const int c = lane & 15, h = lane >> 4;
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            float4 *w = reinterpret_cast<float4 *>(stage + stage_word(lane));
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                w[j] = make_float4(v[i][4 * j], v[i][4 * j + 1], v[i][4 * j + 2], v[i][4 * j + 3]);
-            __syncwarp();
-            float t[16];
-#pragma unroll
-            for (int j = 0; j < 16; j++) t[j] = stage[stage_word(16 * h + j) + c];
-            const bool have = 16 * i + c < n_col;
-            float inv = scale;
-            if (MX) {
-                float m = amax16(t, 0.0f);
-                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                const uint32_t code = mx_code_of(__float_as_uint(m), p.fmt);
-                inv = mx_inv_scale(code);
-                if (h == 0 && (PAD || have))
-                    p.s_col[4 * mx_scale_word(row0 >> 7, cc + 16 * i + c, p.rs_col) + (row0 >> 5 & 3)] = (uint8_t)code;
-            }
-            const int64_t r = row0 + 16 * h;
-            const uint4 q = encode(t, inv, p.fmt);
-            if (have) {
-                uint8_t *dst = p.q_col + (cc + 16 * i + c) * p.ld_col + r;
-                if (r + 16 <= p.M) {
-                    *reinterpret_cast<uint4 *>(dst) = q;
-                } else if (!MX) {  // MX: whole blocks of 32 rows
-                    const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        if (r + j < p.M) dst[j] = (uint8_t)(qw[j >> 2] >> (8 * (j & 3)));
-                }
-            }
-            __syncwarp();
-        }
-    }
+    if (t.live)
+        put_codes(p.q_row + t.row * p.ld_row + oc, encode(v[0], inv, p.fmt), encode(v[1], inv, p.fmt), n, p.q32);
+    return code;
 }
 
-// 16 or 32 bf16 (n of them; zeros after) of a row.
-__device__ __forceinline__ void get_bf16(const uint16_t *p, int n, float (&v)[2][16])
+// ... and into the transposed layout: cc, n the first row in q_col and how many of
+// the 32 it has.  PAD: the scale bytes of all 32 are written, zeros (a zero
+// block's code) behind the data, where the layout's padding is this tile's alone.
+template <bool MX, bool PAD>
+__device__ __forceinline__ void put_col(const Params &p, const float (&v)[2][16], const Place &t, int64_t cc, int n,
+                                        float scale)
 {
+    const int c = t.lane & 15, h = t.lane >> 4;
+    const int64_t r = t.row0 + 16 * h;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        Raw16<__nv_bfloat16> r;
-        r.v[0] = r.v[1] = make_uint4(0, 0, 0, 0);
-        if (n > 16 * i) load16(reinterpret_cast<const __nv_bfloat16 *>(p) + 16 * i, 16, false, r);
-        unpack16(r, v[i]);
+        float4 *w = reinterpret_cast<float4 *>(t.stage + stage_word(t.lane));
+#pragma unroll
+        for (int j = 0; j < 4; j++) w[j] = make_float4(v[i][4 * j], v[i][4 * j + 1], v[i][4 * j + 2], v[i][4 * j + 3]);
+        __syncwarp();
+        float x[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) x[j] = t.stage[h * (16 * 20 + 16) + j * 20 + c];
+        const bool have = 16 * i + c < n;
+        float inv = scale;
+        if (MX) {
+            float m = amax16(x, 0.0f);
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            const uint32_t code = mx_code_of(__float_as_uint(m), p.fmt);
+            inv = mx_inv_scale(code);
+            if (h == 0 && (PAD || have))
+                p.s_col[4 * mx_scale_word(t.row0 >> 7, cc + 16 * i + c, p.rs_col) + (t.row0 >> 5 & 3)] = (uint8_t)code;
+        }
+        const uint4 q = encode(x, inv, p.fmt);
+        if (have) {
+            uint8_t *dst = p.q_col + (cc + 16 * i + c) * p.ld_col + r;
+            if (r + 16 <= p.M) {
+                *reinterpret_cast<uint4 *>(dst) = q;
+            } else if (!MX) {  // MX: whole blocks of 32 rows
+                const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll 1
+                for (int j = 0; j < 16; j++)
+                    if (r + j < p.M)
+                        dst[j] = (uint8_t)((j < 8 ? j < 4 ? qw[0] : qw[1] : j < 12 ? qw[2] : qw[3]) >> (8 * (j & 3)));
+            }
+        }
+        __syncwarp();
     }
 }
 
-// The block of 32 from a checkpoint.
-__device__ __forceinline__ void get_kept(const uint8_t *q, const uint8_t *s, bool live, int fmt, float (&v)[2][16])
+// What the backward reads of a unit of 32 columns of gate and of up.
+template <int KIND>
+struct Kept {
+    uint4 q[4];       // codes: gate's, then up's
+    uint32_t s[2];
+};
+template <>
+struct Kept<BACKWARD_BF16> {
+    uint4 q[8];
+};
+
+// n: columns that the data has from c on (0, 16, 32); zeros after, and in rows
+// outside the matrix.
+template <int KIND>
+__device__ __forceinline__ void get_kept(const Params &p, const Place &t, int64_t c, int n, Kept<KIND> &k)
 {
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    uint32_t code = 127;
-    if (live) {
-        ld_stream_32b(q, lo, hi);
-        code = __ldg(s);
-    }
-    const float x = ckpt_scale(code);
-    if (fmt == FP8_E5M2) {
-        decode16<FP8_E5M2>(lo, x, v[0]);
-        decode16<FP8_E5M2>(hi, x, v[1]);
-    } else {
-        decode16<FP8_E4M3FN>(lo, x, v[0]);
-        decode16<FP8_E4M3FN>(hi, x, v[1]);
+    constexpr int N = sizeof(k.q) / sizeof(uint4) / 2;
+    const bool have = t.live && n > 0;
+#pragma unroll
+    for (int i = 0; i < 2 * N; i++) k.q[i] = make_uint4(0, 0, 0, 0);
+    if constexpr (KIND == BACKWARD_CKPT) {
+        k.s[0] = k.s[1] = 127;
+        if (have) {
+            const uint8_t *q = p.cq + t.row * p.ld_cq + c, *s = p.cs + t.row * p.ld_cs + (c >> 5);
+            ld_stream_32b(q, k.q[0], k.q[1]);
+            ld_stream_32b(q + p.W, k.q[2], k.q[3]);
+            k.s[0] = __ldg(s);
+            k.s[1] = __ldg(s + (p.W >> 5));
+        }
+    } else if (have) {
+        const uint16_t *src = p.gate_up + t.row * p.ld_gu + c;
+#pragma unroll
+        for (int h = 0; h < 2; h++, src += p.F)
+#pragma unroll
+            for (int i = 0; i < N; i += 2)
+                if (n > 8 * i) {
+                    if (p.gu32) {
+                        ld_stream_32b(src + 8 * i, k.q[N * h + i], k.q[N * h + i + 1]);
+                    } else {
+                        k.q[N * h + i] = ld_stream_16b(src + 8 * i);
+                        k.q[N * h + i + 1] = ld_stream_16b(src + 8 * i + 8);
+                    }
+                }
     }
 }
 
-// 32 accumulator columns as fp32, with the operands' scales (`col`: of B, for
-// its row of column j of the 32 at lane j) and 0 where there is no data.
+// Half h (16 columns) of gate (w = 0) or up (w = 1).
+template <int KIND>
+__device__ __forceinline__ void kept16(const Params &p, const Kept<KIND> &k, int w, int h, float (&v)[16])
+{
+    if constexpr (KIND == BACKWARD_CKPT) {
+        const float x = ckpt_scale(k.s[w]);
+        if (p.cfmt == FP8_E5M2) decode16<FP8_E5M2>(k.q[2 * w + h], x, v);
+        else decode16<FP8_E4M3FN>(k.q[2 * w + h], x, v);
+    } else {
+        Raw16<__nv_bfloat16> r;
+        r.v[0] = k.q[4 * w + 2 * h], r.v[1] = k.q[4 * w + 2 * h + 1];
+        unpack16(r, v);
+    }
+}
+
+// 32 accumulator columns as fp32, with the operands' scales (`col`: lane j holds
+// that of column j, or all the same one).
 template <bool MX>
-__device__ __forceinline__ void from_acc(const uint32_t (&r)[32], float sa, float col, bool per_col, bool live, int n,
-                                         float (&v)[2][16])
+__device__ __forceinline__ void from_acc(const uint32_t (&r)[32], float sa, float col, bool per_col, float (&v)[2][16])
 {
 #pragma unroll
     for (int j = 0; j < 32; j++) {
         float f = __uint_as_float(r[j]);
         if (!MX) f = f * sa * (per_col ? __shfl_sync(0xffffffffu, col, j) : col);
-        v[j >> 4][j & 15] = live && j < n ? f : 0.0f;
+        v[j >> 4][j & 15] = f;
     }
 }
 
-// 32 columns of h from its gate and up (forward).
-template <bool MX>
-__device__ __forceinline__ void forward_unit(const Params &p, float (&g)[2][16], float (&u)[2][16], int64_t row,
-                                             bool live, int64_t row0, int64_t c, int n, float scale, float *stage,
-                                             int lane, float &amax)
+// Zeros where there is no data: rows outside the matrix, columns from n on.
+__device__ __forceinline__ void mask32(float (&v)[2][16], bool live, int n)
 {
-    if (p.gate_up && live) {
-        uint16_t *dst = p.gate_up + row * p.ld_gu + c;
+#pragma unroll
+    for (int j = 0; j < 32; j++) v[j >> 4][j & 15] = live && j < n ? v[j >> 4][j & 15] : 0.0f;
+}
+
+// What a unit of 32 columns of h leaves, from its gate and up (forward) or its dh
+// and kept gate | up (backward).  Returns MX: its blocks' scale codes in the row
+// layout (the backward's d_up in bits 8 to 15).
+template <bool MX>
+__device__ __forceinline__ uint32_t forward_unit(const Params &p, float (&g)[2][16], float (&u)[2][16],
+                                                 const Place &t, int64_t c, int n, float scale, float &amax)
+{
+    if (p.gate_up && t.live) {
+        uint16_t *dst = p.gate_up + t.row * p.ld_gu + c;
         put_bf16(dst, g, n, p.gu32);
         put_bf16(dst + p.F, u, n, p.gu32);
     }
-    if (p.cq && live && c < p.W) {
+    if (p.cq && t.live && c < p.W) {
         const uint32_t a = ckpt_code(__float_as_uint(amax16(g[1], amax16(g[0], 0.0f))), p.cfmt);
         const uint32_t b = ckpt_code(__float_as_uint(amax16(u[1], amax16(u[0], 0.0f))), p.cfmt);
         const float ia = ckpt_inv_scale(a), ib = ckpt_inv_scale(b);
-        uint8_t *q = p.cq + row * p.ld_cq + c, *s = p.cs + row * p.ld_cs + (c >> 5);
+        uint8_t *q = p.cq + t.row * p.ld_cq + c, *s = p.cs + t.row * p.ld_cs + (c >> 5);
         st_32b(q, encode(g[0], ia, p.cfmt), encode(g[1], ia, p.cfmt));
         st_32b(q + p.W, encode(u[0], ib, p.cfmt), encode(u[1], ib, p.cfmt));
         s[0] = (uint8_t)a;
@@ -309,64 +355,76 @@ __device__ __forceinline__ void forward_unit(const Params &p, float (&g)[2][16],
             si = mul2(si, make_float2(u[i][j], u[i][j + 1]));
             g[i][j] = si.x, g[i][j + 1] = si.y;
         }
-    if (p.out && live) put_bf16(p.out + row * p.ld_out + c, g, n, p.out32);
-    if (p.q_row || p.q_col)
-        put_8bit<MX, MX>(p, g, row, live, row0, c, n, c, n, scale, stage, lane, amax);
+    if (p.out && t.live) put_bf16(p.out + t.row * p.ld_out + c, g, n, p.out32);
+    if (!MX) amax = amax16(g[1], amax16(g[0], amax));
+    uint32_t code = 0;
+    if (p.q_row) code = put_row<MX>(p, g, t, c, n, scale);
+    if (p.q_col && (MX || n > 0)) put_col<MX, MX>(p, g, t, c, n, scale);
+    return code;
 }
 
-// 32 columns of d_gate and d_up from dh (backward).
-template <bool MX>
-__device__ __forceinline__ void backward_unit(const Params &p, float (&d)[2][16], int64_t row, bool live,
-                                              int64_t row0, int64_t c, int n, float scale, float *stage, int lane,
-                                              float &amax)
+template <bool MX, int KIND>
+__device__ __forceinline__ uint32_t backward_unit(const Params &p, float (&g)[2][16], const Kept<KIND> &kept,
+                                                  const Place &t, int64_t c, int n, float scale, float &amax)
 {
-    float g[2][16], u[2][16];
-    if (p.gate_up) {
-        const uint16_t *src = p.gate_up + row * p.ld_gu + c;
-        get_bf16(src, live ? n : 0, g);
-        get_bf16(src + p.F, live ? n : 0, u);
-    } else {
-        const uint8_t *q = p.cq + row * p.ld_cq + c, *s = p.cs + row * p.ld_cs + (c >> 5);
-        const bool have = live && n > 0;
-        get_kept(q, s, have, p.cfmt, g);
-        get_kept(q + p.W, s + (p.W >> 5), have, p.cfmt, u);
-    }
+    float u[2][16];
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < 2; i++) {
+        float kg[16], ku[16];
+        kept16(p, kept, 0, i, kg);
+        kept16(p, kept, 1, i, ku);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
             float2 dg, du, h;
-            swiglu_grad2(make_float2(g[i][j], g[i][j + 1]), make_float2(u[i][j], u[i][j + 1]),
-                         make_float2(d[i][j], d[i][j + 1]), dg, du, h);
-            // columns behind the data: what stands in the checkpoint there is not read into the result
-            const bool have = live && 16 * i + j < n;
-            g[i][j] = have ? dg.x : 0.0f, g[i][j + 1] = have ? dg.y : 0.0f;
-            u[i][j] = have ? du.x : 0.0f, u[i][j + 1] = have ? du.y : 0.0f;
+            swiglu_grad2(make_float2(kg[j], kg[j + 1]), make_float2(ku[j], ku[j + 1]),
+                         make_float2(g[i][j], g[i][j + 1]), dg, du, h);
+            g[i][j] = dg.x, g[i][j + 1] = dg.y;
+            u[i][j] = du.x, u[i][j + 1] = du.y;
         }
-    if (p.out && live) {
-        uint16_t *dst = p.out + row * p.ld_out + c;
+    }
+    // what stands in the checkpoint behind the data is not read into the result
+    if (n < 32 || t.row0 + 32 > p.M) {
+        mask32(g, t.live, n);
+        mask32(u, t.live, n);
+    }
+    if (p.out && t.live) {
+        uint16_t *dst = p.out + t.row * p.ld_out + c;
         put_bf16(dst, g, n, p.out32);
         put_bf16(dst + p.F, u, n, p.out32);
     }
-    if (p.q_row || p.q_col) {
-        const int n_row = c < p.Fr ? (MX ? 32 : n) : 0;
-        put_8bit<MX, false>(p, g, row, live, row0, c, n_row, c, n, scale, stage, lane, amax);
-        put_8bit<MX, false>(p, u, row, live, row0, p.Fr + c, n_row, p.F + c, n, scale, stage, lane, amax);
+    if (!MX) amax = amax16(u[1], amax16(u[0], amax16(g[1], amax16(g[0], amax))));
+    uint32_t codes = 0;
+    // d_gate, then d_up, through the same instructions: twice as many would not stay
+    // in the instruction cache
+#pragma unroll 1
+    for (int h = 0; h < 2; h++) {
+        if (p.q_row) {
+            const uint32_t code = put_row<MX>(p, g, t, h ? p.Fr + c : c, c < p.Fr ? (MX ? 32 : n) : 0, scale);
+            codes |= code << (8 * h);
+        }
+        if (p.q_col && n > 0) put_col<MX, false>(p, g, t, h ? p.F + c : c, n, scale);
+#pragma unroll
+        for (int j = 0; j < 32; j++) g[j >> 4][j & 15] = u[j >> 4][j & 15];
     }
+    return codes;
 }
 
-template <bool MX, bool BWD>
+template <bool MX, bool PAIR, int KIND>
 __global__ void __launch_bounds__(THREADS, 1)
     swiglu_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                        const __grid_constant__ Params p, uint32_t idesc)
 {
+    using L = Smem<PAIR>;
+    constexpr int STAGES = L::stages;
+    constexpr bool BWD = KIND != FORWARD;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sA = smem + Smem::a_off;
-    uint8_t *sB = smem + Smem::b_off;
-    uint8_t *sfa = smem + Smem::sfa_off;
-    uint8_t *sfb = smem + Smem::sfb_off;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Smem::bar_off);
+    uint8_t *sA = smem + L::a_off;
+    uint8_t *sB = smem + L::b_off;
+    uint8_t *sfa = smem + L::sfa_off;
+    uint8_t *sfb = smem + L::sfb_off;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bar_off);
     uint64_t *full = bars;
     uint64_t *empty = bars + STAGES;
     uint64_t *sf_full = bars + 2 * STAGES;  // MX: the stage's scales are in TMEM
@@ -374,9 +432,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t *tempty = tfull + 2;
     uint64_t *done = tempty + 2;
     uint64_t *sf_done = done + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Smem::slot_off);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::slot_off);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? (int)cluster_ctarank() : 0;  // the even CTA leads
+    const int64_t first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
     constexpr int ACCS = MX ? 1 : 2;
 
     if (warp == 0 && lane == 0) {
@@ -387,17 +447,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], EPI_WARPS);
+            mbar_init(&tempty[b], (PAIR ? 2 : 1) * EPI_WARPS);
         }
         mbar_init(done, 1);
         mbar_init(sf_done, 1);
         fence_barrier_init();
         prefetch_tensormap(&tmA);
         prefetch_tensormap(&tmB);
+        if (MX) {
+            prefetch_tensormap(&tmSA);
+            prefetch_tensormap(&tmSB);
+        }
     }
-    if (warp == 1) tmem_alloc(tmem_slot, TMEM_COLS);
+    if (warp == 1) {
+        if (PAIR) tmem_alloc_pair(tmem_slot, TMEM_COLS);
+        else tmem_alloc(tmem_slot, TMEM_COLS);
+    }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // both CTAs' barriers are initialised before any remote use
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
@@ -410,39 +478,52 @@ __global__ void __launch_bounds__(THREADS, 1)
             mb = (int)(tt / (uint32_t)p.num_n);
             nb = (int)(tt - (uint32_t)mb * (uint32_t)p.num_n);
         }
+        if (PAIR) mb = 2 * mb + rank;  // this CTA's 128 rows
     };
     const int last_steps = (int)((p.K - (int64_t)(p.num_k - 1) * BK + UMMA_K - 1) / UMMA_K);
 
     if (warp < EPI_FIRST) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
         if (warp == 0 && lane == 0) {
-            // ---------------- producer ----------------
+            // ---------------- producer (both CTAs) ----------------
             int stage = 0;
             uint32_t phase = 0, used = 0;
             bool ok = true;
-            for (int64_t t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+            for (int64_t t = first; t < p.tiles && ok; t += step) {
                 int mb, nb;
                 coords(t, mb, nb);
+                const int32_t y = mb * BM;
+                // first rows of the tile's two boxes of B, and of their scales
                 const int32_t b0 = nb * (BWD ? 2 * BB : BB), b1 = BWD ? b0 + BB : p.b1_row + b0;
-                const int64_t s0 = b0, s1 = BWD ? b0 + BB : p.b1_srow + b0;
-                // the last tile of an odd number of 128-row blocks has one
-                const bool two = s1 < p.rsB;
+                const int32_t s1 = BWD ? b0 + BB : p.b1_srow + b0;
                 for (int kb = 0; kb < p.num_k; kb++) {
                     if (!mbar_wait_bounded(&empty[stage], phase ^ 1, WAIT_LIMIT_NS, p.err, ERR_PRODUCER_WAIT)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&full[stage], A_BYTES + B_BYTES + (MX ? (two ? 3 : 2) * SF_BLOCK : 0));
-                    tma_load_2d(sA + stage * A_BYTES, &tmA, kb * BK, mb * BM, &full[stage]);
-                    tma_load_2d(sB + stage * B_BYTES, &tmB, kb * BK, b0, &full[stage]);
-                    tma_load_2d(sB + stage * B_BYTES + B_BYTES / 2, &tmB, kb * BK, b1, &full[stage]);
-                    if (MX) {
-                        bulk_load(sfa + stage * SF_BLOCK, p.sA + (kb * p.rsA + (int64_t)mb * BM) * 4, SF_BLOCK,
-                                  &full[stage]);
-                        bulk_load(sfb + stage * 2 * SF_BLOCK, p.sB + (kb * p.rsB + s0) * 4, SF_BLOCK, &full[stage]);
-                        if (two)
-                            bulk_load(sfb + stage * 2 * SF_BLOCK + SF_BLOCK, p.sB + (kb * p.rsB + s1) * 4, SF_BLOCK,
-                                      &full[stage]);
+                    constexpr uint32_t bytes = A_BYTES + L::b_bytes + (MX ? 3 * SF_BLOCK : 0);
+                    uint8_t *a = sA + stage * A_BYTES, *b = sB + stage * L::b_bytes;
+                    uint8_t *fa = sfa + stage * SF_BLOCK, *fb = sfb + stage * 2 * SF_BLOCK;
+                    if constexpr (PAIR) {  // both CTAs' copies count on the even one's barrier
+                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+                        const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+                        tma_load_2d_pair(a, &tmA, kb * BK, y, bar);
+                        tma_load_2d_pair(b, &tmB, kb * BK, rank ? b1 : b0, bar);
+                        if (MX) {
+                            tma_load_2d_pair(fa, &tmSA, y, kb, bar);
+                            tma_load_2d_pair(fb, &tmSB, b0, kb, bar);
+                            tma_load_2d_pair(fb + SF_BLOCK, &tmSB, s1, kb, bar);
+                        }
+                    } else {
+                        mbar_arrive_expect_tx(&full[stage], bytes);
+                        tma_load_2d(a, &tmA, kb * BK, y, &full[stage]);
+                        tma_load_2d(b, &tmB, kb * BK, b0, &full[stage]);
+                        tma_load_2d(b + BB * BK, &tmB, kb * BK, b1, &full[stage]);
+                        if (MX) {
+                            tma_load_2d(fa, &tmSA, y, kb, &full[stage]);
+                            tma_load_2d(fb, &tmSB, b0, kb, &full[stage]);
+                            tma_load_2d(fb + SF_BLOCK, &tmSB, s1, kb, &full[stage]);
+                        }
                     }
                     used |= 1u << stage;
                     if (++stage == STAGES) {
@@ -452,16 +533,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             // copies in flight land before the block ends: the last of stage s is of
-            // this round for the stages before `stage`, of the round before for the others
-            for (int s = 0; s < STAGES; s++)
-                if (used >> s & 1)
-                    mbar_wait_bounded(&full[s], s < stage ? phase : phase ^ 1, WAIT_LIMIT_NS, p.err, ERR_TEARDOWN_WAIT);
-        } else if (warp == 1 && lane == 0) {
-            // ---------------- MMA issuer ----------------
+            // this round for the stages before `stage`, of the round before for the others.
+            // The even CTA's barriers count both CTAs' (the odd one waits at the end)
+            if (rank == 0)
+                for (int s = 0; s < STAGES; s++)
+                    if (used >> s & 1)
+                        mbar_wait_bounded(&full[s], s < stage ? phase : phase ^ 1, WAIT_LIMIT_NS, p.err,
+                                          ERR_TEARDOWN_WAIT);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // ---------------- MMA issuer (even CTA) ----------------
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int64_t t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+            for (int64_t t = first; t < p.tiles && ok; t += step) {
                 if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, WAIT_LIMIT_NS, p.err, ERR_MMA_WAIT)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(acc * 2 * BB);
@@ -472,39 +556,43 @@ __global__ void __launch_bounds__(THREADS, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(sA + stage * A_BYTES), b_addr = smem_u32(sB + stage * B_BYTES);
+                    const uint32_t a_addr = smem_u32(sA + stage * A_BYTES), b_addr = smem_u32(sB + stage * L::b_bytes);
+                    const uint32_t ca = tmem_base + SFA_COL + 4 * stage, cb = tmem_base + SFB_COL + 8 * stage;
                     const int steps = kb == p.num_k - 1 ? last_steps : BK / UMMA_K;
                     for (int k = 0; k < steps; k++) {
                         const uint64_t ad = smem_desc_k128_sw128(a_addr + k * UMMA_K);
                         const uint64_t bd = smem_desc_k128_sw128(b_addr + k * UMMA_K);
-                        if (MX)
-                            mma_mxf8f6f4(d, ad, bd, idesc_sf_ids(idesc, (uint32_t)k, (uint32_t)k),
-                                         tmem_base + SFA_COL + 4 * stage, tmem_base + SFB_COL + 8 * stage,
-                                         (kb | k) != 0);
-                        else
-                            mma_f8f6f4(d, ad, bd, idesc, (kb | k) != 0);
+                        const uint32_t id = MX ? idesc_sf_ids(idesc, (uint32_t)k, (uint32_t)k) : idesc;
+                        if constexpr (MX && PAIR) mma_mxf8f6f4_pair(d, ad, bd, id, ca, cb, (kb | k) != 0);
+                        else if constexpr (MX) mma_mxf8f6f4(d, ad, bd, id, ca, cb, (kb | k) != 0);
+                        else if constexpr (PAIR) mma_f8f6f4_pair(d, ad, bd, id, (kb | k) != 0);
+                        else mma_f8f6f4(d, ad, bd, id, (kb | k) != 0);
                     }
-                    mma_commit(&empty[stage]);
+                    if (PAIR) mma_commit_pair(&empty[stage], 0x3);
+                    else mma_commit(&empty[stage]);
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
                 if (!ok) break;
-                mma_commit(&tfull[acc]);
+                if (PAIR) mma_commit_pair(&tfull[acc], 0x3);
+                else mma_commit(&tfull[acc]);
                 if (++acc == ACCS) {
                     acc = 0;
                     acc_phase ^= 1;
                 }
             }
-            mma_commit(done);  // all issued MMAs complete before TMEM is released
+            // all issued MMAs complete before TMEM is released
+            if (PAIR) mma_commit_pair_local(done);
+            else mma_commit(done);
             mbar_wait_bounded(done, 0, WAIT_LIMIT_NS, p.err, ERR_TEARDOWN_WAIT);
-        } else if (MX && warp == 2 && lane == 0) {
-            // ---------------- scale copies ----------------
+        } else if (MX && warp == 2 && lane == 0 && rank == 0) {
+            // ---------------- scale copies (even CTA) ----------------
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int64_t t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+            for (int64_t t = first; t < p.tiles && ok; t += step) {
                 for (int kb = 0; kb < p.num_k; kb++) {
                     if (!mbar_wait_bounded(&full[stage], phase, WAIT_LIMIT_NS, p.err, ERR_MMA_WAIT)) {
                         ok = false;
@@ -513,24 +601,35 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc_fence_after();
                     const uint32_t ca = tmem_base + SFA_COL + 4 * stage, cb = tmem_base + SFB_COL + 8 * stage;
                     const uint32_t ra = smem_u32(sfa + stage * SF_BLOCK), rb = smem_u32(sfb + stage * 2 * SF_BLOCK);
-                    tmem_cp_32x128b_x4(ca, smem_desc_sf(ra));
-                    tmem_cp_32x128b_x4(cb, smem_desc_sf(rb));
-                    tmem_cp_32x128b_x4(cb + 4, smem_desc_sf(rb + SF_BLOCK));
-                    mma_commit(&sf_full[stage]);
+                    if constexpr (PAIR) {
+                        tmem_cp_32x128b_x4_pair(ca, smem_desc_sf(ra));
+                        tmem_cp_32x128b_x4_pair(cb, smem_desc_sf(rb));
+                        tmem_cp_32x128b_x4_pair(cb + 4, smem_desc_sf(rb + SF_BLOCK));
+                        mma_commit_pair_local(&sf_full[stage]);
+                    } else {
+                        tmem_cp_32x128b_x4(ca, smem_desc_sf(ra));
+                        tmem_cp_32x128b_x4(cb, smem_desc_sf(rb));
+                        tmem_cp_32x128b_x4(cb + 4, smem_desc_sf(rb + SF_BLOCK));
+                        mma_commit(&sf_full[stage]);
+                    }
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
             }
-            mma_commit(sf_done);  // every issued copy lands before TMEM is released
+            // every issued copy lands before TMEM is released
+            if (PAIR) mma_commit_pair_local(sf_done);
+            else mma_commit(sf_done);
             mbar_wait_bounded(sf_done, 0, WAIT_LIMIT_NS, p.err, ERR_TEARDOWN_WAIT);
         }
     } else {
-        // ---------------- epilogue ----------------
+        // ---------------- epilogue (both CTAs) ----------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
         const int q = warp & 3, hb = (warp - EPI_FIRST) >> 2;
-        float *stage = reinterpret_cast<float *>(smem + Smem::stage_off) + (warp - EPI_FIRST) * STAGE_WORDS;
+        Place pl;
+        pl.lane = lane;
+        pl.stage = reinterpret_cast<float *>(smem + L::stage_off) + (warp - EPI_FIRST) * STAGE_WORDS;
         constexpr int UNITS = BWD ? 4 : 2;
         float scale = 1.0f, amax = 0.0f;
         if (!MX && p.scale_in) {
@@ -539,62 +638,106 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+        for (int64_t t = first; t < p.tiles; t += step) {
             int mb, nb;
             coords(t, mb, nb);
-            const int64_t row0 = (int64_t)mb * BM + q * 32, row = row0 + lane;
-            const bool live = row < p.M;
+            pl.row0 = (int64_t)mb * BM + q * 32;
+            pl.row = pl.row0 + lane;
+            pl.live = pl.row < p.M;
             const int64_t c0 = (int64_t)nb * (BWD ? 2 * BB : BB) + hb * 32 * UNITS;  // this warp's columns of h
+            const auto columns = [&](int u) {  // that the data has in unit u
+                const int64_t n = p.F - c0 - 32 * u;
+                return (int)(n < 0 ? 0 : n < 32 ? n : 32);
+            };
+            // a pair's second 128 rows may lie behind the padded rows too
+            const int units = (int64_t)mb * BM < p.rs_row ? UNITS : 0;
             float sa = 1.0f;
-            if (!MX) sa = p.sa_row ? (live ? __ldg(p.sa + row) : 0.0f) : __ldg(p.sa);
+            if (!MX) sa = p.sa_row ? (pl.live ? __ldg(p.sa + pl.row) : 0.0f) : __ldg(p.sa);
+            Kept<KIND> kept;
+            if constexpr (BWD) get_kept<KIND>(p, pl, c0, columns(0), kept);
             if (!mbar_wait_bounded(&tfull[acc], acc_phase, WAIT_LIMIT_NS, p.err, ERR_EPILOGUE_WAIT)) break;
             tc_fence_after();
-            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 2 * BB);
-            // accumulator column of unit u's first (forward: gate's; up's is 128 further)
-            const auto column = [&](int u) { return taddr + (uint32_t)(hb * 32 * UNITS + 32 * u); };
+            // accumulator column of the warp's first unit (forward: gate's; up's is 128 further)
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 2 * BB + hb * 32 * UNITS);
             const auto release = [&]() {
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty[acc]);
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+                    else mbar_arrive(&tempty[acc]);
+                }
             };
-            uint32_t r[MX ? 4 : BWD ? 1 : 2][32];
+            uint32_t r[MX ? 4 : BWD ? 1 : 2][32];  // forward: gate and up of a unit, then of the next
             if constexpr (MX) {
 #pragma unroll
-                for (int u = 0; u < 4; u++)
-                    tmem_ld_32x32b_x32(BWD ? column(u) : column(u & 1) + (u >> 1) * BB, r[u]);
+                for (int i = 0; i < 4; i++)
+                    tmem_ld_32x32b_x32(BWD ? taddr + 32 * i : taddr + 32 * (i >> 1) + (i & 1) * BB, r[i]);
                 release();
             }
-#pragma unroll
+            uint32_t codes = 0, codes_up = 0;
+            // a loop, not copies of it: four units' instructions do not stay in the instruction cache
+#pragma unroll 1
             for (int u = 0; u < UNITS; u++) {
                 const int64_t c = c0 + 32 * u;
-                const int n = (int)(p.F - c < 0 ? 0 : p.F - c < 32 ? p.F - c : 32);
+                const int n = columns(u);
                 if constexpr (!MX) {
-                    tmem_ld_32x32b_x32(column(u), r[0]);
-                    if (!BWD) tmem_ld_32x32b_x32(column(u) + BB, r[BWD ? 0 : 1]);
+                    tmem_ld_32x32b_x32(taddr + 32 * u, r[0]);
+                    if (!BWD) tmem_ld_32x32b_x32(taddr + 32 * u + BB, r[BWD ? 0 : 1]);
                     if (u == UNITS - 1) release();
                     else tmem_ld_wait();
                 }
-                float g[2][16], up[2][16];
-                float cg = 1.0f, cu = 1.0f;
-                if (!MX) {
-                    cg = cu = p.sb_row ? 0.0f : __ldg(p.sb);
-                    if (p.sb_row && lane < n) {
-                        cg = __ldg(p.sb + c + lane);
-                        if (!BWD) cu = __ldg(p.sb + p.F + c + lane);
+                if (u < units) {
+                    float cg = 1.0f, cu = 1.0f;
+                    if (!MX) {
+                        cg = cu = p.sb_row ? 0.0f : __ldg(p.sb);
+                        if (p.sb_row && lane < n) {
+                            cg = __ldg(p.sb + c + lane);
+                            if (!BWD) cu = __ldg(p.sb + p.F + c + lane);
+                        }
+                    }
+                    float v[2][16];
+                    from_acc<MX>(r[0], sa, cg, p.sb_row, v);
+                    uint32_t code;
+                    if constexpr (BWD) {
+                        const Kept<KIND> now = kept;
+                        if (u + 1 < UNITS) get_kept<KIND>(p, pl, c + 32, columns(u + 1), kept);
+                        code = backward_unit<MX, KIND>(p, v, now, pl, c, n, scale, amax);
+                    } else {
+                        float up[2][16];
+                        from_acc<MX>(r[1], sa, cu, p.sb_row, up);
+                        if (n < 32 || pl.row0 + 32 > p.M) {
+                            mask32(v, pl.live, n);
+                            mask32(up, pl.live, n);
+                        }
+                        code = forward_unit<MX>(p, v, up, pl, c, n, scale, amax);
+                    }
+                    codes |= (code & 0xFFu) << (8 * u);
+                    codes_up |= (code >> 8) << (8 * u);
+                }
+                if constexpr (MX) {  // the next unit's accumulators
+#pragma unroll
+                    for (int j = 0; j < 32; j++) {
+                        if (BWD) r[0][j] = r[1][j], r[1][j] = r[2][j], r[2][j] = r[3][j];
+                        else r[0][j] = r[2][j], r[1][j] = r[3][j];
                     }
                 }
-                from_acc<MX>(r[MX ? u : 0], sa, cg, p.sb_row, live, n, g);
+            }
+            if (MX && units && p.q_row) {
+                // the row's scale bytes of its columns: a whole word of the layout, or the forward's half
+                const int64_t w = mx_scale_word(c0 >> 7, pl.row, p.rs_row);
                 if constexpr (BWD) {
-                    backward_unit<MX>(p, g, row, live, row0, c, n, scale, stage, lane, amax);
+                    if (c0 < p.Fr) {
+                        reinterpret_cast<uint32_t *>(p.s_row)[w] = codes;
+                        reinterpret_cast<uint32_t *>(p.s_row)[w + (p.Fr >> 7) * p.rs_row] = codes_up;
+                    }
                 } else {
-                    from_acc<MX>(r[MX ? 2 + u : 1], sa, cu, p.sb_row, live, n, up);
-                    forward_unit<MX>(p, g, up, row, live, row0, c, n, scale, stage, lane, amax);
+                    reinterpret_cast<uint16_t *>(p.s_row)[2 * w + hb] = (uint16_t)codes;
                 }
             }
-            if (MX && BWD && p.q_col && hb == 0 && nb == p.num_n - 1)  // scale rows behind the data
+            if (MX && BWD && units && p.q_col && hb == 0 && nb == p.num_n - 1)  // scale rows behind the data
                 for (int64_t i = 2 * p.F + lane; i < p.rs_col; i += 32)
-                    p.s_col[4 * mx_scale_word(row0 >> 7, i, p.rs_col) + (row0 >> 5 & 3)] = 0;
+                    p.s_col[4 * mx_scale_word(pl.row0 >> 7, i, p.rs_col) + (pl.row0 >> 5 & 3)] = 0;
             if (++acc == ACCS) {
                 acc = 0;
                 acc_phase ^= 1;
@@ -608,10 +751,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // no CTA leaves while its peer may still touch its shared memory or TMEM
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem_base, TMEM_COLS);
+        if (PAIR) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        else tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
 
@@ -652,41 +797,111 @@ static bool make_map(CUtensorMap *map, const void *base, int64_t rows, int64_t c
     return r == CUDA_SUCCESS;
 }
 
-// The limit of a kernel's dynamic shared memory, set once per device.
-template <auto KERNEL>
-static bool allow_shared()
+// 2D map over MX scales [kt][rows] of words (rows: of the padded layout), box 128
+// words: one 128-row block of a K tile.
+static bool make_scale_map(CUtensorMap *map, const void *base, int64_t kt, int64_t rows)
 {
-    constexpr int MAX_DEVICES = 64;
-    static std::atomic<bool> allowed[MAX_DEVICES];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    if (dev < MAX_DEVICES && allowed[dev].load(std::memory_order_acquire)) return true;
-    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess)
-        return false;
-    if (dev < MAX_DEVICES) allowed[dev].store(true, std::memory_order_release);
-    return true;
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)rows, (cuuint64_t)kt};
+    cuuint64_t strides[1] = {(cuuint64_t)rows * 4};
+    cuuint32_t box[2] = {(cuuint32_t)BM, 1};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
 }
 
-template <bool MX, bool BWD>
-static fp8_status_t launch(const void *A, int fa, int64_t lda, const void *B, int fb, int64_t ldb, int64_t b_rows,
-                           Params p, void *stream)
+// Lets a kernel's launches take their shared memory, and gives the pairs (or
+// blocks) that run at once; asked once per device.  0: it failed.
+template <auto KERNEL, bool PAIR>
+static int at_once()
 {
-    CUtensorMap ma, mb;
-    if (!make_map(&ma, A, p.M, p.K, lda) || !make_map(&mb, B, b_rows, p.K, ldb)) return FP8_ERR_CUDA;
-    constexpr auto kernel = swiglu_gemm_kernel<MX, BWD>;
-    if (!allow_shared<kernel>()) return cuda_fail();
-    constexpr int cols = BWD ? 2 * BB : BB;  // of h in a tile
-    p.num_m = (int)((p.M + BM - 1) / BM);
+    constexpr int MAX_DEVICES = 64;
+    static std::atomic<int> known[MAX_DEVICES];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return 0;
+    int n = known[dev].load(std::memory_order_acquire);
+    if (n > 0) return n;
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<PAIR>::bytes) != cudaSuccess)
+        return 0;
+    n = num_sms();
+    if (PAIR) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(num_sms() / 2 * 2));
+        cfg.blockDim = dim3(THREADS);
+        cfg.dynamicSmemBytes = Smem<PAIR>::bytes;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = num_sms() / 2;
+        }
+    }
+    known[dev].store(n, std::memory_order_release);
+    return n;
+}
+
+// The operands of a launch; sA, sB: MX scales, of rsA and rsB rows.
+struct Operands {
+    const void *A, *B;
+    int fa, fb;
+    int64_t lda, ldb, b_rows;
+    const void *sA, *sB;
+    int64_t rsA, rsB;
+};
+
+template <bool MX, bool PAIR, int KIND>
+static fp8_status_t launch_as(const Operands &o, Params p, cudaStream_t st)
+{
+    CUtensorMap ma, mb, msa = {}, msb = {};
+    if (!make_map(&ma, o.A, p.M, p.K, o.lda) || !make_map(&mb, o.B, o.b_rows, p.K, o.ldb)) return FP8_ERR_CUDA;
+    constexpr int rows = PAIR ? 2 * BM : BM, cols = KIND == FORWARD ? BB : 2 * BB;  // of a tile of h
+    p.num_m = (int)((p.M + rows - 1) / rows);
     p.num_n = (int)((p.F + cols - 1) / cols);
     p.num_k = (int)((p.K + BK - 1) / BK);
-    p.m_fastest = p.M <= b_rows;  // the smaller operand stays in L2
+    if (MX && (!make_scale_map(&msa, o.sA, p.num_k, o.rsA) || !make_scale_map(&msb, o.sB, p.num_k, o.rsB)))
+        return FP8_ERR_CUDA;
+    p.m_fastest = p.M <= o.b_rows;  // the smaller operand stays in L2
     p.tiles = (int64_t)p.num_m * p.num_n;
     if (p.tiles > INT32_MAX) return FP8_ERR_UNSUPPORTED;
     p.err = device_error_word();
-    const uint32_t idesc = MX ? idesc_mxf8f6f4(fa, fb, BM, 2 * BB) : idesc_f8f6f4(fa, fb, BM, 2 * BB);
-    const int64_t grid = p.tiles < num_sms() ? p.tiles : num_sms();
-    kernel<<<(unsigned)grid, THREADS, SMEM_BYTES, static_cast<cudaStream_t>(stream)>>>(ma, mb, p, idesc);
+    constexpr auto kernel = swiglu_gemm_kernel<MX, PAIR, KIND>;
+    const int most = at_once<kernel, PAIR>();
+    if (!most) return cuda_fail();
+    const uint32_t idesc = MX ? idesc_mxf8f6f4(o.fa, o.fb, rows, 2 * BB) : idesc_f8f6f4(o.fa, o.fb, rows, 2 * BB);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.tiles < most ? p.tiles : most) * (PAIR ? 2 : 1)));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = Smem<PAIR>::bytes;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = PAIR;
+    cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, p, idesc);
     return check_launch();
+}
+
+// Pairs from 129 rows on, as the plain products.
+template <bool MX, int KIND>
+static fp8_status_t launch(const Operands &o, const Params &p, void *stream)
+{
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return p.M > BM ? launch_as<MX, true, KIND>(o, p, st) : launch_as<MX, false, KIND>(o, p, st);
+}
+
+template <bool MX>
+static fp8_status_t launch_backward(const Operands &o, const Params &p, void *stream)
+{
+    return p.gate_up ? launch<MX, BACKWARD_BF16>(o, p, stream) : launch<MX, BACKWARD_CKPT>(o, p, stream);
 }
 
 static fp8_status_t check_format(int f)
@@ -804,15 +1019,15 @@ static fp8_status_t set_delayed(int layouts, const float *scale_in, float *amax_
     return FP8_OK;
 }
 
-// MX operands: A's scale rows are M, B's `b_rows` (a multiple of 128).
-static fp8_status_t set_mx(const uint8_t *sA, const uint8_t *sB, int64_t b_rows, Params &p)
+// MX scales: A's have M rows, B's `b_rows` (a multiple of 128).
+static fp8_status_t set_mx(const uint8_t *sA, const uint8_t *sB, int64_t b_rows, int64_t M, Operands &o)
 {
-    if (p.M > 0 && (!sA || !sB)) return FP8_ERR_INVALID_ARG;
+    if (M > 0 && (!sA || !sB)) return FP8_ERR_INVALID_ARG;
     if (!aligned(sA, 16) || !aligned(sB, 16)) return FP8_ERR_ALIGNMENT;
-    p.sA = sA;
-    p.sB = sB;
-    p.rsA = round_up_128(p.M);
-    p.rsB = b_rows;
+    o.sA = sA;
+    o.sB = sB;
+    o.rsA = round_up_128(M);
+    o.rsB = b_rows;
     return FP8_OK;
 }
 
@@ -823,7 +1038,7 @@ static Params sizes(int64_t M, int64_t F, int64_t K)
     p.F = F;
     p.K = K;
     p.b1_row = (int32_t)F;
-    p.b1_srow = round_up_128(F);
+    p.b1_srow = (int32_t)round_up_128(F);
     return p;
 }
 
@@ -850,7 +1065,7 @@ extern "C" fp8_status_t fp8_swiglu_gemm(const uint8_t *A, int fa, int64_t lda, c
     SG_TRY(sg::set_checkpoint(q, ld_q, s, ld_s, ckpt_fmt, p));
     if (!layouts && !p.out && !p.gate_up && !p.cq && M > 0) return FP8_ERR_INVALID_ARG;
     if (M == 0) return FP8_OK;
-    return sg::launch<false, false>(A, fa, lda, W, fw, ldw, 2 * F, p, stream);
+    return sg::launch<false, sg::FORWARD>({A, W, fa, fw, lda, ldw, 2 * F}, p, stream);
 }
 
 extern "C" fp8_status_t fp8_mx_swiglu_gemm(const uint8_t *A, int fa, int64_t lda, const uint8_t *sA, const uint8_t *W,
@@ -862,14 +1077,15 @@ extern "C" fp8_status_t fp8_mx_swiglu_gemm(const uint8_t *A, int fa, int64_t lda
 {
     SG_TRY(sg::check_operands(A, fa, lda, W, fw, ldw, M, F, K, FP8_MX_BLOCK));
     sg::Params p = sg::sizes(M, F, K);
-    SG_TRY(sg::set_mx(sA, sW, 2 * round_up_128(F), p));
+    sg::Operands o{A, W, fa, fw, lda, ldw, 2 * F};
+    SG_TRY(sg::set_mx(sA, sW, 2 * round_up_128(F), M, o));
     SG_TRY(sg::set_8bit<true>(fmt, layouts, q_row, s_row, q_colT, ld_colT, s_col, 1, p));
     SG_TRY(sg::set_bf16(h_bf16, ld_h, F, 1, p.out, p.ld_out, p.out32));
     SG_TRY(sg::set_bf16(gate_up_bf16, ld_gu, F, 2, p.gate_up, p.ld_gu, p.gu32));
     SG_TRY(sg::set_checkpoint(q, ld_q, s, ld_s, ckpt_fmt, p));
     if (!layouts && !p.out && !p.gate_up && !p.cq && M > 0) return FP8_ERR_INVALID_ARG;
     if (M == 0) return FP8_OK;
-    return sg::launch<true, false>(A, fa, lda, W, fw, ldw, 2 * F, p, stream);
+    return sg::launch<true, sg::FORWARD>(o, p, stream);
 }
 
 extern "C" fp8_status_t fp8_swiglu_gemm_backward(const uint8_t *A, int fa, int64_t lda, const uint8_t *B, int fb,
@@ -892,7 +1108,7 @@ extern "C" fp8_status_t fp8_swiglu_gemm_backward(const uint8_t *A, int fa, int64
     SG_TRY(sg::set_bf16(d_gate_up_bf16, ld_d, F, 2, p.out, p.ld_out, p.out32));
     if (!layouts && !p.out && M > 0) return FP8_ERR_INVALID_ARG;
     if (M == 0) return FP8_OK;
-    return sg::launch<false, true>(A, fa, lda, B, fb, ldb, F, p, stream);
+    return sg::launch_backward<false>({A, B, fa, fb, lda, ldb, F}, p, stream);
 }
 
 extern "C" fp8_status_t fp8_mx_swiglu_gemm_backward(const uint8_t *A, int fa, int64_t lda, const uint8_t *sA,
@@ -905,7 +1121,8 @@ extern "C" fp8_status_t fp8_mx_swiglu_gemm_backward(const uint8_t *A, int fa, in
 {
     SG_TRY(sg::check_operands(A, fa, lda, B, fb, ldb, M, F, K, FP8_MX_BLOCK));
     sg::Params p = sg::sizes(M, F, K);
-    SG_TRY(sg::set_mx(sA, sB, round_up_128(F), p));
+    sg::Operands o{A, B, fa, fb, lda, ldb, F};
+    SG_TRY(sg::set_mx(sA, sB, round_up_128(F), M, o));
     SG_TRY(sg::set_bf16(gate_up_bf16, ld_gu, F, 2, p.gate_up, p.ld_gu, p.gu32));
     SG_TRY(sg::set_checkpoint(q, ld_q, s, ld_s, ckpt_fmt, p));
     if (M > 0 && (p.gate_up != nullptr) == (p.cq != nullptr)) return FP8_ERR_INVALID_ARG;  // one of them
@@ -913,5 +1130,5 @@ extern "C" fp8_status_t fp8_mx_swiglu_gemm_backward(const uint8_t *A, int fa, in
     SG_TRY(sg::set_bf16(d_gate_up_bf16, ld_d, F, 2, p.out, p.ld_out, p.out32));
     if (!layouts && !p.out && M > 0) return FP8_ERR_INVALID_ARG;
     if (M == 0) return FP8_OK;
-    return sg::launch<true, true>(A, fa, lda, B, fb, ldb, F, p, stream);
+    return sg::launch_backward<true>(o, p, stream);
 }
