@@ -556,17 +556,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(sA + stage * A_BYTES), b_addr = smem_u32(sB + stage * L::b_bytes);
+                    const uint64_t ad = smem_desc_k128_sw128(smem_u32(sA + stage * A_BYTES));
+                    const uint64_t bd = smem_desc_k128_sw128(smem_u32(sB + stage * L::b_bytes));
                     const uint32_t ca = tmem_base + SFA_COL + 4 * stage, cb = tmem_base + SFB_COL + 8 * stage;
-                    const int steps = kb == p.num_k - 1 ? last_steps : BK / UMMA_K;
-                    for (int k = 0; k < steps; k++) {
-                        const uint64_t ad = smem_desc_k128_sw128(a_addr + k * UMMA_K);
-                        const uint64_t bd = smem_desc_k128_sw128(b_addr + k * UMMA_K);
+                    const auto mma = [&](int k) {  // K = 32: the descriptors' addresses are in 16 bytes
+                        const uint64_t a = ad + k * (UMMA_K >> 4), b = bd + k * (UMMA_K >> 4);
                         const uint32_t id = MX ? idesc_sf_ids(idesc, (uint32_t)k, (uint32_t)k) : idesc;
-                        if constexpr (MX && PAIR) mma_mxf8f6f4_pair(d, ad, bd, id, ca, cb, (kb | k) != 0);
-                        else if constexpr (MX) mma_mxf8f6f4(d, ad, bd, id, ca, cb, (kb | k) != 0);
-                        else if constexpr (PAIR) mma_f8f6f4_pair(d, ad, bd, id, (kb | k) != 0);
-                        else mma_f8f6f4(d, ad, bd, id, (kb | k) != 0);
+                        if constexpr (MX && PAIR) mma_mxf8f6f4_pair(d, a, b, id, ca, cb, (kb | k) != 0);
+                        else if constexpr (MX) mma_mxf8f6f4(d, a, b, id, ca, cb, (kb | k) != 0);
+                        else if constexpr (PAIR) mma_f8f6f4_pair(d, a, b, id, (kb | k) != 0);
+                        else mma_f8f6f4(d, a, b, id, (kb | k) != 0);
+                    };
+                    if (kb < p.num_k - 1 || last_steps == BK / UMMA_K) {
+#pragma unroll
+                        for (int k = 0; k < BK / UMMA_K; k++) mma(k);
+                    } else {
+                        for (int k = 0; k < last_steps; k++) mma(k);
                     }
                     if (PAIR) mma_commit_pair(&empty[stage], 0x3);
                     else mma_commit(&empty[stage]);
@@ -664,7 +669,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+                    // only TMEM is handed over: a release at cluster scope would wait for the stores
+                    // of the tile before (2 us a tile)
+                    if (PAIR)
+                        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
+                                         mapa_shared(smem_u32(&tempty[acc]), 0))
+                                     : "memory");
                     else mbar_arrive(&tempty[acc]);
                 }
             };
