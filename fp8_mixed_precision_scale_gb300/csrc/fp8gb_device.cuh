@@ -586,27 +586,22 @@ __device__ __forceinline__ uint32_t swiglu2(uint32_t g2, uint32_t u2)
 // ---------------------------------------------------------------------------
 
 // E8M0 code of a block from the fp32 bit pattern of its largest magnitude:
-// floor(log2 amax) is the exponent field (normal) or the position of the top
-// mantissa bit (subnormal), minus emax_elem, clamped to [-127, 127].
+// floor(log2 amax) - emax_elem clamped to [-127, 127], plus 127.  floor(log2) is
+// the exponent field less its bias, which cancels the code's; a subnormal or zero
+// amax (field 0) clamps to code 0, and nothing finite reaches the upper clamp.
 template <int FMT>
 __device__ __forceinline__ uint32_t mx_code(uint32_t amax_bits)
 {
     constexpr int emax = FMT == FP8_E5M2 ? 15 : 8;
-    if (amax_bits >= 0x7F800000u) return 255u;  // Inf or NaN in the block
-    if (amax_bits == 0u) return 0u;
-    const int ex = (int)(amax_bits >> 23);
-    const int fl = ex > 0 ? ex - 127 : (31 - __clz((int)amax_bits)) - 149;
-    int e = fl - emax;
-    e = e < -127 ? -127 : (e > 127 ? 127 : e);
-    return (uint32_t)(e + 127);
+    const int code = (int)(amax_bits >> 23) - emax;
+    return amax_bits >= 0x7F800000u ? 255u : (uint32_t)(code < 0 ? 0 : code);  // Inf or NaN in the block: 255
 }
 
-// 1 / X = 2^(127 - code) as an fp32 (a normal number for every code a bf16
-// block can produce); NaN for the NaN scale, so the block's elements are NaN.
+// 1 / X = 2^(127 - code) as an fp32 (a normal number for every code that mx_code
+// gives); NaN for the NaN scale, so the block's elements are NaN.
 __device__ __forceinline__ float mx_inv_scale(uint32_t code)
 {
-    if (code == 255u) return __uint_as_float(0x7FC00000u);
-    return code <= 253u ? __uint_as_float((254u - code) << 23) : __uint_as_float(0x00400000u);
+    return __uint_as_float(code == 255u ? 0x7FC00000u : (254u - code) << 23);
 }
 
 // ---------------------------------------------------------------------------

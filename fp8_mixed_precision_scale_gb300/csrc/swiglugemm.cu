@@ -26,7 +26,7 @@
 //              the columns.  A thread has one row: blocks of 32 columns, their
 //              maxima and codes need no other thread.  The transposed layout's
 //              blocks are 32 rows of a column, a warp's rows exactly: they go
-//              through the warp's shared-memory staging, 16 columns at a time.
+//              through the warp's shared-memory staging.
 // With per-row scales two accumulators overlap the epilogue and the next tile's
 // main loop.  MX scales take part of TMEM, which leaves one accumulator: each
 // epilogue thread first takes its 128 columns into registers and releases it.
@@ -65,15 +65,14 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t SFA_COL = 256, SFB_COL = 288;
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 
-// Staging of a warp: 32 rows x 16 columns of fp32, rows 20 words apart and the
-// second 16 rows 16 words further, so that neither the row writes (16 bytes a
-// thread) nor the column reads (two columns' halves a warp) meet a bank twice.
-constexpr int STAGE_WORDS = 31 * 20 + 16 + 16;
-__device__ __forceinline__ int stage_word(int row) { return row * 20 + (row & 16); }
+// Staging of a warp: 32 rows x 32 columns of fp32.  Rows of 36 words: the row
+// writes (16 bytes a thread) and the column reads meet no bank twice.
+constexpr int STAGE_PITCH = 36;
+constexpr int STAGE_WORDS = 32 * STAGE_PITCH;
 
 template <bool PAIR>
 struct Smem {
-    static constexpr int stages = PAIR ? 6 : 4;
+    static constexpr int stages = PAIR ? 5 : 3;
     static constexpr int boxes = PAIR ? 1 : 2;  // of B a CTA stages
     static constexpr int b_bytes = boxes * BB * BK;
     static constexpr int a_off = 0;
@@ -120,6 +119,7 @@ struct Params {
     int64_t ld_row, ld_col, rs_row, rs_col;
     int64_t Fr;  // columns of h that q_row has (backward: of each half; zeros from F on)
     int q32;     // q_row's rows and halves start on 32-byte boundaries
+    int c32;     // q_col's rows do
     unsigned int *err;
 };
 
@@ -133,12 +133,34 @@ __device__ __forceinline__ uint32_t mx_code_of(uint32_t amax_bits, int fmt)
     return fmt == FP8_E5M2 ? mx_code<FP8_E5M2>(amax_bits) : mx_code<FP8_E4M3FN>(amax_bits);
 }
 
-__device__ __forceinline__ float amax16(const float (&v)[16], float m)  // NaN if any is
+__device__ __forceinline__ float max3_nan(float a, float b, float c)  // NaN if any is
 {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Largest magnitude of 32 values and m, in four chains.
+__device__ __forceinline__ float amax32(const float (&v)[2][16], float m)
+{
+    float a[4] = {m, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 16; j += 2)
-        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(fabsf(v[j])), "f"(fabsf(v[j + 1])));
-    return m;
+    for (int j = 0; j < 32; j += 2)
+        a[j / 2 & 3] = max3_nan(a[j / 2 & 3], fabsf(v[j >> 4][j & 15]), fabsf(v[j >> 4][(j & 15) + 1]));
+    return max_nan(max3_nan(a[0], a[1], a[2]), a[3]);
+}
+
+// sigma(g), e^-g and silu(g) of two gates as silu2 has them, with the exponential's
+// result flushed to zero below 2^-126 (1 - sigma and sigma - 1 are below that then).
+__device__ __forceinline__ void silu2_ftz(float2 g, float2 &e, float2 &sigma, float2 &silu)
+{
+    g = make_float2(max_nan(g.x, -88.0f), max_nan(g.y, -88.0f));
+    const float2 x = mul2(g, make_float2(-1.44269504f, -1.44269504f));  // -log2 e
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(x.y));
+    const float2 d = add2(e, make_float2(1.0f, 1.0f));
+    sigma = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    silu = mul2(g, sigma);
 }
 
 // n (0, 16 or 32) codes, or their first n.
@@ -190,7 +212,7 @@ __device__ __forceinline__ uint32_t put_row(const Params &p, const float (&v)[2]
     uint32_t code = 0;
     float inv = scale;
     if (MX) {
-        code = mx_code_of(__float_as_uint(amax16(v[1], amax16(v[0], 0.0f))), p.fmt);
+        code = mx_code_of(__float_as_uint(amax32(v, 0.0f)), p.fmt);
         inv = mx_inv_scale(code);
     }
     if (t.live)
@@ -199,47 +221,42 @@ __device__ __forceinline__ uint32_t put_row(const Params &p, const float (&v)[2]
 }
 
 // ... and into the transposed layout: cc, n the first row in q_col and how many of
-// the 32 it has.  PAD: the scale bytes of all 32 are written, zeros (a zero
-// block's code) behind the data, where the layout's padding is this tile's alone.
+// the 32 it has.  A lane takes a column.  PAD: the scale bytes of all 32 are
+// written, zeros (a zero block's code) behind the data, where the layout's
+// padding is this tile's alone.
 template <bool MX, bool PAD>
 __device__ __forceinline__ void put_col(const Params &p, const float (&v)[2][16], const Place &t, int64_t cc, int n,
                                         float scale)
 {
-    const int c = t.lane & 15, h = t.lane >> 4;
-    const int64_t r = t.row0 + 16 * h;
+    float4 *w = reinterpret_cast<float4 *>(t.stage + t.lane * STAGE_PITCH);
+    __syncwarp();  // the columns before are read
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        float4 *w = reinterpret_cast<float4 *>(t.stage + stage_word(t.lane));
+    for (int j = 0; j < 8; j++)
+        w[j] = make_float4(v[j >> 2][4 * j & 15], v[j >> 2][(4 * j & 15) + 1], v[j >> 2][(4 * j & 15) + 2],
+                           v[j >> 2][(4 * j & 15) + 3]);
+    __syncwarp();
+    float x[2][16];
 #pragma unroll
-        for (int j = 0; j < 4; j++) w[j] = make_float4(v[i][4 * j], v[i][4 * j + 1], v[i][4 * j + 2], v[i][4 * j + 3]);
-        __syncwarp();
-        float x[16];
+    for (int j = 0; j < 32; j++) x[j >> 4][j & 15] = t.stage[j * STAGE_PITCH + t.lane];
+    const bool have = t.lane < n;
+    const int64_t r = cc + t.lane;
+    float inv = scale;
+    if (MX) {
+        const uint32_t code = mx_code_of(__float_as_uint(amax32(x, 0.0f)), p.fmt);
+        inv = mx_inv_scale(code);
+        if (PAD || have) p.s_col[4 * mx_scale_word(t.row0 >> 7, r, p.rs_col) + (t.row0 >> 5 & 3)] = (uint8_t)code;
+    }
+    if (have) {
+        uint8_t *dst = p.q_col + r * p.ld_col + t.row0;
+        const uint4 lo = encode(x[0], inv, p.fmt), hi = encode(x[1], inv, p.fmt);
+        if (t.row0 + 32 <= p.M) {
+            put_codes(dst, lo, hi, 32, p.c32);
+        } else if (!MX) {  // MX: whole blocks of 32 rows
+            const uint32_t qw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int j = 0; j < 16; j++) x[j] = t.stage[h * (16 * 20 + 16) + j * 20 + c];
-        const bool have = 16 * i + c < n;
-        float inv = scale;
-        if (MX) {
-            float m = amax16(x, 0.0f);
-            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            const uint32_t code = mx_code_of(__float_as_uint(m), p.fmt);
-            inv = mx_inv_scale(code);
-            if (h == 0 && (PAD || have))
-                p.s_col[4 * mx_scale_word(t.row0 >> 7, cc + 16 * i + c, p.rs_col) + (t.row0 >> 5 & 3)] = (uint8_t)code;
+            for (int j = 0; j < 32; j++)
+                if (t.row0 + j < p.M) dst[j] = (uint8_t)(qw[j >> 2] >> (8 * (j & 3)));
         }
-        const uint4 q = encode(x, inv, p.fmt);
-        if (have) {
-            uint8_t *dst = p.q_col + (cc + 16 * i + c) * p.ld_col + r;
-            if (r + 16 <= p.M) {
-                *reinterpret_cast<uint4 *>(dst) = q;
-            } else if (!MX) {  // MX: whole blocks of 32 rows
-                const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll 1
-                for (int j = 0; j < 16; j++)
-                    if (r + j < p.M)
-                        dst[j] = (uint8_t)((j < 8 ? j < 4 ? qw[0] : qw[1] : j < 12 ? qw[2] : qw[3]) >> (8 * (j & 3)));
-            }
-        }
-        __syncwarp();
     }
 }
 
@@ -337,8 +354,8 @@ __device__ __forceinline__ uint32_t forward_unit(const Params &p, float (&g)[2][
         put_bf16(dst + p.F, u, n, p.gu32);
     }
     if (p.cq && t.live && c < p.W) {
-        const uint32_t a = ckpt_code(__float_as_uint(amax16(g[1], amax16(g[0], 0.0f))), p.cfmt);
-        const uint32_t b = ckpt_code(__float_as_uint(amax16(u[1], amax16(u[0], 0.0f))), p.cfmt);
+        const uint32_t a = ckpt_code(__float_as_uint(amax32(g, 0.0f)), p.cfmt);
+        const uint32_t b = ckpt_code(__float_as_uint(amax32(u, 0.0f)), p.cfmt);
         const float ia = ckpt_inv_scale(a), ib = ckpt_inv_scale(b);
         uint8_t *q = p.cq + t.row * p.ld_cq + c, *s = p.cs + t.row * p.ld_cs + (c >> 5);
         st_32b(q, encode(g[0], ia, p.cfmt), encode(g[1], ia, p.cfmt));
@@ -351,12 +368,12 @@ __device__ __forceinline__ uint32_t forward_unit(const Params &p, float (&g)[2][
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
             float2 e, sg, si;
-            silu2(make_float2(g[i][j], g[i][j + 1]), e, sg, si);
+            silu2_ftz(make_float2(g[i][j], g[i][j + 1]), e, sg, si);
             si = mul2(si, make_float2(u[i][j], u[i][j + 1]));
             g[i][j] = si.x, g[i][j + 1] = si.y;
         }
     if (p.out && t.live) put_bf16(p.out + t.row * p.ld_out + c, g, n, p.out32);
-    if (!MX) amax = amax16(g[1], amax16(g[0], amax));
+    if (!MX) amax = amax32(g, amax);
     uint32_t code = 0;
     if (p.q_row) code = put_row<MX>(p, g, t, c, n, scale);
     if (p.q_col && (MX || n > 0)) put_col<MX, MX>(p, g, t, c, n, scale);
@@ -375,9 +392,11 @@ __device__ __forceinline__ uint32_t backward_unit(const Params &p, float (&g)[2]
         kept16(p, kept, 1, i, ku);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-            float2 dg, du, h;
-            swiglu_grad2(make_float2(kg[j], kg[j + 1]), make_float2(ku[j], ku[j + 1]),
-                         make_float2(g[i][j], g[i][j + 1]), dg, du, h);
+            float2 e, sg, si;
+            silu2_ftz(make_float2(kg[j], kg[j + 1]), e, sg, si);
+            const float2 dh = make_float2(g[i][j], g[i][j + 1]);
+            const float2 dg = mul2(mul2(dh, make_float2(ku[j], ku[j + 1])), fma2(si, mul2(e, sg), sg));
+            const float2 du = mul2(dh, si);
             g[i][j] = dg.x, g[i][j + 1] = dg.y;
             u[i][j] = du.x, u[i][j + 1] = du.y;
         }
@@ -392,19 +411,16 @@ __device__ __forceinline__ uint32_t backward_unit(const Params &p, float (&g)[2]
         put_bf16(dst, g, n, p.out32);
         put_bf16(dst + p.F, u, n, p.out32);
     }
-    if (!MX) amax = amax16(u[1], amax16(u[0], amax16(g[1], amax16(g[0], amax))));
+    if (!MX) amax = amax32(u, amax32(g, amax));
     uint32_t codes = 0;
-    // d_gate, then d_up, through the same instructions: twice as many would not stay
-    // in the instruction cache
-#pragma unroll 1
-    for (int h = 0; h < 2; h++) {
-        if (p.q_row) {
-            const uint32_t code = put_row<MX>(p, g, t, h ? p.Fr + c : c, c < p.Fr ? (MX ? 32 : n) : 0, scale);
-            codes |= code << (8 * h);
-        }
-        if (p.q_col && n > 0) put_col<MX, false>(p, g, t, h ? p.F + c : c, n, scale);
-#pragma unroll
-        for (int j = 0; j < 32; j++) g[j >> 4][j & 15] = u[j >> 4][j & 15];
+    if (p.q_row) {
+        const int m = c < p.Fr ? (MX ? 32 : n) : 0;
+        codes = put_row<MX>(p, g, t, c, m, scale);
+        codes |= put_row<MX>(p, u, t, p.Fr + c, m, scale) << 8;
+    }
+    if (p.q_col && n > 0) {
+        put_col<MX, false>(p, g, t, c, n, scale);
+        put_col<MX, false>(p, u, t, p.F + c, n, scale);
     }
     return codes;
 }
@@ -1000,6 +1016,7 @@ static fp8_status_t set_8bit(int fmt, int layouts, uint8_t *q_row, uint8_t *s_ro
         p.q_col = q_colT;
         p.s_col = s_col;
         p.ld_col = ld_colT;
+        p.c32 = rows_of(q_colT, ld_colT, 0, 1, 32);
     }
     return FP8_OK;
 }
