@@ -1087,9 +1087,9 @@ def _mx_scale_buffer(rows, blocks, dev):
 def _scaled_outputs(rows, cols, dev, layouts, per_row) -> Quantized:
     ld_colT = max(16, (rows + 15) // 16 * 16)
     q = Quantized(None, None, None, None, ld_colT)
-    scale = torch.empty(max(rows, 1) if per_row else 1, dtype=torch.float32, device=dev)
+    scale = torch.empty(rows if per_row else 1, dtype=torch.float32, device=dev)
     if layouts & LAYOUT_ROW:
-        q.q_row, q.scale_inv_row = _u8(rows, cols, dev), scale[:rows] if per_row else scale
+        q.q_row, q.scale_inv_row = _u8(rows, cols, dev), scale
     if layouts & LAYOUT_COLT:
         q.q_colT, q.scale_inv_col = _u8(cols, ld_colT, dev), scale
     return q

@@ -492,6 +492,14 @@ __device__ __forceinline__ float max_nan(float a, float b)  // NaN if either is
     return r;
 }
 
+// The largest magnitude of three; NaN if any is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ float rcp_fast(float v)  // 1 ulp; 0 where 1 / v is subnormal
 {
     float r;

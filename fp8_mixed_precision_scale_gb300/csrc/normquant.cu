@@ -40,6 +40,7 @@ struct Args {
     float *amax_out, *scale_inv_row, *scale_inv_col;
     uint8_t *q_row, *s_row, *q_col, *s_col;
     int64_t ld_col, rs_row, rs_col;
+    int c32;                  // q_col's rows start on 32-byte boundaries
     int G, ranks, part_cols;  // as in a norm's launch
     int w32;
     int64_t end_x, end_res;  // elements from their start to the end of their last row
@@ -265,78 +266,119 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_quantize_rows(Args a)
             }
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the columns' blocks may start
     if (a.recipe == DELAYED) {
         amax = __reduce_max_sync(0xffffffffu, amax);
         if ((threadIdx.x & 31) == 0 && amax) atomicMax(reinterpret_cast<unsigned int *>(a.amax_out), amax);
     }
 }
 
-// The transposed layout: tiles of 128 rows x 64 columns of the sum through
-// shared memory; a thread then has 32 rows of a column, a block.
-constexpr int CR = 128, CC = 64, C_THREADS = 256;
+// The transposed layout: tiles of 128 rows x 128 columns of the normalized rows
+// through shared memory, in fp32; a thread then has 32 rows of a column, a block.
+// Launched while the rows' kernel ends (programmatic dependent launch), and from
+// the last rows on, which are still in L2.
+constexpr int CR = 128, CC = 128, C_THREADS = 256;
+constexpr int C_SMEM = CR * CC * (int)sizeof(float);
+
+// Word of column c in its row: 16-byte unit u is kept at u ^ (u / 4 % 8), so that
+// neither the writes (threads 64 bytes apart) nor the reads (consecutive columns)
+// meet a bank twice (four times without: the kernel was bound by that).
+__device__ __forceinline__ int tile_word(int c) { return c ^ (c >> 2 & 28); }
+
+// The first n of 32 codes.  Out of line: only the last rows have fewer.
+static __device__ __noinline__ void put_some(uint8_t *dst, uint4 lo, uint4 hi, int n)
+{
+    const uint64_t q[4] = {lo.x | (uint64_t)lo.y << 32, lo.z | (uint64_t)lo.w << 32, hi.x | (uint64_t)hi.y << 32,
+                           hi.z | (uint64_t)hi.w << 32};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint64_t v = q[i];
+#pragma unroll 1
+        for (int j = 8 * i; j < n && j < 8 * i + 8; j++, v >>= 8) dst[j] = (uint8_t)v;
+    }
+}
 
 template <typename T, bool ANY>
-__global__ void __launch_bounds__(C_THREADS) norm_quantize_cols(Args a)
+__global__ void __launch_bounds__(C_THREADS, 3) norm_quantize_cols(Args a)
 {
-    constexpr int PITCH = CC + 16 / sizeof(T);
-    __shared__ __align__(16) T tile[CR * PITCH];
-    __shared__ float mean[CR], rstd[CR];
+    extern __shared__ __align__(16) float tile[];  // [CR][CC] xhat
     const T *src = static_cast<const T *>(a.res ? a.sum : a.x);
     const int64_t ld = a.res ? a.ld_sum : a.ld_x, end = rows_end(ld, a.rows, a.cols);
-    const int64_t n_ct = (a.recipe == MX ? a.rs_col : a.cols + CC - 1) / CC;  // MX: scale rows of the padding too
-    const int64_t rt = blockIdx.x / n_ct, ct = blockIdx.x - rt * n_ct;
-    const int64_t r0 = rt * CR, col0 = ct * CC;
+    const uint32_t n_ct = (uint32_t)(a.rs_col / CC), n_rt = gridDim.x / n_ct;
+    const uint32_t rt = blockIdx.x / n_ct, ct = blockIdx.x - rt * n_ct;
+    const int64_t r0 = (int64_t)(n_rt - 1 - rt) * CR;
+    const int col0 = (int)ct * CC;
+    const int left = (int)(a.rows - r0 < CR ? a.rows - r0 : CR);
+    constexpr int PER = CC / 16, UNITS = CR * PER / C_THREADS, STEP = C_THREADS / PER;  // of 16 columns
+    const int lr = threadIdx.x / PER, lc = threadIdx.x % PER * 16;
+    const bool in = col0 + lc < a.cols;  // widths are multiples of 16
+
+    const int c = col0 + threadIdx.x % CC;
+    const bool column = c < a.cols;
+    const float w = column ? param(a.weight, a.w_dtype, c, 1.0f) : 0.0f;
+    const float b = column ? param(a.bias, a.w_dtype, c, 0.0f) : 0.0f;
+    const float scale = a.recipe == MX ? 1.0f : __ldg(a.scale_in);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the sum and the statistics are written
+
+    Raw<T, ANY> raw[UNITS];
+    float rs[UNITS], mm[UNITS];
 #pragma unroll
-    for (int i = 0; i < CR * CC / 16 / C_THREADS; i++) {
-        const int u = i * C_THREADS + threadIdx.x, lr = u / (CC / 16), lc = u % (CC / 16) * 16;
-        const int64_t r = r0 + lr, c = col0 + lc, at = r * ld + c;
-        const int n = r < a.rows && c < a.cols ? 16 : 0;  // widths are multiples of 16
-        Raw<T, ANY> raw;
+    for (int i = 0; i < UNITS; i++) {
+        const int k = lr + i * STEP;
+        const int64_t at = (r0 + k) * ld + col0 + lc;
+        const bool live = k < left;
+        load_chunk<ANY>(src + at, live && in ? 16 : 0, a.w32, at, end, raw[i]);
+        rs[i] = live ? a.rstd[r0 + k] : 0.0f;
+        mm[i] = live && !a.rms ? -a.mean[r0 + k] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < UNITS; i++) {
         float f[16];
-        load_chunk<ANY>(src + at, n, a.w32, at, end, raw);
-        unpack16(raw, f);
-        if (n) store16(tile + lr * PITCH + lc, f, 16, false);
-    }
-    if (threadIdx.x < CR) {
-        const int64_t r = r0 + threadIdx.x;
-        const bool live = r < a.rows;
-        mean[threadIdx.x] = live && !a.rms ? a.mean[r] : 0.0f;
-        rstd[threadIdx.x] = live ? a.rstd[r] : 0.0f;
-    }
-    __syncthreads();
-    const int lc = threadIdx.x % CC, rb = threadIdx.x / CC;
-    const int64_t c = col0 + lc, r = r0 + 32 * rb;
-    const bool have = c < a.cols && r < a.rows;
-    float v[2][16] = {};
-    if (have) {
-        const float w = param(a.weight, a.w_dtype, c, 1.0f), b = param(a.bias, a.w_dtype, c, 0.0f);
+        unpack16(raw[i], f);
 #pragma unroll
-        for (int j = 0; j < 32; j++) {
-            const int lr = 32 * rb + j;
-            const float xh = (to_f32(tile[lr * PITCH + lc]) - mean[lr]) * rstd[lr];
-            v[j >> 4][j & 15] = r + j < a.rows ? (a.bias ? fmaf(xh, w, b) : xh * w) : 0.0f;
+        for (int j = 0; j < 16; j += 4) {
+            const float2 u = mul2(add2(make_float2(f[j], f[j + 1]), make_float2(mm[i], mm[i])), make_float2(rs[i], rs[i]));
+            const float2 v =
+                mul2(add2(make_float2(f[j + 2], f[j + 3]), make_float2(mm[i], mm[i])), make_float2(rs[i], rs[i]));
+            *reinterpret_cast<float4 *>(tile + (lr + i * STEP) * CC + tile_word(lc + j)) = make_float4(u.x, u.y, v.x, v.y);
         }
     }
-    float inv;
-    if (a.recipe == MX) {
-        const uint32_t code = mx_code_of(amax16(v[1], amax16(v[0], 0u)), a.fmt);
-        inv = mx_inv_scale(code);
-        a.s_col[4 * mx_scale_word(rt, c, a.rs_col) + rb] = (uint8_t)code;  // zero blocks: the padding's zeros
-    } else {
-        inv = __ldg(a.scale_in);
-    }
-    if (!have) return;
-    uint8_t *dst = a.q_col + c * a.ld_col + r;
+    __syncthreads();
+    uint8_t *s = a.recipe == MX ? a.s_col + 4 * mx_scale_word(r0 >> 7, c, a.rs_col) : nullptr;
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const uint4 q = encode(v[i], inv, a.fmt);
-        if (r + 16 * i + 16 <= a.rows) {
-            *reinterpret_cast<uint4 *>(dst + 16 * i) = q;
+    for (int i = 0; i < CR / 32 * CC / C_THREADS; i++) {
+        const int rb = threadIdx.x / CC + i * (C_THREADS / CC), n = min(32, left - 32 * rb);
+        const float *from = tile + 32 * rb * CC + tile_word(threadIdx.x % CC);
+        float v[2][16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            // w = b = 0 behind the last column, where what the load left is 0
+            const float2 y = fma2(make_float2(from[j * CC], from[(j + 1) * CC]), make_float2(w, w),
+                                  make_float2(b, b));
+            v[j >> 4][j & 15] = y.x, v[j >> 4][(j & 15) + 1] = y.y;
+        }
+        float inv = scale;
+        if (a.recipe == MX) {  // whole blocks of 32 rows; zeros behind the data
+            float m = 0.0f, o = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                m = max3_abs(m, v[0][j], v[0][j + 1]);
+                o = max3_abs(o, v[1][j], v[1][j + 1]);
+            }
+            const uint32_t code = n > 0 ? mx_code_of(__float_as_uint(max_nan(m, o)), a.fmt) : 0u;
+            inv = mx_inv_scale(code);
+            s[rb] = (uint8_t)code;
+        }
+        if (!column || n <= 0) continue;
+        uint8_t *dst = a.q_col + c * a.ld_col + r0 + 32 * rb;
+        const uint4 lo = encode(v[0], inv, a.fmt), hi = encode(v[1], inv, a.fmt);
+        if (n < 32) {
+            put_some(dst, lo, hi, n);
+        } else if (a.c32) {
+            st_32b(dst, lo, hi);
         } else {
-            const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int j = 0; j < 16; j++)
-                if (r + 16 * i + j < a.rows) dst[16 * i + j] = (uint8_t)(qw[j >> 2] >> (8 * (j & 3)));
+            *reinterpret_cast<uint4 *>(dst) = lo;
+            *reinterpret_cast<uint4 *>(dst + 16) = hi;
         }
     }
 }
@@ -387,10 +429,24 @@ static fp8_status_t launch_cols(Args a, cudaStream_t st)
     const void *src = a.res ? a.sum : a.x;
     const int64_t ld = a.res ? a.ld_sum : a.ld_x;
     a.w32 = rows_aligned(src, ld, sizeof(T), 32);
-    const int64_t n_ct = (a.recipe == MX ? a.rs_col : a.cols + CC - 1) / CC;
-    const int64_t grid = (a.rows + CR - 1) / CR * n_ct;
-    if (rows_aligned(src, ld, sizeof(T), 16)) norm_quantize_cols<T, false><<<(unsigned)grid, C_THREADS, 0, st>>>(a);
-    else norm_quantize_cols<T, true><<<(unsigned)grid, C_THREADS, 0, st>>>(a);
+    a.c32 = rows_aligned(a.q_col, a.ld_col, 1, 32);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.rows + CR - 1) / CR * (a.rs_col / CC)));
+    cfg.blockDim = dim3(C_THREADS);
+    cfg.dynamicSmemBytes = C_SMEM;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (rows_aligned(src, ld, sizeof(T), 16)) {
+        if (!allow_shared<norm_quantize_cols<T, false>, C_SMEM>()) return cuda_fail();
+        cudaLaunchKernelEx(&cfg, norm_quantize_cols<T, false>, a);
+    } else {
+        if (!allow_shared<norm_quantize_cols<T, true>, C_SMEM>()) return cuda_fail();
+        cudaLaunchKernelEx(&cfg, norm_quantize_cols<T, true>, a);
+    }
     return check_launch();
 }
 

@@ -133,21 +133,14 @@ __device__ __forceinline__ uint32_t mx_code_of(uint32_t amax_bits, int fmt)
     return fmt == FP8_E5M2 ? mx_code<FP8_E5M2>(amax_bits) : mx_code<FP8_E4M3FN>(amax_bits);
 }
 
-__device__ __forceinline__ float max3_nan(float a, float b, float c)  // NaN if any is
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 // Largest magnitude of 32 values and m, in four chains.
 __device__ __forceinline__ float amax32(const float (&v)[2][16], float m)
 {
     float a[4] = {m, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < 32; j += 2)
-        a[j / 2 & 3] = max3_nan(a[j / 2 & 3], fabsf(v[j >> 4][j & 15]), fabsf(v[j >> 4][(j & 15) + 1]));
-    return max_nan(max3_nan(a[0], a[1], a[2]), a[3]);
+        a[j / 2 & 3] = max3_abs(a[j / 2 & 3], v[j >> 4][j & 15], v[j >> 4][(j & 15) + 1]);
+    return max_nan(max3_abs(a[0], a[1], a[2]), a[3]);
 }
 
 // sigma(g), e^-g and silu(g) of two gates as silu2 has them, with the exponential's
