@@ -1035,6 +1035,7 @@ def norm_backward(dy: torch.Tensor, src, mean, rstd: torch.Tensor, weight=None, 
         if kind == LAYER_NORM and mean is None:
             _refuse(where, "a layer norm's backward from x needs its mean")
         dx_dtype = x.dtype
+    ld_dsum = 0 if dsum is None else _matrix(dsum, where, "dsum", rows, cols, dx_dtype)
     if out is None:
         out, ld_dx = torch.empty((rows, cols), dtype=dx_dtype, device=dev), cols
     else:
@@ -1053,7 +1054,6 @@ def norm_backward(dy: torch.Tensor, src, mean, rstd: torch.Tensor, weight=None, 
                                                 _ptr(weight), DTYPES[w_dtype], out.data_ptr(), DTYPES[dx_dtype],
                                                 ld_dx, _ptr(dw), _ptr(db), _ptr(ws), n, _stream(None)), where)
     else:
-        ld_dsum = _matrix(dsum, where, "dsum", rows, cols, dx_dtype)
         _check(load_library().fp8_residual_norm_backward(
             dy.data_ptr(), DTYPES[dy.dtype], ld_dy, _ptr(x), ld_x, _ptr(q), ld_q, _ptr(s), ld_s, fmt, dsum.data_ptr(),
             ld_dsum, rows, cols, kind, _ptr(mean), rstd.data_ptr(), _ptr(weight), DTYPES[w_dtype], out.data_ptr(),
@@ -1149,10 +1149,10 @@ def norm_quantize(x: torch.Tensor, residual=None, weight=None, bias=None, kind: 
             return norm_quantize(x, residual, weight, bias, kind, eps, fmt, recipe, layouts, scale_in, amax_out, out)
     where = "norm_quantize"
     recipe = recipe or Recipe(kind=ROWWISE)
-    front, params, total, mean, rstd = _norm_inputs(x, residual, weight, bias, kind, out, where)
     for t, name in ((scale_in, "scale_in"), (amax_out, "amax_out")):
         if t is not None:
             _vector(t, where, name, 1, torch.float32)
+    front, params, total, mean, rstd = _norm_inputs(x, residual, weight, bias, kind, out, where)
     rows, cols = x.shape
     q = _scaled_outputs(rows, cols, x.device, layouts, recipe.kind == ROWWISE)
     _check(load_library().fp8_norm_quantize(*front, kind, eps, *params, fmt, ctypes.byref(recipe.c()), layouts,
@@ -1222,7 +1222,8 @@ def _kept(src, M, F, where):
     if isinstance(src, Checkpoint):
         ld_q, ld_s = _checkpoint_strides(src, where, M, F, 2)
         return None, 0, src.q.data_ptr(), ld_q, src.s.data_ptr(), ld_s, src.fmt
-    return src.data_ptr(), _matrix(src, where, "gate_up", M, 2 * F, torch.bfloat16), None, 0, None, 0, 0
+    ld = _matrix(src, where, "gate_up", M, 2 * F, torch.bfloat16)
+    return src.data_ptr(), ld, None, 0, None, 0, 0
 
 
 def _swiglu_gemm_outputs(M, F, dev, h, gate_up, checkpoint_fmt):
@@ -1251,21 +1252,26 @@ def swiglu_gemm(A: torch.Tensor, fa: int, W: torch.Tensor, fw: int, sa: torch.Te
         _refuse(where, "W must have an even number of rows")
     F, dev = W.shape[0] // 2, A.device
     modes = _scale(sa, where, "sa", M), _scale(sw, where, "sw", 2 * F)
-    q, quant = _delayed_outputs(M, F, F, dev, fmt, layouts, scale_in, amax_out, where)
+    _delayed_scales(fmt, scale_in, amax_out, where)
+    q, quant = _delayed_outputs(M, F, F, dev, fmt, layouts, scale_in, amax_out)
     h, gate_up, c, rest = _swiglu_gemm_outputs(M, F, dev, h, gate_up, checkpoint_fmt)
     _check(load_library().fp8_swiglu_gemm(A.data_ptr(), fa, lda, W.data_ptr(), fw, ldw, M, F, K, sa.data_ptr(),
                                           modes[0], sw.data_ptr(), modes[1], *quant, *rest, _stream(None)), where)
     return SwigluGemm(q, h, gate_up, c)
 
 
-def _delayed_outputs(M, row_cols, col_rows, dev, fmt, layouts, scale_in, amax_out, where):
+def _delayed_scales(fmt, scale_in, amax_out, where):
+    for t, name in ((scale_in, "scale_in"), (amax_out, "amax_out")):
+        if t is not None:
+            _vector(t, where, name, 1, torch.float32)
+        elif fmt is not None:
+            _refuse(where, f"8-bit results need {name}")
+
+
+def _delayed_outputs(M, row_cols, col_rows, dev, fmt, layouts, scale_in, amax_out):
     """The delayed recipe's 8-bit outputs, and the C call's arguments for them."""
     if fmt is None:
         return None, (0, 0, None, None, None, None, 0, None)
-    for t, name in ((scale_in, "scale_in"), (amax_out, "amax_out")):
-        if t is None:
-            _refuse(where, f"8-bit results need {name}")
-        _vector(t, where, name, 1, torch.float32)
     q = Quantized(None, None, None, None, max(16, (M + 15) // 16 * 16))
     scale = torch.empty(1, dtype=torch.float32, device=dev)
     if layouts & LAYOUT_ROW:
@@ -1322,8 +1328,9 @@ def swiglu_gemm_backward(A: torch.Tensor, fa: int, B: torch.Tensor, fb: int, sa:
     lda, ldb = _codes(A, where, "A", K), _codes(B, where, "B", K)
     F, dev = B.shape[0], A.device
     modes = _scale(sa, where, "sa", M), _scale(sb, where, "sb", F)
+    _delayed_scales(fmt, scale_in, amax_out, where)
     kept = _kept(src, M, F, where)
-    q, quant = _delayed_outputs(M, 2 * F, 2 * F, dev, fmt, layouts, scale_in, amax_out, where)
+    q, quant = _delayed_outputs(M, 2 * F, 2 * F, dev, fmt, layouts, scale_in, amax_out)
     d = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev) if d_gate_up else None
     _check(load_library().fp8_swiglu_gemm_backward(A.data_ptr(), fa, lda, B.data_ptr(), fb, ldb, M, F, K,
                                                    sa.data_ptr(), modes[0], sb.data_ptr(), modes[1], *kept, *quant,

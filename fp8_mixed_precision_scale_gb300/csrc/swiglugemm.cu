@@ -995,7 +995,7 @@ static fp8_status_t set_8bit(int fmt, int layouts, uint8_t *q_row, uint8_t *s_ro
     SG_TRY(check_format(fmt));
     p.fmt = fmt;
     if (layouts & FP8_LAYOUT_ROW) {
-        if (!q_row || (MX && !s_row)) return FP8_ERR_INVALID_ARG;
+        if (p.M > 0 && (!q_row || (MX && !s_row))) return FP8_ERR_INVALID_ARG;
         if (!aligned(q_row, 16) || !aligned(s_row, 4)) return FP8_ERR_ALIGNMENT;
         p.q_row = q_row;
         p.s_row = s_row;
@@ -1003,7 +1003,7 @@ static fp8_status_t set_8bit(int fmt, int layouts, uint8_t *q_row, uint8_t *s_ro
         p.q32 = rows_of(q_row, p.ld_row, halves == 2 ? p.Fr : 0, 1, 32);
     }
     if (layouts & FP8_LAYOUT_COLT) {
-        if (!q_colT || (MX && !s_col) || ld_colT < p.M) return FP8_ERR_INVALID_ARG;
+        if ((p.M > 0 && (!q_colT || (MX && !s_col))) || ld_colT < p.M) return FP8_ERR_INVALID_ARG;
         if ((MX && p.M % FP8_MX_BLOCK != 0) || ld_colT % 16 != 0 || !aligned(q_colT, 16) || !aligned(s_col, 4))
             return FP8_ERR_ALIGNMENT;
         p.q_col = q_colT;
