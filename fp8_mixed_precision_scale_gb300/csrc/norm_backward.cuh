@@ -203,8 +203,9 @@ __device__ __forceinline__ void cp_async_wait()
 // forward is: 18 instructions an element in half of the issue slots ([32768, 7168]
 // 215 us, 5.5 TB/s).
 //
-// RES adds dsum, the gradient of x that does not come through the norm.  Its loads go out
-// before the row's sums, whose shuffles and barrier they pass under.
+// RES adds dsum, the gradient of x that does not come through the norm.  The ring has
+// no room for it and the registers none while the sums are made: its lines are
+// fetched into L2 with the rows ahead and read once the sums are there.
 template <typename TX, typename TY, bool MULTI, bool CKPT, bool ANY, bool CLUSTER, bool RES = false>
 __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
 {
@@ -290,6 +291,13 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
             if (row < rows && (g.t & ~1) * 16 < cols) scale = __ldg(a.s + row * a.ld_s + (g.t >> 1));
         }
         if constexpr (S > 0) asm volatile("cp.async.commit_group;" ::: "memory");
+        if constexpr (RES) {
+#pragma unroll
+            for (int i = 0; i < ROWS; i++)
+                if (row0 + i * step < rows && n > 0)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const TX *>(a.dsum) +
+                                                                  (row0 + i * step) * a.ld_dsum + g.t * 16));
+        }
     };
     const auto advance = [&]() {
 #pragma unroll
@@ -372,16 +380,6 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
                 }
             }
         }
-        Raw<TX, ANY> past[RES ? ROWS : 1];
-        if constexpr (RES) {
-#pragma unroll
-            for (int i = 0; i < ROWS; i++) {
-                const uint32_t row = r + i * step;
-                const int64_t at = (int64_t)row * a.ld_dsum + g.t * 16;
-                load_chunk<ANY>(static_cast<const TX *>(a.dsum) + at, row < rows ? n : 0, a.w32, at, a.end_dsum,
-                                past[i]);
-            }
-        }
 #pragma unroll
         for (int i = 0; i < ROWS; i++) sum[i] = make_float2(s1[i].x + s1[i].y, s2[i].x + s2[i].y);
         row_sum<MULTI>(sum, G, g, slot);
@@ -394,6 +392,16 @@ __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
             for (int i = 0; i < ROWS; i++) sum[i] = make_float2(t[2 * i], t[2 * i + 1]);
         }
         slot ^= 1;
+        Raw<TX, ANY> past[RES ? ROWS : 1];
+        if constexpr (RES) {
+#pragma unroll
+            for (int i = 0; i < ROWS; i++) {
+                const uint32_t row = r + i * step;
+                const int64_t at = (int64_t)row * a.ld_dsum + g.t * 16;
+                load_chunk<ANY>(static_cast<const TX *>(a.dsum) + at, row < rows ? n : 0, a.w32, at, a.end_dsum,
+                                past[i]);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < ROWS; i++) {
             const uint32_t row = r + i * step;

@@ -55,8 +55,8 @@ constexpr int UMMA_K = 32;
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_FIRST = 4;  // their first warp: a warpgroup of its own for the registers
 constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
-// registers a thread at launch, and after the split: 128 * 56 + 256 * 224 = 384 * 168
-constexpr int REGS = 168, REGS_OTHER = 56, REGS_EPI = 224;
+// registers a thread at launch, and after the split: 128 * 40 + 256 * 232 = 384 * 168
+constexpr int REGS = 168, REGS_OTHER = 40, REGS_EPI = 232;
 static_assert(128 * REGS_OTHER + 32 * EPI_WARPS * REGS_EPI <= THREADS * REGS, "registers");
 constexpr int A_BYTES = BM * BK;
 constexpr int SF_BLOCK = 512;  // scale words of 128 rows in one K tile
