@@ -191,8 +191,7 @@ __device__ __forceinline__ void put_col(const Params &p, const float (&v)[2][16]
 // What the backward reads of a unit of 32 columns of gate and of up.
 template <int KIND>
 struct Kept {
-    uint4 q[4];       // codes: gate's, then up's
-    uint32_t s[2];
+    uint4 q[4];  // codes: gate's, then up's
 };
 template <>
 struct Kept<BACKWARD_BF16> {
@@ -209,13 +208,10 @@ __device__ __forceinline__ void get_kept(const Params &p, const Place &t, int64_
 #pragma unroll
     for (int i = 0; i < 2 * N; i++) k.q[i] = make_uint4(0, 0, 0, 0);
     if constexpr (KIND == BACKWARD_CKPT) {
-        k.s[0] = k.s[1] = 127;
         if (have) {
-            const uint8_t *q = p.cq + t.row * p.ld_cq + c, *s = p.cs + t.row * p.ld_cs + (c >> 5);
+            const uint8_t *q = p.cq + t.row * p.ld_cq + c;
             ld_stream_32b(q, k.q[0], k.q[1]);
             ld_stream_32b(q + p.W, k.q[2], k.q[3]);
-            k.s[0] = __ldg(s);
-            k.s[1] = __ldg(s + (p.W >> 5));
         }
     } else if (have) {
         const uint16_t *src = p.gate_up + t.row * p.ld_gu + c;
@@ -234,12 +230,25 @@ __device__ __forceinline__ void get_kept(const Params &p, const Place &t, int64_
     }
 }
 
-// Half h (16 columns) of gate (w = 0) or up (w = 1).
+// Scale bytes of four blocks of a checkpoint's part from column c on, for the row.
+// Every row is a line of its own, whatever is read of it: a word at a time.
+__device__ __forceinline__ uint32_t kept_scales(const Params &p, const Place &t, int64_t c, int part)
+{
+    if (!t.live || c >= p.F) return 0;
+    const uint8_t *s = p.cs + t.row * p.ld_cs + part * (p.W >> 5) + (c >> 5);
+    if (p.cs4) return __ldg(reinterpret_cast<const uint32_t *>(s));
+    uint32_t v = 0;
+    for (int i = 0; i < 4 && c + 32 * i < p.W; i++) v |= (uint32_t)__ldg(s + i) << (8 * i);
+    return v;
+}
+
+// Half h (16 columns) of gate (w = 0) or up (w = 1); `scales`: their scale bytes.
 template <int KIND>
-__device__ __forceinline__ void kept16(const Params &p, const Kept<KIND> &k, int w, int h, float (&v)[16])
+__device__ __forceinline__ void kept16(const Params &p, const Kept<KIND> &k, const uint32_t (&scales)[2], int w, int h,
+                                       float (&v)[16])
 {
     if constexpr (KIND == BACKWARD_CKPT) {
-        const float x = ckpt_scale(k.s[w]);
+        const float x = ckpt_scale(scales[w] & 0xFFu);
         if (p.cfmt == FP8_E5M2) decode16<FP8_E5M2>(k.q[2 * w + h], x, v);
         else decode16<FP8_E4M3FN>(k.q[2 * w + h], x, v);
     } else {
@@ -271,10 +280,12 @@ __device__ __forceinline__ void mask32(float (&v)[2][16], bool live, int n)
 
 // What a unit of 32 columns of h leaves, from its gate and up (forward) or its dh
 // and kept gate | up (backward).  Returns MX: its blocks' scale codes in the row
-// layout (the backward's d_up in bits 8 to 15).
+// layout (the backward's d_up in bits 8 to 15).  kept: the checkpoint's scale bytes
+// (up's in bits 16 to 23).
 template <bool MX>
 __device__ __forceinline__ uint32_t forward_unit(const Params &p, float (&g)[2][16], float (&u)[2][16],
-                                                 const Place &t, int64_t c, int n, float scale, float &amax)
+                                                 const Place &t, int64_t c, int n, float scale, float &amax,
+                                                 uint32_t &kept)
 {
     if (p.gate_up && t.live) {
         uint16_t *dst = p.gate_up + t.row * p.ld_gu + c;
@@ -285,11 +296,10 @@ __device__ __forceinline__ uint32_t forward_unit(const Params &p, float (&g)[2][
         const uint32_t a = ckpt_code(__float_as_uint(amax32(g, 0.0f)), p.cfmt);
         const uint32_t b = ckpt_code(__float_as_uint(amax32(u, 0.0f)), p.cfmt);
         const float ia = ckpt_inv_scale(a), ib = ckpt_inv_scale(b);
-        uint8_t *q = p.cq + t.row * p.ld_cq + c, *s = p.cs + t.row * p.ld_cs + (c >> 5);
+        uint8_t *q = p.cq + t.row * p.ld_cq + c;
         st_32b(q, encode(g[0], ia, p.cfmt), encode(g[1], ia, p.cfmt));
         st_32b(q + p.W, encode(u[0], ib, p.cfmt), encode(u[1], ib, p.cfmt));
-        s[0] = (uint8_t)a;
-        s[p.W >> 5] = (uint8_t)b;
+        kept = a | b << 16;
     }
 #pragma unroll
     for (int i = 0; i < 2; i++)
@@ -310,14 +320,14 @@ __device__ __forceinline__ uint32_t forward_unit(const Params &p, float (&g)[2][
 
 template <bool MX, int KIND>
 __device__ __forceinline__ uint32_t backward_unit(const Params &p, float (&g)[2][16], const Kept<KIND> &kept,
-                                                  const Place &t, int64_t c, int n, float scale, float &amax)
+                                                  const uint32_t (&scales)[2], const Place &t, int64_t c, int n, float scale, float &amax)
 {
     float u[2][16];
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         float kg[16], ku[16];
-        kept16(p, kept, 0, i, kg);
-        kept16(p, kept, 1, i, ku);
+        kept16(p, kept, scales, 0, i, kg);
+        kept16(p, kept, scales, 1, i, ku);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
             float2 e, sg, si;
@@ -603,7 +613,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             float sa = 1.0f;
             if (!MX) sa = p.sa_row ? (pl.live ? __ldg(p.sa + pl.row) : 0.0f) : __ldg(p.sa);
             Kept<KIND> kept;
+            uint32_t scales[2] = {};
             if constexpr (BWD) get_kept<KIND>(p, pl, c0, columns(0), kept);
+            if constexpr (KIND == BACKWARD_CKPT) {
+                scales[0] = kept_scales(p, pl, c0, 0);
+                scales[1] = kept_scales(p, pl, c0, 1);
+            }
             if (!mbar_wait_bounded(&tfull[acc], acc_phase, WAIT_LIMIT_NS, p.err, ERR_EPILOGUE_WAIT)) break;
             tc_fence_after();
             // accumulator column of the warp's first unit (forward: gate's; up's is 128 further)
@@ -656,7 +671,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if constexpr (BWD) {
                         const Kept<KIND> now = kept;
                         if (u + 1 < UNITS) get_kept<KIND>(p, pl, c + 32, columns(u + 1), kept);
-                        code = backward_unit<MX, KIND>(p, v, now, pl, c, n, scale, amax);
+                        code = backward_unit<MX, KIND>(p, v, now, scales, pl, c, n, scale, amax);
+                        scales[0] >>= 8, scales[1] >>= 8;
                     } else {
                         float up[2][16];
                         from_acc<MX>(r[1], sa, cu, p.sb_row, up);
@@ -664,7 +680,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                             mask32(v, pl.live, n);
                             mask32(up, pl.live, n);
                         }
-                        code = forward_unit<MX>(p, v, up, pl, c, n, scale, amax);
+                        uint32_t k = 0;
+                        code = forward_unit<MX>(p, v, up, pl, c, n, scale, amax, k);
+                        scales[0] |= k << (8 * u);
                     }
                     codes |= (code & 0xFFu) << (8 * u);
                     codes_up |= (code >> 8) << (8 * u);
@@ -674,6 +692,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int j = 0; j < 32; j++) {
                         if (BWD) r[0][j] = r[1][j], r[1][j] = r[2][j], r[2][j] = r[3][j];
                         else r[0][j] = r[2][j], r[1][j] = r[3][j];
+                    }
+                }
+            }
+            if (!BWD && p.cq && pl.live && units && c0 < p.W) {  // the two units' scale bytes of gate, and of up
+                uint8_t *s = p.cs + pl.row * p.ld_cs + (c0 >> 5);
+                const bool two = c0 + 32 < p.W;
+#pragma unroll
+                for (int i = 0; i < 2; i++, s += p.W >> 5) {
+                    const uint32_t v = scales[0] >> (16 * i);
+                    if (two && p.cs4) {
+                        *reinterpret_cast<uint16_t *>(s) = (uint16_t)v;
+                    } else {
+                        s[0] = (uint8_t)v;
+                        if (two) s[1] = (uint8_t)(v >> 8);
                     }
                 }
             }
@@ -906,6 +938,7 @@ static fp8_status_t set_checkpoint(const void *q, int64_t ld_q, const void *s, i
     p.cs = static_cast<uint8_t *>(const_cast<void *>(s));
     p.ld_cq = ld_q;
     p.ld_cs = ld_s;
+    p.cs4 = aligned(s, 4) && ld_s % 4 == 0 && p.W % 128 == 0;
     p.cfmt = fmt;
     return FP8_OK;
 }

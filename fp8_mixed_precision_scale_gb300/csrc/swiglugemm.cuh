@@ -32,6 +32,7 @@ struct Params {
     uint8_t *cq, *cs;
     int64_t ld_cq, ld_cs;
     int cfmt;
+    int cs4;    // its scale bytes of four blocks stand on word boundaries
     int64_t W;  // columns of a part of the checkpoint
     // 8 bits
     int fmt;
