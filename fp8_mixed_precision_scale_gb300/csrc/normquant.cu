@@ -9,8 +9,15 @@
 //
 //   norm_quantize_rows  a row stays in the registers of its group of threads, as
 //                       in the norm's forward: sum, statistics, the row layout.
+//                       Bound by HBM: [8192, 4096] bf16, MX 38 us = 6.2 TB/s, [32768,
+//                       7168] with an fp32 residual 414 us = 6.3 TB/s.
 //   norm_quantize_cols  the transposed layout, whose blocks run over rows, from
-//                       the stored sum and the rows' statistics.
+//                       the stored sum and the rows' statistics: [8192, 4096] 24 us
+//                       (cold), [32768, 7168] fp32 231 us = 5.1 TB/s.
+// Two kernels, and the sum read once more: both layouts in one kernel, 32 rows in
+// the shared memory of a cluster, took 70 to 79 us for [8192, 4096] against 65, and
+// 920 against 652 for the fp32 one: 26 instructions an element instead of 13 + 11, and
+// phases that two or three blocks an SM do not hide.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -12,25 +12,38 @@
 // the next product, in either layout, or in bf16, and of gate | up what the
 // backward needs, in 8 bits or bf16.
 //
-// Design (GB300, sm_103a): persistent, warp-specialised, one CTA of 384 threads
-// per SM.
-//   warp 0     TMA producer: a 128 x 128-byte tile of A and two of B (forward:
-//              128 gate rows and the 128 up rows of the same columns of h) per
-//              stage of a four-stage ring, and for MX their scale blocks.
-//   warp 1     MMA issuer: M = 128, N = 256, K = 32; gate in accumulator columns
-//              0 .. 127, up in 128 .. 255, so that one thread of the epilogue
+// Design (GB300, sm_103a): persistent, warp-specialised, one CTA of 384 threads per
+// SM; from 129 rows on CTA pairs with 256 x 256 tiles from 2-SM MMAs, each CTA staging
+// its 128 rows of A and half of B (forward: the even one 128 gate rows, the odd one
+// the 128 up rows of the same columns of h).
+//   warp 0     TMA producer: the CTA's tiles of A and B, 128 bytes along K, per stage
+//              of a five-stage ring (three with a single CTA, which stages both halves
+//              of B), and for MX their scale blocks.
+//   warp 1     MMA issuer (the even CTA's): N = 256, K = 32; gate in accumulator
+//              columns 0 .. 127, up in 128 .. 255, so that one thread of the epilogue
 //              finds both of an element of h in its own TMEM lane.
 //   warp 2     MX: copies each stage's scale blocks into the stage's own TMEM
 //              columns, ahead of the MMA thread.
 //   warps 4-11 epilogue: warp w has TMEM lane quarter w % 4 (32 rows) and half of
-//              the columns.  A thread has one row: blocks of 32 columns, their
-//              maxima and codes need no other thread.  The transposed layout's
-//              blocks are 32 rows of a column, a warp's rows exactly: they go
+//              the columns, 32 at a time (a unit).  A thread has one row: blocks of 32
+//              columns, their maxima and codes need no other thread.  The transposed
+//              layout's blocks are 32 rows of a column, a warp's rows exactly: they go
 //              through the warp's shared-memory staging.
 // With per-row scales two accumulators overlap the epilogue and the next tile's
 // main loop.  MX scales take part of TMEM, which leaves one accumulator: each
 // epilogue thread first takes its 128 columns into registers and releases it.
 // For that the epilogue's warps take registers from the others (setmaxnreg).
+//
+// 8192 rows, K = 4096, F = 14336, MX, times of single calls in us: forward with h in bf16
+// 547 (3.52 PFLOP/s; the plain product of the same size 622), with both 8-bit layouts
+// and the 8-bit gate | up 596; backward from the 8-bit gate | up to both layouts 443.
+// The forward is bound by the tensor cores: a tile's MMAs take 11.0 us of 12.3.  The
+// backward is bound by its epilogue and by what it shares with the MMAs, the shared
+// memory's port: 14.1 us a tile by itself, 18.1 beside MMAs that take 11.4 by themselves.
+// Steps that carried it: a loop over the units in place of four copies (instructions
+// then stay in the cache: backward 1066 -> 549), no release at cluster scope when an
+// accumulator is handed back (it waited for the stores of the tile before: forward
+// 688 -> 599), the transposed layout 32 columns at once (backward 527 -> 452).
 // Every mbarrier wait is bounded (about 2 s); a wait that gives up records the
 // device error word, drains what is in flight, releases TMEM and returns.
 #include <cuda.h>
@@ -867,7 +880,10 @@ static fp8_status_t launch_as(const Operands &o, Params p, cudaStream_t st)
     return check_launch();
 }
 
-// Pairs from 129 rows on, as the plain products.
+// Pairs from 129 rows on, as the plain products.  MX forward, backward in us, pairs
+// against single CTAs: F = 14336, K = 4096 at 160 rows 36.7, 33.0 against 45.5, 35.6, at
+// 1024 rows 81.6, 72.5 against 110.2, 78.2; F = 2048, K = 7168 at 160 rows 27.2, 39.0
+// against 31.4, 41.6.
 template <bool MX, int KIND>
 static fp8_status_t launch(const Operands &o, const Params &p, void *stream)
 {
