@@ -12,11 +12,11 @@
 //                       Bound by HBM: [8192, 4096] bf16, MX 38 us = 6.2 TB/s, [32768,
 //                       7168] with an fp32 residual 414 us = 6.3 TB/s.
 //   norm_quantize_cols  the transposed layout, whose blocks run over rows, from
-//                       the stored sum and the rows' statistics: [8192, 4096] 24 us
-//                       (cold), [32768, 7168] fp32 231 us = 5.1 TB/s.
+//                       the stored sum and the rows' statistics: [8192, 4096] 21 us,
+//                       [32768, 7168] fp32 165 us = 7.2 TB/s (some of it from L2).
 // Two kernels, and the sum read once more: both layouts in one kernel, 32 rows in
-// the shared memory of a cluster, took 70 to 79 us for [8192, 4096] against 65, and
-// 920 against 652 for the fp32 one: 26 instructions an element instead of 13 + 11, and
+// the shared memory of a cluster, took 70 to 79 us for [8192, 4096] against 64, and
+// 920 against 613 for the fp32 one: 26 instructions an element instead of 13 + 11, and
 // phases that two or three blocks an SM do not hide.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -305,8 +305,11 @@ static __device__ __noinline__ void put_some(uint8_t *dst, uint4 lo, uint4 hi, i
     }
 }
 
+// Three blocks an SM; two of fp32, whose 64 registers of loads in flight would spill
+// ([32768, 7168] 207 against 165 us).  A persistent block that loads its next tile
+// under this one's columns took 27 us against 21 for [8192, 4096] bf16 (25 with two blocks).
 template <typename T, bool ANY>
-__global__ void __launch_bounds__(C_THREADS, 3) norm_quantize_cols(Args a)
+__global__ void __launch_bounds__(C_THREADS, sizeof(T) == 4 ? 2 : 3) norm_quantize_cols(Args a)
 {
     extern __shared__ __align__(16) float tile[];  // [CR][CC] xhat
     const T *src = static_cast<const T *>(a.res ? a.sum : a.x);
