@@ -423,9 +423,21 @@ static fp8_status_t launch_rows_kernel(const Plan &p, int smem, Args a, cudaStre
 template <typename TX, typename TR, bool ANY>
 static fp8_status_t launch_rows(const Args &a, cudaStream_t st)
 {
+    constexpr int narrow = rows_shared(2, 32, true), wide = rows_shared(2, NM_BLOCK, true);
+    // Unaligned fp32 rows take one chunk a thread: two need 42 registers more of words
+    // in flight, which spill ([16384, 4096] 240 against 167 us, bf16 + fp32 167 against 151;
+    // 16 bits do not spill).  Beyond what one chunk covers in a block they stay two: a
+    // cluster costs more ([8192, 14336] bf16 + fp32 346 against 431 us).
+    if constexpr (ANY && sizeof(TR) == 4) {
+        if (a.cols <= NM_PART) {
+            const Plan p = make_plan(a.rows, a.cols, 1);
+            const int smem = rows_shared(1, p.G, a.bias != nullptr);
+            if (p.multi) return launch_rows_kernel<norm_quantize_rows<TX, TR, 1, true, ANY, false>, wide>(p, smem, a, st);
+            return launch_rows_kernel<norm_quantize_rows<TX, TR, 1, false, ANY, false>, narrow>(p, smem, a, st);
+        }
+    }
     const Plan p = make_plan(a.rows, a.cols, 2);
     const int smem = rows_shared(p.chunks, p.G, a.bias != nullptr);
-    constexpr int narrow = rows_shared(2, 32, true), wide = rows_shared(2, NM_BLOCK, true);
     if (p.ranks > 1) return launch_rows_kernel<norm_quantize_rows<TX, TR, 2, true, ANY, true>, wide>(p, smem, a, st);
     if (p.chunks == 1)
         return launch_rows_kernel<norm_quantize_rows<TX, TR, 1, false, ANY, false>, narrow>(p, smem, a, st);
