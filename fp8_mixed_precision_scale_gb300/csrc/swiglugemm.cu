@@ -18,7 +18,7 @@
 // the 128 up rows of the same columns of h).
 //   warp 0     TMA producer: the CTA's tiles of A and B, 128 bytes along K, per stage
 //              of a five-stage ring (three with a single CTA, which stages both halves
-//              of B), and for MX their scale blocks.
+//              of B; with half as many columns five again), and for MX their scale blocks.
 //   warp 1     MMA issuer (the even CTA's): N = 256, K = 32; gate in accumulator
 //              columns 0 .. 127, up in 128 .. 255, so that one thread of the epilogue
 //              finds both of an element of h in its own TMEM lane.
@@ -63,7 +63,6 @@ namespace fp8gb {
 namespace sg {
 
 constexpr int BM = 128;  // rows of A a CTA stages, and of the result that it holds
-constexpr int BB = 128;  // rows of one box of B
 constexpr int BK = 128;
 constexpr int UMMA_K = 32;
 constexpr int EPI_WARPS = 8;
@@ -84,11 +83,17 @@ constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr int STAGE_PITCH = 36;
 constexpr int STAGE_WORDS = 32 * STAGE_PITCH;
 
-template <bool PAIR>
+// The three forms of a tile: CTA pairs, one CTA, and one CTA with half as many
+// columns (not for the MX forward, whose gate and up rows would start inside their
+// 128-row scale blocks).
+enum { PAIR = 0, SINGLE = 1, NARROW = 2 };
+
+template <int FORM>
 struct Smem {
-    static constexpr int stages = PAIR ? 5 : 3;
-    static constexpr int boxes = PAIR ? 1 : 2;  // of B a CTA stages
-    static constexpr int b_bytes = boxes * BB * BK;
+    static constexpr int half = FORM == NARROW ? 64 : 128;  // rows of one box of B, half a tile's columns of B
+    static constexpr int stages = FORM == SINGLE ? 3 : 5;
+    static constexpr int boxes = FORM == PAIR ? 1 : 2;      // of B a CTA stages
+    static constexpr int b_bytes = boxes * half * BK;
     static constexpr int a_off = 0;
     static constexpr int b_off = stages * A_BYTES;
     static constexpr int sfa_off = b_off + stages * b_bytes;
@@ -243,15 +248,17 @@ __device__ __forceinline__ void get_kept(const Params &p, const Place &t, int64_
     }
 }
 
-// Scale bytes of four blocks of a checkpoint's part from column c on, for the row.
+// Scale bytes of a warp's blocks of a checkpoint's part from column c on, for the row.
 // Every row is a line of its own, whatever is read of it: a word at a time.
+template <int UNITS>
 __device__ __forceinline__ uint32_t kept_scales(const Params &p, const Place &t, int64_t c, int part)
 {
     if (!t.live || c >= p.F) return 0;
     const uint8_t *s = p.cs + t.row * p.ld_cs + part * (p.W >> 5) + (c >> 5);
-    if (p.cs4) return __ldg(reinterpret_cast<const uint32_t *>(s));
+    if (p.cs4 && UNITS == 4) return __ldg(reinterpret_cast<const uint32_t *>(s));
+    if (p.cs4 && UNITS == 2) return __ldg(reinterpret_cast<const uint16_t *>(s));
     uint32_t v = 0;
-    for (int i = 0; i < 4 && c + 32 * i < p.W; i++) v |= (uint32_t)__ldg(s + i) << (8 * i);
+    for (int i = 0; i < UNITS && c + 32 * i < p.W; i++) v |= (uint32_t)__ldg(s + i) << (8 * i);
     return v;
 }
 
@@ -376,15 +383,15 @@ __device__ __forceinline__ uint32_t backward_unit(const Params &p, float (&g)[2]
     return codes;
 }
 
-template <bool MX, bool PAIR, int KIND>
+template <bool MX, int FORM, int KIND>
 __global__ void __launch_bounds__(THREADS, 1)
     swiglu_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                        const __grid_constant__ Params p, uint32_t idesc)
 {
-    using L = Smem<PAIR>;
-    constexpr int STAGES = L::stages;
-    constexpr bool BWD = KIND != FORWARD;
+    using L = Smem<FORM>;
+    constexpr int STAGES = L::stages, HALF = L::half;
+    constexpr bool BWD = KIND != FORWARD, PAIRED = FORM == PAIR;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sA = smem + L::a_off;
@@ -402,8 +409,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::slot_off);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = PAIR ? (int)cluster_ctarank() : 0;  // the even CTA leads
-    const int64_t first = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
+    const int rank = PAIRED ? (int)cluster_ctarank() : 0;  // the even CTA leads
+    const int64_t first = PAIRED ? blockIdx.x >> 1 : blockIdx.x, step = PAIRED ? gridDim.x >> 1 : gridDim.x;
     constexpr int ACCS = MX ? 1 : 2;
 
     if (warp == 0 && lane == 0) {
@@ -414,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], (PAIR ? 2 : 1) * EPI_WARPS);
+            mbar_init(&tempty[b], (PAIRED ? 2 : 1) * EPI_WARPS);
         }
         mbar_init(done, 1);
         mbar_init(sf_done, 1);
@@ -427,12 +434,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
     if (warp == 1) {
-        if (PAIR) tmem_alloc_pair(tmem_slot, TMEM_COLS);
+        if (PAIRED) tmem_alloc_pair(tmem_slot, TMEM_COLS);
         else tmem_alloc(tmem_slot, TMEM_COLS);
     }
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();  // both CTAs' barriers are initialised before any remote use
+    if (PAIRED) cluster_sync();  // both CTAs' barriers are initialised before any remote use
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
@@ -445,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mb = (int)(tt / (uint32_t)p.num_n);
             nb = (int)(tt - (uint32_t)mb * (uint32_t)p.num_n);
         }
-        if (PAIR) mb = 2 * mb + rank;  // this CTA's 128 rows
+        if (PAIRED) mb = 2 * mb + rank;  // this CTA's 128 rows
     };
     const int last_steps = (int)((p.K - (int64_t)(p.num_k - 1) * BK + UMMA_K - 1) / UMMA_K);
 
@@ -461,8 +468,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 coords(t, mb, nb);
                 const int32_t y = mb * BM;
                 // first rows of the tile's two boxes of B, and of their scales
-                const int32_t b0 = nb * (BWD ? 2 * BB : BB), b1 = BWD ? b0 + BB : p.b1_row + b0;
-                const int32_t s1 = BWD ? b0 + BB : p.b1_srow + b0;
+                const int32_t b0 = nb * (BWD ? 2 * HALF : HALF), b1 = BWD ? b0 + HALF : p.b1_row + b0;
+                const int32_t s1 = (BWD ? b0 + HALF : p.b1_srow + b0) & ~127;  // whole blocks (narrow: the first again)
                 for (int kb = 0; kb < p.num_k; kb++) {
                     if (!mbar_wait_bounded(&empty[stage], phase ^ 1, WAIT_LIMIT_NS, p.err, ERR_PRODUCER_WAIT)) {
                         ok = false;
@@ -471,7 +478,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     constexpr uint32_t bytes = A_BYTES + L::b_bytes + (MX ? 3 * SF_BLOCK : 0);
                     uint8_t *a = sA + stage * A_BYTES, *b = sB + stage * L::b_bytes;
                     uint8_t *fa = sfa + stage * SF_BLOCK, *fb = sfb + stage * 2 * SF_BLOCK;
-                    if constexpr (PAIR) {  // both CTAs' copies count on the even one's barrier
+                    if constexpr (PAIRED) {  // both CTAs' copies count on the even one's barrier
                         if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
                         const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
                         tma_load_2d_pair(a, &tmA, kb * BK, y, bar);
@@ -485,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         mbar_arrive_expect_tx(&full[stage], bytes);
                         tma_load_2d(a, &tmA, kb * BK, y, &full[stage]);
                         tma_load_2d(b, &tmB, kb * BK, b0, &full[stage]);
-                        tma_load_2d(b + BB * BK, &tmB, kb * BK, b1, &full[stage]);
+                        tma_load_2d(b + HALF * BK, &tmB, kb * BK, b1, &full[stage]);
                         if (MX) {
                             tma_load_2d(fa, &tmSA, y, kb, &full[stage]);
                             tma_load_2d(fb, &tmSB, b0, kb, &full[stage]);
@@ -515,7 +522,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int64_t t = first; t < p.tiles && ok; t += step) {
                 if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, WAIT_LIMIT_NS, p.err, ERR_MMA_WAIT)) break;
                 tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(acc * 2 * BB);
+                const uint32_t d = tmem_base + (uint32_t)(acc * 2 * HALF);
                 for (int kb = 0; kb < p.num_k; kb++) {
                     if (!mbar_wait_bounded(MX ? &sf_full[stage] : &full[stage], phase, WAIT_LIMIT_NS, p.err,
                                            ERR_MMA_WAIT)) {
@@ -529,9 +536,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const auto mma = [&](int k) {  // K = 32: the descriptors' addresses are in 16 bytes
                         const uint64_t a = ad + k * (UMMA_K >> 4), b = bd + k * (UMMA_K >> 4);
                         const uint32_t id = MX ? idesc_sf_ids(idesc, (uint32_t)k, (uint32_t)k) : idesc;
-                        if constexpr (MX && PAIR) mma_mxf8f6f4_pair(d, a, b, id, ca, cb, (kb | k) != 0);
+                        if constexpr (MX && PAIRED) mma_mxf8f6f4_pair(d, a, b, id, ca, cb, (kb | k) != 0);
                         else if constexpr (MX) mma_mxf8f6f4(d, a, b, id, ca, cb, (kb | k) != 0);
-                        else if constexpr (PAIR) mma_f8f6f4_pair(d, a, b, id, (kb | k) != 0);
+                        else if constexpr (PAIRED) mma_f8f6f4_pair(d, a, b, id, (kb | k) != 0);
                         else mma_f8f6f4(d, a, b, id, (kb | k) != 0);
                     };
                     if (kb < p.num_k - 1 || last_steps == BK / UMMA_K) {
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     } else {
                         for (int k = 0; k < last_steps; k++) mma(k);
                     }
-                    if (PAIR) mma_commit_pair(&empty[stage], 0x3);
+                    if (PAIRED) mma_commit_pair(&empty[stage], 0x3);
                     else mma_commit(&empty[stage]);
                     if (++stage == STAGES) {
                         stage = 0;
@@ -548,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 if (!ok) break;
-                if (PAIR) mma_commit_pair(&tfull[acc], 0x3);
+                if (PAIRED) mma_commit_pair(&tfull[acc], 0x3);
                 else mma_commit(&tfull[acc]);
                 if (++acc == ACCS) {
                     acc = 0;
@@ -556,7 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             // all issued MMAs complete before TMEM is released
-            if (PAIR) mma_commit_pair_local(done);
+            if (PAIRED) mma_commit_pair_local(done);
             else mma_commit(done);
             mbar_wait_bounded(done, 0, WAIT_LIMIT_NS, p.err, ERR_TEARDOWN_WAIT);
         } else if (MX && warp == 2 && lane == 0 && rank == 0) {
@@ -573,7 +580,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc_fence_after();
                     const uint32_t ca = tmem_base + SFA_COL + 4 * stage, cb = tmem_base + SFB_COL + 8 * stage;
                     const uint32_t ra = smem_u32(sfa + stage * SF_BLOCK), rb = smem_u32(sfb + stage * 2 * SF_BLOCK);
-                    if constexpr (PAIR) {
+                    if constexpr (PAIRED) {
                         tmem_cp_32x128b_x4_pair(ca, smem_desc_sf(ra));
                         tmem_cp_32x128b_x4_pair(cb, smem_desc_sf(rb));
                         tmem_cp_32x128b_x4_pair(cb + 4, smem_desc_sf(rb + SF_BLOCK));
@@ -591,7 +598,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             // every issued copy lands before TMEM is released
-            if (PAIR) mma_commit_pair_local(sf_done);
+            if (PAIRED) mma_commit_pair_local(sf_done);
             else mma_commit(sf_done);
             mbar_wait_bounded(sf_done, 0, WAIT_LIMIT_NS, p.err, ERR_TEARDOWN_WAIT);
         }
@@ -602,7 +609,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         Place pl;
         pl.lane = lane;
         pl.stage = reinterpret_cast<float *>(smem + L::stage_off) + (warp - EPI_FIRST) * STAGE_WORDS;
-        constexpr int UNITS = BWD ? 4 : 2;
+        constexpr int UNITS = (BWD ? 2 * HALF : HALF) / 64;  // of 32 columns, a warp: it has half of the tile's
         float scale = 1.0f, amax = 0.0f;
         if (!MX && p.scale_in) {
             scale = __ldg(p.scale_in);
@@ -616,7 +623,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             pl.row0 = (int64_t)mb * BM + q * 32;
             pl.row = pl.row0 + lane;
             pl.live = pl.row < p.M;
-            const int64_t c0 = (int64_t)nb * (BWD ? 2 * BB : BB) + hb * 32 * UNITS;  // this warp's columns of h
+            const int64_t c0 = (int64_t)nb * (BWD ? 2 * HALF : HALF) + hb * 32 * UNITS;  // this warp's columns of h
             const auto columns = [&](int u) {  // that the data has in unit u
                 const int64_t n = p.F - c0 - 32 * u;
                 return (int)(n < 0 ? 0 : n < 32 ? n : 32);
@@ -629,13 +636,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t scales[2] = {};
             if constexpr (BWD) get_kept<KIND>(p, pl, c0, columns(0), kept);
             if constexpr (KIND == BACKWARD_CKPT) {
-                scales[0] = kept_scales(p, pl, c0, 0);
-                scales[1] = kept_scales(p, pl, c0, 1);
+                scales[0] = kept_scales<UNITS>(p, pl, c0, 0);
+                scales[1] = kept_scales<UNITS>(p, pl, c0, 1);
             }
             if (!mbar_wait_bounded(&tfull[acc], acc_phase, WAIT_LIMIT_NS, p.err, ERR_EPILOGUE_WAIT)) break;
             tc_fence_after();
             // accumulator column of the warp's first unit (forward: gate's; up's is 128 further)
-            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 2 * BB + hb * 32 * UNITS);
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 2 * HALF + hb * 32 * UNITS);
             const auto release = [&]() {
                 tmem_ld_wait();
                 tc_fence_before();
@@ -643,18 +650,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) {
                     // only TMEM is handed over: a release at cluster scope would wait for the stores
                     // of the tile before (2 us a tile)
-                    if (PAIR)
+                    if (PAIRED)
                         asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
                                          mapa_shared(smem_u32(&tempty[acc]), 0))
                                      : "memory");
                     else mbar_arrive(&tempty[acc]);
                 }
             };
-            uint32_t r[MX ? 4 : BWD ? 1 : 2][32];  // forward: gate and up of a unit, then of the next
+            constexpr int R = MX ? (BWD ? UNITS : 2 * UNITS) : BWD ? 1 : 2;
+            uint32_t r[R][32];  // forward: gate and up of a unit, then of the next
             if constexpr (MX) {
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    tmem_ld_32x32b_x32(BWD ? taddr + 32 * i : taddr + 32 * (i >> 1) + (i & 1) * BB, r[i]);
+                for (int i = 0; i < R; i++)
+                    tmem_ld_32x32b_x32(BWD ? taddr + 32 * i : taddr + 32 * (i >> 1) + (i & 1) * HALF, r[i]);
                 release();
             }
             uint32_t codes = 0, codes_up = 0;
@@ -665,7 +673,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int n = columns(u);
                 if constexpr (!MX) {
                     tmem_ld_32x32b_x32(taddr + 32 * u, r[0]);
-                    if (!BWD) tmem_ld_32x32b_x32(taddr + 32 * u + BB, r[BWD ? 0 : 1]);
+                    if (!BWD) tmem_ld_32x32b_x32(taddr + 32 * u + HALF, r[BWD ? 0 : 1]);
                     if (u == UNITS - 1) release();
                     else tmem_ld_wait();
                 }
@@ -688,7 +696,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         scales[0] >>= 8, scales[1] >>= 8;
                     } else {
                         float up[2][16];
-                        from_acc<MX>(r[1], sa, cu, p.sb_row, up);
+                        from_acc<MX>(r[R > 1 ? 1 : 0], sa, cu, p.sb_row, up);
                         if (n < 32 || pl.row0 + 32 > p.M) {
                             mask32(v, pl.live, n);
                             mask32(up, pl.live, n);
@@ -702,15 +710,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if constexpr (MX) {  // the next unit's accumulators
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        if (BWD) r[0][j] = r[1][j], r[1][j] = r[2][j], r[2][j] = r[3][j];
-                        else r[0][j] = r[2][j], r[1][j] = r[3][j];
-                    }
+                    for (int i = 0; i + (BWD ? 1 : 2) < R; i++)
+#pragma unroll
+                        for (int j = 0; j < 32; j++) r[i][j] = r[i + (BWD ? 1 : 2)][j];
                 }
             }
-            if (!BWD && p.cq && pl.live && units && c0 < p.W) {  // the two units' scale bytes of gate, and of up
+            if (!BWD && p.cq && pl.live && units && c0 < p.W) {  // the units' scale bytes of gate, and of up
                 uint8_t *s = p.cs + pl.row * p.ld_cs + (c0 >> 5);
-                const bool two = c0 + 32 < p.W;
+                const bool two = UNITS == 2 && c0 + 32 < p.W;
 #pragma unroll
                 for (int i = 0; i < 2; i++, s += p.W >> 5) {
                     const uint32_t v = scales[0] >> (16 * i);
@@ -722,17 +729,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            if (MX && units && p.q_row) {
-                // the row's scale bytes of its columns: a whole word of the layout, or the forward's half
-                const int64_t w = mx_scale_word(c0 >> 7, pl.row, p.rs_row);
-                if constexpr (BWD) {
-                    if (c0 < p.Fr) {
-                        reinterpret_cast<uint32_t *>(p.s_row)[w] = codes;
-                        reinterpret_cast<uint32_t *>(p.s_row)[w + (p.Fr >> 7) * p.rs_row] = codes_up;
-                    }
-                } else {
-                    reinterpret_cast<uint16_t *>(p.s_row)[2 * w + hb] = (uint16_t)codes;
-                }
+            if (MX && units && p.q_row && (!BWD || c0 < p.Fr)) {
+                // the row's scale bytes of its columns: a word of the layout, or a part of one
+                const int64_t at = 4 * mx_scale_word(c0 >> 7, pl.row, p.rs_row) + (c0 >> 5 & 3);
+                const auto put = [&](uint8_t *dst, uint32_t v) {
+                    if (UNITS == 4) *reinterpret_cast<uint32_t *>(dst) = v;
+                    else if (UNITS == 2) *reinterpret_cast<uint16_t *>(dst) = (uint16_t)v;
+                    else *dst = (uint8_t)v;
+                };
+                put(p.s_row + at, codes);
+                if (BWD) put(p.s_row + at + 4 * (p.Fr >> 7) * p.rs_row, codes_up);
             }
             if (MX && BWD && units && p.q_col && hb == 0 && nb == p.num_n - 1)  // scale rows behind the data
                 for (int64_t i = 2 * p.F + lane; i < p.rs_col; i += 32)
@@ -750,11 +756,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();  // no CTA leaves while its peer may still touch its shared memory or TMEM
+    if (PAIRED) cluster_sync();  // no CTA leaves while its peer may still touch its shared memory or TMEM
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        if (PAIR) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        if (PAIRED) tmem_dealloc_pair(tmem_base, TMEM_COLS);
         else tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
@@ -781,14 +787,14 @@ static EncodeTiledFn get_encode_fn()
 }
 
 // 2D map over a row-major u8 matrix [rows][ld] of `cols` columns, box {128
-// bytes, 128 rows}, 128-byte swizzle, zero fill out of bounds.
-static bool make_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld)
+// bytes, box_rows}, 128-byte swizzle, zero fill out of bounds.
+static bool make_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows)
 {
     EncodeTiledFn enc = get_encode_fn();
     if (!enc) return false;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)ld};
-    cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)BB};
+    cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -814,7 +820,7 @@ static bool make_scale_map(CUtensorMap *map, const void *base, int64_t kt, int64
 
 // Lets a kernel's launches take their shared memory, and gives the pairs (or
 // blocks) that run at once; asked once per device.  0: it failed.
-template <auto KERNEL, bool PAIR>
+template <auto KERNEL, int FORM>
 static int at_once()
 {
     constexpr int MAX_DEVICES = 64;
@@ -823,10 +829,10 @@ static int at_once()
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return 0;
     int n = known[dev].load(std::memory_order_acquire);
     if (n > 0) return n;
-    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<PAIR>::bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<FORM>::bytes) != cudaSuccess)
         return 0;
     n = num_sms();
-    if (PAIR) {
+    if (FORM == PAIR) {
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = 2;
@@ -834,7 +840,7 @@ static int at_once()
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(num_sms() / 2 * 2));
         cfg.blockDim = dim3(THREADS);
-        cfg.dynamicSmemBytes = Smem<PAIR>::bytes;
+        cfg.dynamicSmemBytes = Smem<FORM>::bytes;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess || n < 1) {
@@ -846,12 +852,14 @@ static int at_once()
     return n;
 }
 
-template <bool MX, bool PAIR, int KIND>
+template <bool MX, int FORM, int KIND>
 static fp8_status_t launch_as(const Operands &o, Params p, cudaStream_t st)
 {
+    using L = Smem<FORM>;
     CUtensorMap ma, mb, msa = {}, msb = {};
-    if (!make_map(&ma, o.A, p.M, p.K, o.lda) || !make_map(&mb, o.B, o.b_rows, p.K, o.ldb)) return FP8_ERR_CUDA;
-    constexpr int rows = PAIR ? 2 * BM : BM, cols = KIND == FORWARD ? BB : 2 * BB;  // of a tile of h
+    if (!make_map(&ma, o.A, p.M, p.K, o.lda, BM) || !make_map(&mb, o.B, o.b_rows, p.K, o.ldb, L::half))
+        return FP8_ERR_CUDA;
+    constexpr int rows = FORM == PAIR ? 2 * BM : BM, cols = KIND == FORWARD ? L::half : 2 * L::half;  // of a tile of h
     p.num_m = (int)((p.M + rows - 1) / rows);
     p.num_n = (int)((p.F + cols - 1) / cols);
     p.num_k = (int)((p.K + BK - 1) / BK);
@@ -861,36 +869,50 @@ static fp8_status_t launch_as(const Operands &o, Params p, cudaStream_t st)
     p.tiles = (int64_t)p.num_m * p.num_n;
     if (p.tiles > INT32_MAX) return FP8_ERR_UNSUPPORTED;
     p.err = device_error_word();
-    constexpr auto kernel = swiglu_gemm_kernel<MX, PAIR, KIND>;
-    const int most = at_once<kernel, PAIR>();
+    constexpr auto kernel = swiglu_gemm_kernel<MX, FORM, KIND>;
+    const int most = at_once<kernel, FORM>();
     if (!most) return cuda_fail();
-    const uint32_t idesc = MX ? idesc_mxf8f6f4(o.fa, o.fb, rows, 2 * BB) : idesc_f8f6f4(o.fa, o.fb, rows, 2 * BB);
+    constexpr int n = 2 * L::half;  // columns of an MMA
+    const uint32_t idesc = MX ? idesc_mxf8f6f4(o.fa, o.fb, rows, n) : idesc_f8f6f4(o.fa, o.fb, rows, n);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.tiles < most ? p.tiles : most) * (PAIR ? 2 : 1)));
+    cfg.gridDim = dim3((unsigned)((p.tiles < most ? p.tiles : most) * (FORM == PAIR ? 2 : 1)));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = Smem<PAIR>::bytes;
+    cfg.dynamicSmemBytes = L::bytes;
     cfg.stream = st;
     cfg.attrs = &attr;
-    cfg.numAttrs = PAIR;
+    cfg.numAttrs = FORM == PAIR;
     cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, p, idesc);
     return check_launch();
 }
 
-// Pairs from 129 rows on, as the plain products.  MX forward, backward in us, pairs
+// Pairs from 129 rows on, as the plain products: MX forward, backward in us, pairs
 // against single CTAs: F = 14336, K = 4096 at 160 rows 36.7, 33.0 against 45.5, 35.6, at
 // 1024 rows 81.6, 72.5 against 110.2, 78.2; F = 2048, K = 7168 at 160 rows 27.2, 39.0
-// against 31.4, 41.6.
+// against 31.4, 41.6.  Narrow tiles where all of them run at once: more SMs share the
+// columns, and a tile's epilogue is half as long (F = 2048: backward of K = 128, 96 rows
+// 15.4 against 9.7 us, K = 7168 37.4 against 26.6, 512 rows 39.5 against 32.7;
+// forward with per-row scales, K = 128 7.7 against 5.6, K = 7168 23.1 against 21.0).
 template <bool MX, int KIND>
 static fp8_status_t launch(const Operands &o, const Params &p, void *stream)
 {
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     fp8_status_t rc;
     if (KIND == FORWARD && few_rows(o, p, MX, st, rc)) return rc;
-    return p.M > BM ? launch_as<MX, true, KIND>(o, p, st) : launch_as<MX, false, KIND>(o, p, st);
+    if constexpr (!MX || KIND != FORWARD) {
+        constexpr int cols = KIND == FORWARD ? 64 : 128;
+        if ((p.M + BM - 1) / BM * ((p.F + cols - 1) / cols) <= num_sms()) return launch_as<MX, NARROW, KIND>(o, p, st);
+    }
+    // The MX forward of few rows: a pair's CTAs fetch half of B each, which a long
+    // contraction is bound by, while twice the CTAs still run at once. One CTA a tile against
+    // a pair, 96 rows, F = 2048, one layout: K = 7168 28.2 and 24.1 us, K = 4096 18.5 and
+    // 16.9, K = 1024 9.2 and 9.2 (both layouts 10.8 and 11.3), K = 128 6.7 and 7.2. With 112
+    // tiles (F = 14336, K = 4096, 16 rows), more than half of the SMs: 32.8 and 38.4.
+    const bool halves = MX && KIND == FORWARD && p.K >= 2048 && (p.F + 127) / 128 <= num_sms() / 2;
+    return p.M > BM || halves ? launch_as<MX, PAIR, KIND>(o, p, st) : launch_as<MX, SINGLE, KIND>(o, p, st);
 }
 
 template <bool MX>

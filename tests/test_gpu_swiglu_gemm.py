@@ -137,9 +137,12 @@ def backward(dy, wd, kept, o):
 
 
 MX_SIZES = [(1, 32, 32), (5, 96, 64), (32, 64, 160), (64, 128, 128), (96, 160, 96), (127, 192, 288), (128, 256, 512),
-            (129, 32, 128), (160, 288, 544), (288, 416, 1056), (257, 512, 96), (3, 1504, 2048)]
+            (129, 32, 128), (160, 288, 544), (288, 416, 1056), (257, 512, 96), (3, 1504, 2048),
+            # enough tiles for CTA pairs (forward, backward too), and for wide tiles of few rows
+            (1312, 928, 96), (2592, 928, 160), (1301, 928, 64), (96, 9760, 64), (64, 19488, 96),
+            (96, 288, 2080), (41, 128, 2048)]  # a pair's second rows empty
 SIZES = [(1, 16, 16), (4, 48, 80), (33, 112, 128), (128, 128, 256), (130, 144, 272), (300, 400, 1040), (513, 272, 48),
-         (2, 720, 2064)]
+         (2, 720, 2064), (1301, 944, 80), (2600, 944, 48), (100, 9744, 64), (77, 19472, 48)]
 
 
 def sizes(mx):
