@@ -118,6 +118,15 @@ __device__ __forceinline__ uint4 ld_stream_16b(const void *p)
     return v;
 }
 
+// The same of memory that another kernel may have written while this one was there
+// (before its griddepcontrol.wait, which as asm volatile stays ahead of this).
+__device__ __forceinline__ void ld_32b(const void *p, uint4 &lo, uint4 &hi)
+{
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w)
+                 : "l"(p));
+}
+
 __device__ __forceinline__ uint4 ld_shared_16b(uint32_t p)
 {
     uint4 v;

@@ -305,6 +305,37 @@ static __device__ __noinline__ void put_some(uint8_t *dst, uint4 lo, uint4 hi, i
     }
 }
 
+// 16 elements that the kernel before wrote (zeros if not `have`).  This kernel starts
+// before that one ends, so its loads are the coherent ones: not load_chunk's, which
+// want data that nobody writes while the kernel lives.
+template <typename T, bool ANY>
+__device__ __forceinline__ void load_written(const T *p, bool have, bool w32, int64_t at, int64_t end, Raw<T, ANY> &raw)
+{
+    if constexpr (ANY) {
+        if (have && well_inside(at, end)) {
+            const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+            const uint4 *w = reinterpret_cast<const uint4 *>(from & ~(uintptr_t)15);
+            raw.shift = (uint32_t)from & 15u;
+#pragma unroll
+            for (int j = 0; j <= (int)sizeof(T); j++) raw.v[j] = w[j];
+        } else {
+            load16(p, have ? 16 : 0, false, raw);  // element by element
+        }
+    } else {
+        const uint4 *w = reinterpret_cast<const uint4 *>(p);
+        if (!have) {
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T); j++) raw.v[j] = make_uint4(0, 0, 0, 0);
+        } else if (w32) {
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T); j += 2) ld_32b(w + j, raw.v[j], raw.v[j + 1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T); j++) raw.v[j] = w[j];
+        }
+    }
+}
+
 // Three blocks an SM; two of fp32, whose 64 registers of loads in flight would spill
 // ([32768, 7168] 207 against 165 us).  A persistent block that loads its next tile
 // under this one's columns took 27 us against 21 for [8192, 4096] bf16 (25 with two blocks).
@@ -337,7 +368,7 @@ __global__ void __launch_bounds__(C_THREADS, sizeof(T) == 4 ? 2 : 3) norm_quanti
         const int k = lr + i * STEP;
         const int64_t at = (r0 + k) * ld + col0 + lc;
         const bool live = k < left;
-        load_chunk<ANY>(src + at, live && in ? 16 : 0, a.w32, at, end, raw[i]);
+        load_written<T, ANY>(src + at, live && in, a.w32, at, end, raw[i]);
         rs[i] = live ? a.rstd[r0 + k] : 0.0f;
         mm[i] = live && !a.rms ? -a.mean[r0 + k] : 0.0f;
     }
