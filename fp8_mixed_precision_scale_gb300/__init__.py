@@ -1142,8 +1142,9 @@ def norm_quantize(x: torch.Tensor, residual=None, weight=None, bias=None, kind: 
                   fmt: int = E4M3FN, recipe: Recipe | None = None, layouts: int = LAYOUT_ROW, scale_in=None,
                   amax_out=None, out=None, stream=None) -> NormQuantize:
     """sum = x + residual (stored, in the residual's type: x's or fp32), its layer
-    or RMS norm, and that in 8 bits, in one read.  recipe: ROWWISE (the default;
-    one scale per row, row layout) or DELAYED (scale_in, amax_out; either layout)."""
+    or RMS norm, and that in 8 bits, in one read.  out receives the sum, not in
+    place of an input.  recipe: ROWWISE (the default; one scale per row, row layout)
+    or DELAYED (scale_in, amax_out; either layout)."""
     if stream is not None:
         with _on(stream):
             return norm_quantize(x, residual, weight, bias, kind, eps, fmt, recipe, layouts, scale_in, amax_out, out)

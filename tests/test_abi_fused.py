@@ -157,3 +157,29 @@ def test_swiglu_gemm_validation(lib, mx, back):
         assert c(layouts=0) == INVALID            # nothing to write
     else:
         assert c(layouts=0) == INVALID
+
+
+IN = 0x40000  # apart from FAKE
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_outputs_that_start_where_an_input_does(lib, mx):
+    if mx:
+        c = caller(lib, "fp8_mx_norm_quantize", NORM_ORDER + "layouts q sr qt ld_t sc stream", NORM)
+    else:
+        c = caller(lib, "fp8_norm_quantize", NORM_ORDER + "recipe layouts scale amax q sr qt ld_t sc stream", NORM)
+    assert c(x=IN, res=FAKE, sum=FAKE) == INVALID
+    assert c(x=FAKE, res=IN, sum=FAKE) == INVALID
+    name, order = BACKWARD[mx]
+    c = caller(lib, name, order, dict(BACK, gu=IN, d=IN, ld_d=128, layouts=0))
+    assert c() == INVALID
+
+
+@pytest.mark.parametrize("same", ["dy", "x", "dsum"])
+def test_residual_norm_backward_in_place(lib, same):
+    base = dict(dy=IN, yt=0, ld_dy=64, x=2 * IN, ld_x=64, q=None, ld_q=0, s=None, ld_s=0, fmt=0, dsum=3 * IN, ld_d=64,
+                rows=4, cols=64, kind=1, mean=None, rstd=FAKE, w=FAKE, wt=0, dx=FAKE, xt=0, ld_dx=64, dw=None, db=None,
+                ws=None, wsb=0, stream=None)
+    c = caller(lib, "fp8_residual_norm_backward", "dy yt ld_dy x ld_x q ld_q s ld_s fmt dsum ld_d rows cols kind mean "
+               "rstd w wt dx xt ld_dx dw db ws wsb stream", base)
+    assert c(**{same: FAKE}) == INVALID
