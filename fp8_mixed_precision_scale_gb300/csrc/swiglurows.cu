@@ -4,18 +4,20 @@
 //
 // With one row or two the weights are read once and little else is done, so HBM
 // bounds the call from below: 2 F K bytes.  A 128-row tensor-core tile of 128
-// columns gives few SMs work and reads 128-byte pieces of 256 rows; here a warp reads 512 consecutive bytes of a row
-// and goes along it.  A block has 32 columns of h, the width of an MX block, and
-// each of its eight warps four of them: eight rows of W at a time, a row's next
-// step asked for when this one's has been taken.  A in fp32 with its block scales (exact),
-// in shared memory; each W code is exact in fp16 and fp32; fp32 sums, a W block's
-// scale applied to the sum of 16 products.
+// columns gives few SMs work and reads 128-byte pieces of 256 rows; here a warp reads
+// 512 consecutive bytes of a row and goes along it.  A block has 32 columns of h, the
+// width of an MX block, and each of its eight warps four of them: eight rows of W at a
+// time, a row's next step asked for when this one's has been taken.  A in fp32 with its
+// block scales (exact), in shared memory; each W code is exact in fp16 and fp32; fp32
+// sums, a W block's scale applied to the sum of 16 products.
 //
-// MX, one row, in a graph (tensor-core tiles in brackets): F = 14336, K = 4096 33.7 us
-// = 3.6 TB/s (35.3); F = 2048, K = 7168 24.0 us (33.0); F = 1504, K = 4096 13.1 us (20.6).
-// Bound by the conversions of the codes as much as by memory: 4.2 instructions a
-// weight in 45 % of the issue slots, of which 1.5 convert.  A second row adds 2 to 5
-// us; from three rows on the tiles are as fast.
+// MX, one row, in a graph: F = 14336, K = 4096 33.7 us = 3.6 TB/s; F = 2048, K = 7168
+// 24.0 us; F = 1504, K = 4096 13.6 us.  Bound by the conversions of the codes as much as
+// by memory: 4.2 instructions a weight in 45 % of the issue slots, of which 1.5 convert.
+// Two rows, this against the tiles (F, K): scaled 32.8 and 36.9 (14336, 4096), 24.0 and
+// 22.8 (2048, 7168), 13.8 and 16.4 (1504, 4096), 36.4 and 45.1 (8192, 8192); MX 38.5 and
+// 35.5 to 37.4, 30.0 and 27.3, 16.5 and 18.6, 43.1 and 40.4 to 42.6: two rows of scaled
+// operands come here, of MX operands one.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -222,7 +224,7 @@ static fp8_status_t launch(const RowArgs &o, const Params &p, unsigned grid, int
 
 bool few_rows(const Operands &o, const Params &p, bool mx, cudaStream_t st, fp8_status_t &rc)
 {
-    if (p.M > FR_MOST) return false;
+    if (p.M > (mx ? 1 : FR_MOST)) return false;
     const int mt = (int)p.M;
     const int64_t steps = (p.K + FR_STEP - 1) / FR_STEP, smem = mt * steps * FR_STEP * (int64_t)sizeof(float);
     // MX with the transposed layout has 32 rows at least
@@ -232,8 +234,7 @@ bool few_rows(const Operands &o, const Params &p, bool mx, cudaStream_t st, fp8_
                     o.lda, o.ldb, o.rsA, o.rsB, o.fa, o.fb};
     // MX: the scale bytes of the columns up to whole K tiles of the next product too
     const unsigned grid = (unsigned)((mx ? round_up_128(p.F) : p.F + FR_COLS - 1) / FR_COLS);
-    if (mx) rc = mt == 1 ? launch<swiglu_rows_kernel<true, 1>>(r, p, grid, (int)smem, st)
-                         : launch<swiglu_rows_kernel<true, 2>>(r, p, grid, (int)smem, st);
+    if (mx) rc = launch<swiglu_rows_kernel<true, 1>>(r, p, grid, (int)smem, st);
     else rc = mt == 1 ? launch<swiglu_rows_kernel<false, 1>>(r, p, grid, (int)smem, st)
                       : launch<swiglu_rows_kernel<false, 2>>(r, p, grid, (int)smem, st);
     return true;
