@@ -13,7 +13,8 @@
 // backward needs, in 8 bits or bf16.
 //
 // Design (GB300, sm_103a): persistent, warp-specialised, one CTA of 384 threads per
-// SM; from 129 rows on CTA pairs with 256 x 256 tiles from 2-SM MMAs, each CTA staging
+// SM; from 129 rows on (and for some MX forwards of fewer, at the launch) CTA pairs
+// with 256 x 256 tiles from 2-SM MMAs, each CTA staging
 // its 128 rows of A and half of B (forward: the even one 128 gate rows, the odd one
 // the 128 up rows of the same columns of h).
 //   warp 0     TMA producer: the CTA's tiles of A and B, 128 bytes along K, per stage
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             // copies in flight land before the block ends: the last of stage s is of
-            // this round for the stages before `stage`, of the round before for the others.
+            // this turn of the ring for the stages before `stage`, of the one before for the others.
             // The even CTA's barriers count both CTAs' (the odd one waits at the end)
             if (rank == 0)
                 for (int s = 0; s < STAGES; s++)
