@@ -393,20 +393,20 @@ __global__ void __launch_bounds__(C_THREADS, sizeof(T) == 4 ? 2 : 3) norm_quanti
         float v[2][16];
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-            // w = b = 0 behind the last column, where what the load left is 0
+            // behind the last column w = b = 0: 0, or NaN beside a row whose statistics are not finite
             const float2 y = fma2(make_float2(from[j * CC], from[(j + 1) * CC]), make_float2(w, w),
                                   make_float2(b, b));
             v[j >> 4][j & 15] = y.x, v[j >> 4][(j & 15) + 1] = y.y;
         }
         float inv = scale;
-        if (a.recipe == MX) {  // whole blocks of 32 rows; zeros behind the data
+        if (a.recipe == MX) {  // whole blocks of 32 rows; zeros behind the data, whatever stands there
             float m = 0.0f, o = 0.0f;
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
                 m = max3_abs(m, v[0][j], v[0][j + 1]);
                 o = max3_abs(o, v[1][j], v[1][j + 1]);
             }
-            const uint32_t code = n > 0 ? mx_code_of(__float_as_uint(max_nan(m, o)), a.fmt) : 0u;
+            const uint32_t code = column && n > 0 ? mx_code_of(__float_as_uint(max_nan(m, o)), a.fmt) : 0u;
             inv = mx_inv_scale(code);
             s[rb] = (uint8_t)code;
         }
