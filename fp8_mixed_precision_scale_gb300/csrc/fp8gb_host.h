@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "fp8gb.h"
 
 namespace fp8gb {
@@ -27,5 +29,13 @@ inline fp8_status_t check_launch()
 }
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// An output that starts where an input does would be read while it is written.
+inline bool starts_at_any(const void *out, std::initializer_list<const void *> inputs)
+{
+    for (const void *p : inputs)
+        if (out && p == out) return true;
+    return false;
+}
 
 }  // namespace fp8gb

@@ -633,7 +633,7 @@ static fp8_status_t norm_backward(const void *dy, int y_dtype, int64_t ld_dy, co
         if (!rstd || (x && kind == FP8_NORM_LAYER && !mean)) return FP8_ERR_INVALID_ARG;
         rc = x ? check_tensor(x, x_dtype, ld_x, cols) : check_codes(q, ld_q, s, ld_s, cols);
         if (rc != FP8_OK) return rc;
-        if (RES && (dx == dsum || dx == dy || dx == x)) return FP8_ERR_INVALID_ARG;  // read while it is written
+        if (RES && starts_at_any(dx, {dy, x, q, s, dsum, mean, rstd, weight})) return FP8_ERR_INVALID_ARG;
     }
     NormArgs a{};
     a.dy = dy;

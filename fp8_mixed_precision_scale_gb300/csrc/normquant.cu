@@ -570,7 +570,7 @@ static fp8_status_t run(Args a, int x_dtype, int r_dtype, int kind, int layouts,
     }
     if (a.recipe == DELAYED && (!a.scale_in || !a.amax_out)) return FP8_ERR_INVALID_ARG;
     if (!aligned(a.scale_in, 4) || !aligned(a.amax_out, 4)) return FP8_ERR_ALIGNMENT;
-    if (a.res && (a.sum == a.res || a.sum == a.x)) return FP8_ERR_INVALID_ARG;  // read while it is written
+    if (a.res && starts_at_any(a.sum, {a.x, a.res, a.weight, a.bias, a.scale_in})) return FP8_ERR_INVALID_ARG;
     a.rms = kind == FP8_NORM_RMS;
     a.rs_row = round_up_128(rows);
     a.rs_col = round_up_128(cols);

@@ -1127,7 +1127,7 @@ extern "C" fp8_status_t fp8_swiglu_gemm_backward(const uint8_t *A, int fa, int64
     SG_TRY(sg::set_delayed(layouts, scale_in, amax_out, scale_inv, p));
     SG_TRY(sg::set_bf16(d_gate_up_bf16, ld_d, F, 2, p.out, p.ld_out, p.out32));
     if (!layouts && !p.out && M > 0) return FP8_ERR_INVALID_ARG;
-    if (M > 0 && p.out && p.out == p.gate_up) return FP8_ERR_INVALID_ARG;  // read while it is written
+    if (M > 0 && starts_at_any(p.out, {A, B, sa, sb, p.gate_up, p.cq, p.cs, p.scale_in})) return FP8_ERR_INVALID_ARG;
     if (M == 0) return FP8_OK;
     return sg::launch_backward<false>({A, B, fa, fb, lda, ldb, F}, p, stream);
 }
@@ -1150,7 +1150,7 @@ extern "C" fp8_status_t fp8_mx_swiglu_gemm_backward(const uint8_t *A, int fa, in
     SG_TRY(sg::set_8bit<true>(fmt, layouts, q_row, s_row, q_colT, ld_colT, s_col, 2, p));
     SG_TRY(sg::set_bf16(d_gate_up_bf16, ld_d, F, 2, p.out, p.ld_out, p.out32));
     if (!layouts && !p.out && M > 0) return FP8_ERR_INVALID_ARG;
-    if (M > 0 && p.out && p.out == p.gate_up) return FP8_ERR_INVALID_ARG;  // read while it is written
+    if (M > 0 && starts_at_any(p.out, {A, B, sA, sB, p.gate_up, p.cq, p.cs})) return FP8_ERR_INVALID_ARG;
     if (M == 0) return FP8_OK;
     return sg::launch_backward<true>(o, p, stream);
 }

@@ -639,8 +639,8 @@ FP8GB_API fp8_status_t fp8_norm_backward(const void *dy, int y_dtype, int64_t ld
  * neither the normalized rows, nor gate|up, nor the gradient of h is written in
  * 16 bits only to be read back and quantized.  These entry points are this
  * library's own too.  Results in 8 bits are rounded once, from fp32.  Outputs must
- * not overlap inputs: a sum, dx or d_gate_up_bf16 that starts where an input of
- * the call does is FP8_ERR_INVALID_ARG.
+ * not overlap inputs: a sum, dx or d_gate_up_bf16 that starts where any input of
+ * the call does is FP8_ERR_INVALID_ARG, other overlaps are the caller's to avoid.
  * ------------------------------------------------------------------------ */
 
 /*
