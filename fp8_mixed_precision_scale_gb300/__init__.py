@@ -1084,10 +1084,15 @@ def _mx_scale_buffer(rows, blocks, dev):
     return torch.empty(n or 16, dtype=torch.uint8, device=dev)
 
 
-def _scaled_outputs(rows, cols, dev, layouts, per_row) -> Quantized:
+def _stored_inverse(rows, dev, scale_in):
+    """Where the call leaves 1 / scale_in; with no rows it writes nothing, and the value is put here."""
+    return torch.empty(1, dtype=torch.float32, device=dev) if rows else scale_in.reciprocal()
+
+
+def _scaled_outputs(rows, cols, dev, layouts, scale_in, per_row) -> Quantized:
     ld_colT = max(16, (rows + 15) // 16 * 16)
     q = Quantized(None, None, None, None, ld_colT)
-    scale = torch.empty(rows if per_row else 1, dtype=torch.float32, device=dev)
+    scale = torch.empty(rows, dtype=torch.float32, device=dev) if per_row else _stored_inverse(rows, dev, scale_in)
     if layouts & LAYOUT_ROW:
         q.q_row, q.scale_inv_row = _u8(rows, cols, dev), scale
     if layouts & LAYOUT_COLT:
@@ -1150,12 +1155,10 @@ def norm_quantize(x: torch.Tensor, residual=None, weight=None, bias=None, kind: 
             return norm_quantize(x, residual, weight, bias, kind, eps, fmt, recipe, layouts, scale_in, amax_out, out)
     where = "norm_quantize"
     recipe = recipe or Recipe(kind=ROWWISE)
-    for t, name in ((scale_in, "scale_in"), (amax_out, "amax_out")):
-        if t is not None:
-            _vector(t, where, name, 1, torch.float32)
+    _delayed_scales(fmt if recipe.kind == DELAYED else None, scale_in, amax_out, where)
     front, params, total, mean, rstd = _norm_inputs(x, residual, weight, bias, kind, out, where)
     rows, cols = x.shape
-    q = _scaled_outputs(rows, cols, x.device, layouts, recipe.kind == ROWWISE)
+    q = _scaled_outputs(rows, cols, x.device, layouts, scale_in, recipe.kind != DELAYED)
     _check(load_library().fp8_norm_quantize(*front, kind, eps, *params, fmt, ctypes.byref(recipe.c()), layouts,
                                             _ptr(scale_in), _ptr(amax_out), _ptr(q.q_row), _ptr(q.scale_inv_row),
                                             _ptr(q.q_colT), q.ld_colT, _ptr(q.scale_inv_col), _stream(None)), where)
@@ -1274,7 +1277,7 @@ def _delayed_outputs(M, row_cols, col_rows, dev, fmt, layouts, scale_in, amax_ou
     if fmt is None:
         return None, (0, 0, None, None, None, None, 0, None)
     q = Quantized(None, None, None, None, max(16, (M + 15) // 16 * 16))
-    scale = torch.empty(1, dtype=torch.float32, device=dev)
+    scale = _stored_inverse(M, dev, scale_in)
     if layouts & LAYOUT_ROW:
         q.q_row, q.scale_inv_row = _u8(M, row_cols, dev), scale
     if layouts & LAYOUT_COLT:

@@ -46,3 +46,33 @@ def test_padding_beside_rows_without_a_finite_norm(what, kind, cols, dtype, pad)
     assert np.isfinite(np.delete(y, 40, 0)).all() and not np.isfinite(y[40]).all()
     ref.check_mx(o.q, ref.scales_of(o.s, 64, cols // 32), y, tol, E4M3, "row")
     ref.check_mx(o.qt[:, :64], ref.scales_of(o.st, cols, 2), y.T, tol.T, E4M3, "col")
+
+
+def delayed():
+    return dict(scale_in=torch.tensor([2.5], device=DEV), amax_out=torch.tensor([0.125], device=DEV))
+
+
+def used_memory():
+    """Small blocks of NaN left to the allocator, so that what is not written shows."""
+    for t in [torch.full((128,), float("nan"), device=DEV) for _ in range(64)]:
+        del t
+
+
+@pytest.mark.parametrize("layouts", [1, 2, 3])
+def test_no_rows_have_the_stored_scale(layouts):
+    """The inverse scale follows from the stored one alone."""
+    x, e = torch.empty((0, 64), dtype=BF16, device=DEV), torch.empty((0, 64), dtype=torch.uint8, device=DEV)
+    w, one = torch.zeros((64, 64), dtype=torch.uint8, device=DEV), torch.ones(1, device=DEV)
+    src = torch.empty((0, 128), dtype=BF16, device=DEV)
+    calls = [lambda **k: fp8.norm_quantize(x, recipe=fp8.Recipe(kind=fp8.DELAYED), layouts=layouts, **k),
+             lambda **k: fp8.swiglu_gemm(e, E4M3, w, E4M3, one, one, fmt=E4M3, layouts=layouts, **k),
+             lambda **k: fp8.swiglu_gemm_backward(e, E4M3, w, E4M3, one, one, src, fmt=E4M3, layouts=layouts, **k)]
+    for call in calls:
+        used_memory()
+        d = delayed()
+        q = call(**d).q
+        for s, on in ((q.scale_inv_row, layouts & 1), (q.scale_inv_col, layouts & 2)):
+            assert s.item() == np.float32(1) / np.float32(2.5) if on else s is None
+        assert d["amax_out"].item() == 0.125
+        with pytest.raises(fp8.Fp8Error):
+            call(amax_out=d["amax_out"])
