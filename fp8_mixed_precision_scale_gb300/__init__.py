@@ -1204,8 +1204,9 @@ def _codes(t: torch.Tensor, where: str, name: str, K: int) -> int:
 
 
 def _scale(t: torch.Tensor, where: str, name: str, n: int) -> int:
-    _vector(t, where, name, n if t.numel() > 1 else 1, torch.float32)
-    return SCALE_PER_ROW if t.numel() > 1 else SCALE_TENSOR
+    """Check an operand's scales: one, or one for each of its n rows (none for no rows)."""
+    _vector(t, where, name, 1 if t.numel() == 1 else n, torch.float32)
+    return SCALE_TENSOR if t.numel() == 1 else SCALE_PER_ROW
 
 
 def _mx_scales(t: torch.Tensor, where: str, name: str, rows: int, K: int):

@@ -76,3 +76,19 @@ def test_no_rows_have_the_stored_scale(layouts):
         assert d["amax_out"].item() == 0.125
         with pytest.raises(fp8.Fp8Error):
             call(amax_out=d["amax_out"])
+
+
+@pytest.mark.parametrize("h,gate_up", [(True, False), (False, True)])
+def test_no_rows_of_rowwise_operands(h, gate_up):
+    """What a rowwise quantize of no rows leaves goes into the products."""
+    n = fp8.norm_quantize(torch.empty((0, 64), dtype=BF16, device=DEV), kind=fp8.RMS_NORM)
+    assert n.q.scale_inv_row.numel() == 0
+    w, sw = torch.zeros((64, 64), dtype=torch.uint8, device=DEV), torch.ones(64, device=DEV)
+    f = fp8.swiglu_gemm(n.q.q_row, E4M3, w, E4M3, n.q.scale_inv_row, sw, h=h, gate_up=gate_up)
+    assert (f.h if h else f.gate_up).shape == (0, 32 if h else 64)
+    b = fp8.swiglu_gemm_backward(n.q.q_row, E4M3, w, E4M3, n.q.scale_inv_row, sw,
+                                 torch.empty((0, 128), dtype=BF16, device=DEV), d_gate_up=True)
+    assert b.d_gate_up.shape == (0, 128)
+    # no scales are no scales of rows that there are
+    with pytest.raises(fp8.Fp8Error):
+        fp8.swiglu_gemm(w, E4M3, w, E4M3, n.q.scale_inv_row, sw, h=True)
