@@ -470,9 +470,12 @@ static fp8_status_t launch_rows(const Args &a, cudaStream_t st)
     const Plan p = make_plan(a.rows, a.cols, 2);
     const int smem = rows_shared(p.chunks, p.G, a.bias != nullptr);
     if (p.ranks > 1) return launch_rows_kernel<norm_quantize_rows<TX, TR, 2, true, ANY, true>, wide>(p, smem, a, st);
-    if (p.chunks == 1)
-        return launch_rows_kernel<norm_quantize_rows<TX, TR, 1, false, ANY, false>, narrow>(p, smem, a, st);
-    if (!p.multi) return launch_rows_kernel<norm_quantize_rows<TX, TR, 2, false, ANY, false>, narrow>(p, smem, a, st);
+    if constexpr (!(ANY && sizeof(TR) == 4)) {  // those rows are wider than one warp here
+        if (p.chunks == 1)
+            return launch_rows_kernel<norm_quantize_rows<TX, TR, 1, false, ANY, false>, narrow>(p, smem, a, st);
+        if (!p.multi)
+            return launch_rows_kernel<norm_quantize_rows<TX, TR, 2, false, ANY, false>, narrow>(p, smem, a, st);
+    }
     return launch_rows_kernel<norm_quantize_rows<TX, TR, 2, true, ANY, false>, wide>(p, smem, a, st);
 }
 
