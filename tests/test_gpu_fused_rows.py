@@ -223,3 +223,45 @@ def test_block_stage_by_stage(tokens, hidden, ffn):
     nref.assert_within(nref.f64(d.dx), want, t + nref.U * np.abs(want) + 2.0 ** -8 * (np.abs(want) + t)
                        + nref.TINY[BF16], "dx")
     nref.assert_within(nref.f64(d.dweight), dw, nref.tol_dw(dw, dy64, xh, tx, F32), "dweight")
+
+
+@pytest.mark.parametrize("mx", [True, False])
+@pytest.mark.parametrize("layouts,h,kept", [(0, True, None), (1, False, None), (2, False, "8bit"), (0, False, "bf16"),
+                                            (0, False, "8bit")])
+def test_few_rows_each_output_alone(mx, layouts, h, kept):
+    M, F, K = 1 if mx else 2, 160, 1056
+    if mx and layouts & 2:
+        layouts = 1  # the transposed layout has 32 rows at least
+    x, w = Operand(M, K, E4M3, mx, 1, 1.0), Operand(2 * F, K, E4M3, mx, 2, 0.03, groups=True)
+    both = Out(M, F, mx, 1, kept=kept, layouts=1 if mx else 3)
+    o = Out(M, F, mx, 1, h=h, kept=kept, layouts=layouts)
+    forward(x, w, both)
+    forward(x, w, o)
+    torch.cuda.synchronize()
+    for a, b, on in ((o.q, both.q, layouts & 1), (o.qt, both.qt, layouts & 2), (o.h, both.h, h)):
+        if a is not None:
+            assert torch.equal(a, b) if on else (a == 0xA5).all()
+    if mx:
+        assert torch.equal(o.s, both.s) if layouts & 1 else (o.s == 0xA5).all()
+    elif layouts:
+        assert torch.equal(o.amax, both.amax) and torch.equal(o.inv, both.inv)
+    else:
+        assert o.amax.item() == both.amax.new_tensor(1e-3).item() and o.inv.item() == -1
+    if kept == "8bit":
+        assert torch.equal(o.ck.q, both.ck.q) and torch.equal(o.ck.s, both.ck.s)
+    if kept == "bf16":
+        assert torch.equal(o.gu, both.gu)
+
+
+@pytest.mark.parametrize("rows,cols,pad", [(37, 1111, 3), (64, 512, 0), (9, 9000, 0)])
+def test_norm_backward_with_dsum_and_no_parameter_gradients(rows, cols, pad):
+    """dx is that of the call with all gradients, bit for bit, in rows of another stride too."""
+    x, dy, dsum = (values(rows, cols, BF16, s, 1.0, 0.0, pad) for s in (20, 21, 22))
+    w, _ = params(cols, F32, 23)
+    f = fp8.norm_forward(x, w)
+    full = fp8.norm_backward(dy, x, f.mean, f.rstd, w, dsum=dsum)
+    out = torch.full((rows, cols + 8), 7.0, dtype=BF16, device=DEV)
+    r = fp8.norm_backward(dy, x, f.mean, f.rstd, w, weight_grad=False, bias_grad=False, out=out[:, :cols], dsum=dsum)
+    torch.cuda.synchronize()
+    assert r.dweight is None and r.dbias is None and full.dbias is not None
+    assert torch.equal(out[:, :cols], full.dx) and (out[:, cols:] == 7).all()
