@@ -9,7 +9,9 @@
 // width of an MX block, and each of its eight warps four of them: eight rows of W at a
 // time, a row's next step asked for when this one's has been taken.  A in fp32 with its
 // block scales (exact), in shared memory; each W code is exact in fp16 and fp32; fp32
-// sums, a W block's scale applied to the sum of 16 products.
+// sums, a W block's scale applied to the sum of 16 products.  A's scales go in as far as
+// 2^-60 to 2^60 (16 products of E5M2 are below 2^36), the rest of one beyond that after
+// W's: nothing leaves fp32 on the way that the result would not.
 //
 // MX, one row, in a graph: F = 14336, K = 4096 33.7 us = 3.6 TB/s; F = 2048, K = 7168
 // 24.0 us; F = 1504, K = 4096 13.6 us.  Bound by the conversions of the codes as much as
@@ -35,6 +37,8 @@ constexpr int FR_ROWS = 2 * FR_EACH;            // rows of W a warp reads at onc
 constexpr int FR_STEP = 512;                    // of K
 constexpr int FR_MOST = 2;                      // rows of A at most: their values stay in registers
 constexpr int FR_SMEM = 96 * 1024;              // of A at most: two blocks an SM
+constexpr int FR_BLOCKS = FR_SMEM / (int)sizeof(float) / FP8_MX_BLOCK;  // scales of A at most (MX: one row)
+constexpr uint32_t FR_LOW = 127 - 60, FR_HIGH = 127 + 60;
 
 struct RowArgs {
     const uint8_t *A, *B, *sA, *sB;
@@ -67,6 +71,7 @@ __global__ void __launch_bounds__(FR_THREADS, 2) swiglu_rows_kernel(RowArgs o, P
     extern __shared__ __align__(16) float4 xs[];
     __shared__ float sums[2][MT][FR_COLS];
     __shared__ uint8_t code[FR_MOST];
+    __shared__ float rest[MX ? FR_BLOCKS : 1];  // of A's scales
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c0 = (int64_t)blockIdx.x * FR_COLS;
     const int M = (int)p.M, K = (int)p.K, steps = (K + FR_STEP - 1) / FR_STEP;
@@ -97,15 +102,19 @@ __global__ void __launch_bounds__(FR_THREADS, 2) swiglu_rows_kernel(RowArgs o, P
     for (int i = 0; i < FR_ROWS; i++) fetch(i, 0);
     for (int i = threadIdx.x; i < MT * steps * 32; i += FR_THREADS) {
         const int m = i / (steps * 32), at = i - m * steps * 32, l = at & 31, k = (at >> 5) * FR_STEP + l * 16;
-        float f[16] = {};
+        float f[16] = {}, past = 1.0f;
         if (m < M && k < K) {
             decode(*reinterpret_cast<const uint4 *>(o.A + m * o.lda + k), o.fa, f);
             if (MX) {
-                const float x = ckpt_scale(o.sA[4 * mx_scale_word(k >> 7, m, o.rsA) + (k >> 5 & 3)]);
+                const uint32_t e = o.sA[4 * mx_scale_word(k >> 7, m, o.rsA) + (k >> 5 & 3)];
+                const uint32_t in = e == 255u ? e : min(max(e, FR_LOW), FR_HIGH);
+                const float x = ckpt_scale(in);
+                past = ckpt_scale(127u + e - in);
 #pragma unroll
                 for (int j = 0; j < 16; j++) f[j] *= x;
             }
         }
+        if (MX && !(at & 1)) rest[at >> 1] = past;  // a block's first thread
 #pragma unroll
         for (int j = 0; j < 4; j++)
             xs[((m * steps + (at >> 5)) * 4 + j) * 32 + l] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
@@ -119,6 +128,7 @@ __global__ void __launch_bounds__(FR_THREADS, 2) swiglu_rows_kernel(RowArgs o, P
         for (int m = 0; m < MT; m++)
 #pragma unroll
             for (int j = 0; j < 4; j++) x[m][j] = xs[((m * steps + step) * 4 + j) * 32 + lane];
+        const float past = MX ? rest[step * 16 + (lane >> 1)] : 1.0f;
 #pragma unroll
         for (int i = 0; i < FR_ROWS; i++) {
             float f[16];
@@ -134,7 +144,7 @@ __global__ void __launch_bounds__(FR_THREADS, 2) swiglu_rows_kernel(RowArgs o, P
                     u = fma2(make_float2(f[4 * j + 2], f[4 * j + 3]), make_float2(x[m][j].z, x[m][j].w), u);
                 }
                 t = add2(t, u);
-                acc[i][m] = MX ? fmaf(t.x + t.y, scale, acc[i][m]) : acc[i][m] + (t.x + t.y);
+                acc[i][m] = MX ? fmaf((t.x + t.y) * scale, past, acc[i][m]) : acc[i][m] + (t.x + t.y);
             }
         }
     }

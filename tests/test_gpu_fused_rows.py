@@ -2,6 +2,8 @@
 operands and results, of the wrappers of the stored scale, and of a whole block
 stage by stage, against the float64 references (bounds derived in fused_ref and
 norm_ref)."""
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 import torch
@@ -265,3 +267,30 @@ def test_norm_backward_with_dsum_and_no_parameter_gradients(rows, cols, pad):
     torch.cuda.synchronize()
     assert r.dweight is None and r.dbias is None and full.dbias is not None
     assert torch.equal(out[:, :cols], full.dx) and (out[:, cols:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [1, 3])
+@pytest.mark.parametrize("fmt", [E4M3, E5M2])
+def test_scales_far_apart(fmt, M):
+    """A's and W's scale bytes over their whole range, each block's product of scales 1: a
+    few-row kernel that scales A first must not leave fp32 on the way."""
+    F, K = 160, 1056
+    rng = np.random.RandomState(6)
+    byte = rng.randint(0, 255, K // 32)
+    byte[:3] = 254, 0, 250
+    ops = []
+    for rows, b in ((M, byte), (2 * F, 254 - byte)):
+        q, _ = ref.mx_quantize(rng.randn(rows, K), fmt)
+        q[:, 64:96] = 0  # zeros of W under A's byte 250
+        s = np.broadcast_to(b, (rows, K // 32)).astype(np.uint8)
+        v = nref.decode_table(fmt)[q.numpy()] * np.repeat(np.exp2(s.astype(np.float64) - 127), 32, 1)
+        if rows == 2 * F:
+            h = np.zeros((2, ref.up(F, 128), K // 32), np.uint8)
+            h[:, :F] = s.reshape(2, F, -1)
+            s = h.reshape(-1, K // 32)
+        ops.append(SimpleNamespace(q=q.to(DEV), s=ref.layout_of(s).to(DEV), v=v, fmt=fmt, ld=K))
+    x, w = ops
+    o = Out(M, F, True, 1, kept="bf16", layouts=1)
+    forward(x, w, o)
+    torch.cuda.synchronize()
+    check_forward(x, w, o, f"{M} rows")
