@@ -205,7 +205,14 @@ __device__ __forceinline__ void cp_async_wait()
 //
 // RES adds dsum, the gradient of x that does not come through the norm.  The ring has
 // no room for it and the registers none while the sums are made: its lines are
-// fetched into L2 with the rows ahead and read once the sums are there.
+// fetched into L2 with the rows ahead and read once the sums are there.  Two rows of it
+// beside two rows of gradients spill in the aligned forms of 16-bit dy (bf16 132 bytes
+// stored and 144 loaded a thread, from the checkpoint 100 and 116, rows of one warp 140
+// and 136, in a cluster up to 168 and 148; fp16 alike; fp32 sums from the checkpoint up
+// to 336 and 240); so do unaligned fp32 sums (up to 284 and 180), aligned ones from x
+// do not.  [8192, 4096] bf16 60 us from x, 58 from the checkpoint, against 40 and 38
+// without dsum, 69 and 67 with a separate addition; [32768, 7168] 374 and 368 (222 and
+// 215; 417 and 410).
 template <typename TX, typename TY, bool MULTI, bool CKPT, bool ANY, bool CLUSTER, bool RES = false>
 __global__ void __launch_bounds__(NM_BLOCK) norm_backward_kernel(NormArgs a)
 {

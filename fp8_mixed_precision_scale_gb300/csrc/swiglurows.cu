@@ -13,8 +13,8 @@
 // 2^-60 to 2^60 (16 products of E5M2 are below 2^36), the rest of one beyond that after
 // W's: nothing leaves fp32 on the way that the result would not.
 //
-// MX, one row, in a graph: F = 14336, K = 4096 33.7 us = 3.6 TB/s; F = 2048, K = 7168
-// 24.0 us; F = 1504, K = 4096 13.6 us.  Bound by the conversions of the codes as much as
+// MX, one row, in a graph: F = 14336, K = 4096 31.7 to 34 us = 3.6 TB/s; F = 2048, K =
+// 7168 22.8 us; F = 1504, K = 4096 13.9 us.  Bound by the conversions of the codes as much as
 // by memory: 4.2 instructions a weight in 45 % of the issue slots, of which 1.5 convert.
 // Two rows, this against the tiles (F, K): scaled 32.8 and 36.9 (14336, 4096), 24.0 and
 // 22.8 (2048, 7168), 13.8 and 16.4 (1504, 4096), 36.4 and 45.1 (8192, 8192); MX 38.5 and
